@@ -100,6 +100,19 @@ float effective_scale(const vsa_params* p);
 vsa_status check_qkv(const void* q, const void* k, const void* v, int64_t sb, int64_t ss,
                      int64_t sh, int32_t B, int32_t H);
 
+// A view of `heads` heads and rows of `width` elements: data, type and strides
+// (of dimensions of size above 1) valid, `align` bytes aligned rows. With
+// `output` no dimension of size above 1 may have stride 0.
+vsa_status check_view(const vsa_view* v, int32_t B, int64_t S, int64_t width, int align, bool output);
+inline size_t dtype_bytes(int32_t dtype) { return dtype == VSA_F32 ? 4 : 2; }
+// Strides of dimensions of size 1 replaced by 0.
+struct Strides {
+  int64_t b, s, h;
+};
+inline Strides view_strides(const vsa_view* v, int32_t B, int64_t S) {
+  return Strides{B > 1 ? v->stride_b : 0, S > 1 ? v->stride_s : 0, v->heads > 1 ? v->stride_h : 0};
+}
+
 // Workspace layout of vsa_coarse_select. Bytes [0, 256): status word and
 // count of failed calls; the pooled means [3, B, H, n_tiles, 128] fp32 follow.
 // VSA_COARSE_MEAN runs the tensor-core kernels (vsa_select_tc.cu): Kbar and

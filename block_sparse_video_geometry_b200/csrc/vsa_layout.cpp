@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <new>
@@ -73,6 +74,22 @@ vsa_status check_qkv(const void* q, const void* k, const void* v, int64_t sb, in
     if (reinterpret_cast<uintptr_t>(p) % 16) return VSA_ERR_INVALID_ARG;
   if (sb % 8 || ss % 8 || sh % 8) return VSA_ERR_INVALID_ARG;
   if (sh < kHeadDim && H > 1) return VSA_ERR_INVALID_ARG;
+  return VSA_OK;
+}
+
+vsa_status check_view(const vsa_view* v, int32_t B, int64_t S, int64_t width, int align, bool output) {
+  if (!v || v->heads <= 0 || v->dtype < VSA_F32 || v->dtype > VSA_F16) return VSA_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return VSA_OK;
+  const int64_t size = static_cast<int64_t>(dtype_bytes(v->dtype));
+  if (!v->data || reinterpret_cast<uintptr_t>(v->data) % std::max<int64_t>(align, size)) return VSA_ERR_INVALID_ARG;
+  const Strides st = view_strides(v, B, S);
+  const int64_t stride[3] = {st.b, st.s, st.h}, extent[3] = {B, S, v->heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] == 1) continue;
+    if (stride[i] < 0 || (output && stride[i] < width)) return VSA_ERR_INVALID_ARG;
+    if (stride[i] > INT64_MAX / 16 / extent[i]) return VSA_ERR_INVALID_ARG;
+    if (stride[i] * size % std::max<int64_t>(align, 1)) return VSA_ERR_INVALID_ARG;
+  }
   return VSA_OK;
 }
 

@@ -22,7 +22,10 @@ SELECT_TOPK, SELECT_ADAPTIVE = 0, 1
 SINK_EXACT_KV, SINK_EXACT_KV_AND_ROWS, SINK_OFF = 0, 1, 2
 COARSE_MEAN, COARSE_REWEIGHT = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
 TILE, HEAD_DIM = 64, 128
+MAX_NORM_WIDTH = 16384
 MAX_EXTRA_TOKENS = 64
 
 
@@ -53,9 +56,21 @@ class LayoutInfo(ctypes.Structure):
                 ("video_start", ctypes.c_int64), ("device_bytes", ctypes.c_size_t)]
 
 
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("theta", ctypes.c_double), ("scale_t", ctypes.c_double),
+                ("scale_h", ctypes.c_double), ("scale_w", ctypes.c_double)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_V = ctypes.POINTER(View)
 
 _SIGNATURES = {
     "vsa_layout_build": (_I32, [ctypes.POINTER(Segment), _I32, _I64, _P, _SZ, _P, ctypes.POINTER(_P)]),
@@ -91,6 +106,12 @@ _SIGNATURES = {
     "vsa_sparse_attn_workspace_init": (_I32, [_P, _P]),
     "vsa_sparse_attn_failed_calls": (_I32, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "vsa_debug_inject_wait_timeout": (_I32, [ctypes.c_uint64]),
+    "vsa_rope_positions": (_I32, [_P, _I32, _I32, _I32, _P, _P]),
+    "vsa_rope_fwd": (_I32, [ctypes.POINTER(Rope), _I32, _I64, _P, _I64, _V, _V, _V, _V, _P]),
+    "vsa_rope_bwd": (_I32, [ctypes.POINTER(Rope), _I32, _I64, _P, _I64, _V, _V, _V, _V, _P]),
+    "vsa_layer_norm_fwd": (_I32, [_I32, _I64, _I32, _V, _P, _P, _I32, ctypes.c_float, _V, _P, _P, _P]),
+    "vsa_layer_norm_bwd_workspace_size": (_I32, [_I32, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
+    "vsa_layer_norm_bwd": (_I32, [_I32, _I64, _I32, _V, _V, _P, _I32, _P, _P, _V, _P, _P, _P, _SZ, _P]),
     "vsa_status_string": (ctypes.c_char_p, [_I32]),
     "vsa_version": (_I32, []),
     "vsa_last_error_detail": (ctypes.c_char_p, []),
@@ -359,6 +380,170 @@ def sparse_attn_failed_calls(workspace, stream=None) -> int:
     _check(lib().vsa_sparse_attn_failed_calls(workspace.data_ptr(), _stream_handle(stream), ctypes.byref(n)),
            "vsa_sparse_attn_failed_calls")
     return n.value
+
+
+# ---------------------------------------------------------------- operators around the sparse call
+_DTYPES = {}
+
+
+def _dtype(t) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("tensors must be float32, bfloat16 or float16, got %s" % t.dtype)
+    return code
+
+
+def _view(t):
+    """The vsa_view of a [..., width] tensor of 2 ([S, width]), 3 ([B, S, width]) or 4 dimensions, as a
+    reference that ctypes passes by address."""
+    shape, st = t.shape, t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    if len(shape) == 4:
+        v = View(t.data_ptr(), st[0], st[1], st[2], shape[2], _dtype(t))
+    elif len(shape) == 3:
+        v = View(t.data_ptr(), st[0], st[1], 0, 1, _dtype(t))
+    elif len(shape) == 2:
+        v = View(t.data_ptr(), 0, st[0], 0, 1, _dtype(t))
+    else:
+        raise ValueError("tensors must have 2, 3 or 4 dimensions")
+    return ctypes.byref(v)
+
+
+class _On:
+    """Makes the tensors' device current for a call; they must share one CUDA device."""
+
+    def __init__(self, first, *others):
+        self.device = first.device
+        if self.device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device, got %s" % self.device)
+        for t in others:
+            if t is not None and t.device != self.device:
+                raise ValueError("tensors must be on one device, got %s and %s" % (self.device, t.device))
+        self.guard = None
+
+    def __enter__(self):
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def make_rope(dims=(44, 42, 42), theta: float = 10000.0, scale=(1.0, 1.0, 1.0),
+              pairing: int = ROPE_ADJACENT) -> Rope:
+    """Rotary positions with `dims` (time, height, width) channels of the head's 128; see vsa_rope in vsa.h."""
+    if len(dims) != 3 or len(scale) != 3:
+        raise ValueError("dims and scale hold one value per axis: time, height, width")
+    return Rope(*dims, pairing, theta, *scale)
+
+
+def rope_positions(layout: Layout, pos, origin=(0, 0, 0), stream=None) -> None:
+    """vsa_rope_positions: fills pos, int32 [seq_len, 3], with the positions of the layout's tokens."""
+    import torch
+    if pos.dtype != torch.int32 or tuple(pos.shape) != (layout.info.seq_len, 3) or not pos.is_contiguous():
+        raise ValueError("pos must be a contiguous int32 [seq_len, 3] tensor")
+    with _On(pos):
+        _check(lib().vsa_rope_positions(layout.handle, *origin, pos.data_ptr(), _stream_handle(stream)),
+               "vsa_rope_positions")
+
+
+def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
+    import torch
+    if q.dim() != 4 or q.shape[-1] != HEAD_DIM or q_out.shape != q.shape:
+        raise ValueError("q and its output must be [B, S, H, 128]")
+    B, S = q.shape[0], q.shape[1]
+    if (k is None) != (k_out is None):
+        raise ValueError("k and its output come together")
+    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[-1] != HEAD_DIM
+                          or k_out.shape != k.shape):
+        raise ValueError("k and its output must be [B, S, H, 128] with q's B and S")
+    if pos.dtype != torch.int32 or tuple(pos.shape) not in ((S, 3), (B, S, 3)) \
+            or (S > 1 and pos.stride()[-2:] != (3, 1)):
+        raise ValueError("pos must be int32 [S, 3] or [B, S, 3], contiguous in its last two dimensions")
+    with _On(q, pos, k, q_out, k_out):
+        _check(getattr(lib(), name)(ctypes.byref(rope), B, S, pos.data_ptr(), pos.stride(0) if pos.dim() == 3 else 0,
+                                    _view(q), None if k is None else _view(k), _view(q_out),
+                                    None if k is None else _view(k_out), _stream_handle(stream)), name)
+
+
+def rope_fwd(rope: Rope, pos, q, k, q_out, k_out, stream=None) -> None:
+    """vsa_rope_fwd on torch tensors: q [B, S, Hq, 128] and k [B, S, Hk, 128] (or None, with k_out None) rotated
+    by their positions, int32 [S, 3] or [B, S, 3], into q_out and k_out (which may be q and k)."""
+    _rope_call("vsa_rope_fwd", rope, pos, q, k, q_out, k_out, stream)
+
+
+def rope_bwd(rope: Rope, pos, dq_out, dk_out, dq, dk, stream=None) -> None:
+    """vsa_rope_bwd on torch tensors: dq and dk from the gradients of rope_fwd's outputs."""
+    _rope_call("vsa_rope_bwd", rope, pos, dq_out, dk_out, dq, dk, stream)
+
+
+def _norm_shape(x):
+    """(B, S, heads, width) of x [S, width], [B, S, width] or [B, S, heads, width]."""
+    s = tuple(x.shape)
+    if not 2 <= len(s) <= 4:
+        raise ValueError("x must be [S, width], [B, S, width] or [B, S, heads, width]")
+    return (1, s[0], 1, s[1]) if len(s) == 2 else (s[0], s[1], 1, s[2]) if len(s) == 3 else s
+
+
+def _vector(t, n, what, dtypes):
+    """Address of a contiguous [n] tensor of one of the types, or None."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous() or t.dtype not in dtypes:
+        raise ValueError("%s must be contiguous with %d elements of %s" % (what, n, " or ".join(map(str, dtypes))))
+    return t.data_ptr()
+
+
+def layer_norm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=None) -> None:
+    """vsa_layer_norm_fwd on torch tensors: y = layer norm of x over its last dimension; weight and bias [width]
+    in x's type or float32 (both of one type), or None; mean and rstd float32 of x's leading shape, or None."""
+    import torch
+    B, S, H, N = _norm_shape(x)
+    if y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("y must have x's shape and type")
+    wt = weight if weight is not None else bias
+    types = (x.dtype, torch.float32)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one type")
+    with _On(x, weight, bias, y, mean, rstd):
+        _check(lib().vsa_layer_norm_fwd(B, S, N, _view(x), _vector(weight, N, "weight", types),
+                                        _vector(bias, N, "bias", types), 0 if wt is None else _dtype(wt), eps, _view(y),
+                                        _vector(mean, B * S * H, "mean", (torch.float32,)),
+                                        _vector(rstd, B * S * H, "rstd", (torch.float32,)), _stream_handle(stream)),
+               "vsa_layer_norm_fwd")
+
+
+def layer_norm_bwd_workspace_size(x) -> int:
+    """Workspace bytes of layer_norm_bwd for an x of this shape."""
+    B, S, H, N = _norm_shape(x)
+    n = _SZ()
+    _check(lib().vsa_layer_norm_bwd_workspace_size(B, S, H, N, ctypes.byref(n)), "vsa_layer_norm_bwd_workspace_size")
+    return n.value
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None) -> None:
+    """vsa_layer_norm_bwd on torch tensors: dx (x's type or float32) from dy (x's type or float32), x, weight and
+    the forward's mean and rstd; dweight and dbias float32 [width] out, or None."""
+    import torch
+    B, S, H, N = _norm_shape(x)
+    if dy.shape != x.shape or dx.shape != x.shape:
+        raise ValueError("dy and dx must have x's shape")
+    f32 = (torch.float32,)
+    with _On(x, dy, weight, mean, rstd, dx, dweight, dbias, workspace):
+        _check(lib().vsa_layer_norm_bwd(B, S, N, _view(dy), _view(x),
+                                        _vector(weight, N, "weight", (x.dtype, torch.float32)),
+                                        0 if weight is None else _dtype(weight), _vector(mean, B * S * H, "mean", f32),
+                                        _vector(rstd, B * S * H, "rstd", f32), _view(dx),
+                                        _vector(dweight, N, "dweight", f32), _vector(dbias, N, "dbias", f32),
+                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                        _stream_handle(stream)), "vsa_layer_norm_bwd")
 
 
 def debug_inject_wait_timeout(timeout_ns):

@@ -478,6 +478,107 @@ vsa_status vsa_debug_inject_wait_timeout(uint64_t timeout_ns);
  * timeout_ns = 0 disarms it. Always returns VSA_OK. */
 vsa_status vsa_debug_inject_select_wait_timeout(uint64_t timeout_ns);
 
+/* ------------------------------------------------------------------------ */
+/* Operators around the sparse call                                          */
+/* ------------------------------------------------------------------------ */
+
+/* Element types of the operators below. */
+typedef enum { VSA_F32 = 0, VSA_BF16 = 1, VSA_F16 = 2 } vsa_dtype;
+
+/* A [B, S, heads, width] tensor at element strides, the last dimension
+ * contiguous. The stride of a dimension of size 1 is not read. Inputs may be
+ * broadcast (stride 0); an output's strides must be non-zero where its size is
+ * above 1. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_s, stride_h;
+  int32_t heads;
+  int32_t dtype;      /* vsa_dtype */
+} vsa_view;
+
+/* Rotary positions with three axes. The head's 128 channels are cut into a
+ * time block of dim_t channels, then dim_h of height, then dim_w of width
+ * (each even, their sum at most 128; channels behind them pass through
+ * unchanged). Pair i of an axis' block turns by
+ *     angle = pos[axis] * scale[axis] * theta^(-2 i / dim[axis])
+ * (a, b) -> (a cos - b sin, a sin + b cos), where the pair is channels
+ * (2i, 2i + 1) of the block (VSA_ROPE_ADJACENT) or (i, i + dim / 2)
+ * (VSA_ROPE_HALVES). */
+typedef enum { VSA_ROPE_ADJACENT = 0, VSA_ROPE_HALVES = 1 } vsa_rope_pairing;
+typedef struct {
+  int32_t dim_t, dim_h, dim_w;
+  int32_t pairing;
+  double theta;                       /* > 0, finite */
+  double scale_t, scale_h, scale_w;   /* finite */
+} vsa_rope;
+
+/* vsa_rope_positions: the positions of a layout's tokens, pos int32
+ * [seq_len, 3] (time, height, width) out. Video token (t, h, w) stands at
+ * (t0 + t, h0 + h, w0 + w); conditioning token n (counted over the
+ * conditioning tokens in sequence order) at (n, n, n). Needs no uploaded
+ * tables. Positions wrap as 32-bit integers. */
+vsa_status vsa_rope_positions(const vsa_layout* layout, int32_t t0, int32_t h0, int32_t w0,
+                              int32_t* pos, cudaStream_t stream);
+
+/* vsa_rope_fwd: q_out = rotated q, k_out = rotated k (k and k_out both NULL:
+ * q alone). pos is int32 [S, 3] with pos_stride_b = 0 (shared by the batch),
+ * or [B, S, 3] at an element stride of pos_stride_b >= 3 S; any value,
+ * negative ones among them.
+ * Data and strides are 16-byte multiples. Each input and output has its own
+ * type; an output may be its input's own buffer (same data, strides and type),
+ * any other overlap is the caller's error. q and k have their own head counts.
+ * The angle is reduced to a turn in 64 bits, its sine and cosine and the
+ * rotation are 32-bit, and the result is rounded once. B, S >= 0 (0: nothing
+ * to do); at most 2^31 - 1 tokens and 65535 heads (UNSUPPORTED beyond). */
+vsa_status vsa_rope_fwd(const vsa_rope* rope, int32_t B, int64_t S, const int32_t* pos, int64_t pos_stride_b,
+                        const vsa_view* q, const vsa_view* k, const vsa_view* q_out, const vsa_view* k_out,
+                        cudaStream_t stream);
+
+/* vsa_rope_bwd: the gradient of vsa_rope_fwd, the rotation by the negative
+ * angle: dq = gradient of q from dq_out (same rules as vsa_rope_fwd; the fp32
+ * dq and dk of vsa_sparse_attn_bwd are taken as they are). */
+vsa_status vsa_rope_bwd(const vsa_rope* rope, int32_t B, int64_t S, const int32_t* pos, int64_t pos_stride_b,
+                        const vsa_view* dq_out, const vsa_view* dk_out, const vsa_view* dq, const vsa_view* dk,
+                        cudaStream_t stream);
+
+#define VSA_MAX_NORM_WIDTH 16384
+
+/* vsa_layer_norm_fwd: y = (x - mean) * rstd * weight + bias over the last
+ * dimension of [B, S, heads, width]; mean and the biased variance are those of
+ * the row, rstd = 1 / sqrt(variance + eps).
+ *  x, y         : same heads and type; y may be x's own buffer. Element
+ *                 alignment suffices (16-byte multiples are faster).
+ *  weight, bias : [width] of weight_dtype (x's type or VSA_F32), each may be
+ *                 NULL (1 and 0).
+ *  mean, rstd   : float [B, S, heads] out, both or neither NULL; the backward
+ *                 pass reads them.
+ * Sums and statistics are 32-bit, the variance about the mean; the result is
+ * rounded once. B, S >= 0; 1 <= width <= VSA_MAX_NORM_WIDTH and fewer than
+ * 2^31 rows (UNSUPPORTED beyond); eps >= 0. */
+vsa_status vsa_layer_norm_fwd(int32_t B, int64_t S, int32_t width, const vsa_view* x, const void* weight,
+                              const void* bias, int32_t weight_dtype, float eps, const vsa_view* y, float* mean,
+                              float* rstd, cudaStream_t stream);
+
+vsa_status vsa_layer_norm_bwd_workspace_size(int32_t B, int64_t S, int32_t heads, int32_t width, size_t* bytes);
+
+/* vsa_layer_norm_bwd: the gradients of vsa_layer_norm_fwd, xh = (x - mean) *
+ * rstd, g = dy * weight:
+ *   dx      = rstd * (g - mean(g) - xh * mean(g * xh))
+ *   dweight = sum over rows of dy * xh,   dbias = sum over rows of dy
+ *  dy, dx          : of x's type or VSA_F32, each its own (the fp32 gradients
+ *                    of vsa_rope_bwd or vsa_sparse_attn_bwd are taken as they
+ *                    are); dx may be dy's own buffer.
+ *  dweight, dbias  : float [width] out, each may be NULL.
+ *  workspace       : vsa_layer_norm_bwd_workspace_size bytes, 256-byte aligned;
+ *                    partial sums, written before they are read. Two calls that
+ *                    may overlap need two workspaces.
+ * The sums over rows are 32-bit in a fixed order: equal inputs give equal bits
+ * on the same GPU. */
+vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_view* dy, const vsa_view* x,
+                              const void* weight, int32_t weight_dtype, const float* mean, const float* rstd,
+                              const vsa_view* dx, float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
 const char* vsa_status_string(vsa_status status);
 
 /* Text of the most recent VSA_ERR_CUDA returned on the calling thread (the

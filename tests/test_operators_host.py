@@ -1,0 +1,117 @@
+"""Refusals of the operators around the sparse call, without a GPU: malformed
+arguments return a status before any GPU work (the pointers here are never
+followed)."""
+
+import ctypes
+
+import pytest
+
+from block_sparse_video_geometry_b200 import vsa
+
+FAKE = 1 << 20          # aligned, never dereferenced
+
+
+def view(heads=2, dtype=vsa.DTYPE_BF16, data=FAKE, sb=1 << 14, ss=256, sh=128):
+    return vsa.View(data, sb, ss, sh, heads, dtype)
+
+
+def rope_call(rope=None, B=2, S=8, pos=FAKE, pos_sb=24, q=None, k=None, qo=None, ko=None, name="vsa_rope_fwd"):
+    ref = lambda v: None if v is None else ctypes.byref(v)  # noqa: E731
+    rope = vsa.make_rope() if rope is None else rope
+    return getattr(vsa.lib(), name)(ctypes.byref(rope), B, S, pos, pos_sb, ref(q or view()), ref(k), ref(qo or view()),
+                                    ref(ko), None)
+
+
+@pytest.mark.parametrize("rope", [
+    vsa.make_rope((43, 42, 42)), vsa.make_rope((-2, 64, 64)), vsa.make_rope((64, 64, 2)), vsa.make_rope(theta=0.0),
+    vsa.make_rope(theta=-1.0), vsa.make_rope(theta=float("inf")), vsa.make_rope(theta=float("nan")),
+    vsa.make_rope(scale=(1.0, float("nan"), 1.0)), vsa.make_rope(pairing=2),
+    vsa.make_rope((126, 0, 0), theta=1e-320, scale=(1e300, 1.0, 1.0)),
+])
+def test_rope_refuses_malformed_parameters(rope):
+    assert rope_call(rope) == vsa.ERR_INVALID_ARG
+    assert rope_call(rope, name="vsa_rope_bwd") == vsa.ERR_INVALID_ARG
+
+
+def test_rope_refuses_malformed_arguments():
+    bad = vsa.ERR_INVALID_ARG
+    assert rope_call(B=-1) == bad and rope_call(S=-1) == bad and rope_call(pos=None) == bad
+    assert rope_call(pos_sb=23) == bad and rope_call(pos_sb=-24) == bad and rope_call(pos=FAKE + 2) == bad
+    assert rope_call(k=view()) == bad and rope_call(ko=view()) == bad            # k without its output and back
+    assert rope_call(q=view(heads=3)) == bad and rope_call(q=view(heads=0)) == bad
+    for v in (view(dtype=3), view(dtype=-1), view(data=None), view(data=FAKE + 8), view(ss=-256), view(ss=252)):
+        assert rope_call(q=v) == bad and rope_call(qo=v) == bad
+    for v in (view(sb=0), view(ss=0), view(sh=64)):                               # overlapping output rows
+        assert rope_call(qo=v) == bad
+    assert rope_call(S=1 << 31, pos_sb=0) == vsa.ERR_UNSUPPORTED
+    assert rope_call(q=view(heads=70000), qo=view(heads=70000)) == vsa.ERR_UNSUPPORTED
+    assert rope_call(S=0) == vsa.OK and rope_call(B=0, pos=None) == vsa.OK         # nothing to do
+    L = vsa.lib()
+    lay = vsa.Layout([(vsa.SEG_VIDEO, 0, 8, (2, 2, 2))], 8)
+    assert L.vsa_rope_positions(None, 0, 0, 0, FAKE, None) == bad
+    assert L.vsa_rope_positions(lay.handle, 0, 0, 0, None, None) == bad
+
+
+def norm_fwd(B=2, S=8, width=64, x=None, w=FAKE, b=FAKE, wt=vsa.DTYPE_F32, eps=1e-6, y=None, mean=FAKE, rstd=FAKE):
+    x, y = x or view(), y or view()
+    return vsa.lib().vsa_layer_norm_fwd(B, S, width, ctypes.byref(x), w, b, wt, eps, ctypes.byref(y), mean, rstd, None)
+
+
+def norm_bwd(B=2, S=8, width=64, dy=None, x=None, w=FAKE, wt=vsa.DTYPE_F32, mean=FAKE, rstd=FAKE, dx=None, dw=FAKE,
+             db=FAKE, ws=FAKE, nbytes=1 << 30):
+    dy, x, dx = dy or view(), x or view(), dx or view()
+    return vsa.lib().vsa_layer_norm_bwd(B, S, width, ctypes.byref(dy), ctypes.byref(x), w, wt, mean, rstd,
+                                        ctypes.byref(dx), dw, db, ws, nbytes, None)
+
+
+def test_layer_norm_refuses_malformed_arguments():
+    bad = vsa.ERR_INVALID_ARG
+    for call in (norm_fwd, norm_bwd):
+        assert call(B=-1) == bad and call(S=-1) == bad and call(width=0) == bad and call(width=-4) == bad
+        assert call(width=vsa.MAX_NORM_WIDTH + 1) == vsa.ERR_UNSUPPORTED
+        assert call(S=1 << 31) == vsa.ERR_UNSUPPORTED and call(S=1 << 29) == vsa.ERR_UNSUPPORTED
+        assert call(wt=vsa.DTYPE_F16) == bad and call(wt=7) == bad and call(w=FAKE + 2) == bad
+        for v in (view(heads=0), view(heads=3), view(dtype=5), view(data=None), view(data=FAKE + 1), view(sb=-1)):
+            assert call(x=v) == bad
+    for v in (view(dtype=vsa.DTYPE_F32), view(heads=1), view(ss=0), view(sh=63)):
+        assert norm_fwd(y=v) == bad
+    assert norm_fwd(eps=-1e-6) == bad and norm_fwd(eps=float("nan")) == bad and norm_fwd(eps=float("inf")) == bad
+    assert norm_fwd(mean=None) == bad and norm_fwd(rstd=None) == bad and norm_fwd(rstd=FAKE + 1) == bad
+    for v in (view(dtype=vsa.DTYPE_F16), view(heads=1)):
+        assert norm_bwd(dy=v) == bad and norm_bwd(dx=v) == bad
+    assert norm_bwd(mean=None) == bad and norm_bwd(rstd=None) == bad and norm_bwd(dw=FAKE + 2) == bad
+    assert norm_bwd(ws=None) == bad and norm_bwd(ws=FAKE + 128) == bad
+    n = ctypes.c_size_t()
+    assert vsa.lib().vsa_layer_norm_bwd_workspace_size(2, 8, 2, 64, ctypes.byref(n)) == vsa.OK and n.value >= 512
+    assert norm_bwd(nbytes=n.value - 1) == vsa.ERR_WORKSPACE_TOO_SMALL
+    assert vsa.lib().vsa_layer_norm_bwd_workspace_size(2, 8, 0, 64, ctypes.byref(n)) == bad
+    assert vsa.lib().vsa_layer_norm_bwd_workspace_size(2, 8, 2, 64, None) == bad
+    assert norm_fwd(S=0) == vsa.OK
+
+
+def test_binding_refuses_what_it_cannot_pass_on():
+    import torch
+    cpu = torch.zeros((1, 4, 2, 128))
+    pos = torch.zeros((4, 3), dtype=torch.int32)
+    rope = vsa.make_rope()
+    with pytest.raises(ValueError, match="CUDA device"):
+        vsa.rope_fwd(rope, pos, cpu, None, cpu.clone(), None)
+    with pytest.raises(ValueError, match="128"):
+        vsa.rope_fwd(rope, pos, cpu[..., :64], None, cpu[..., :64], None)
+    with pytest.raises(ValueError, match="pos"):
+        vsa.rope_fwd(rope, pos.long(), cpu, None, cpu, None)
+    with pytest.raises(ValueError, match="pos"):
+        vsa.rope_fwd(rope, pos[:3], cpu, None, cpu, None)
+    with pytest.raises(ValueError, match="together"):
+        vsa.rope_fwd(rope, pos, cpu, cpu, cpu, None)
+    with pytest.raises(ValueError, match="dims"):
+        vsa.make_rope((64, 64))
+    x = torch.zeros((4, 128))
+    with pytest.raises(ValueError, match="CUDA device"):
+        vsa.layer_norm_fwd(x, None, None, 1e-6, x.clone())
+    with pytest.raises(ValueError, match="shape"):
+        vsa.layer_norm_fwd(x, None, None, 1e-6, x[:2])
+    with pytest.raises(ValueError, match="one type"):
+        vsa.layer_norm_fwd(x, torch.zeros(128), torch.zeros(128).half(), 1e-6, x.clone())
+    with pytest.raises(ValueError, match=r"\[S, width\]"):
+        vsa.layer_norm_fwd(x[0], None, None, 1e-6, x[0])
