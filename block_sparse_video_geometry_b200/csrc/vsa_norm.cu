@@ -25,11 +25,13 @@ namespace {
 
 constexpr int kWarpBlock = 256;      // threads of a block of the short-row kernels
 
-// Rows [B, S, heads] in one index.
+// Rows [B, S, heads] in one index. Where the rows of every view lie at one
+// stride the host gives them as [1, n, 1], which needs no division.
 struct Rows {
   int64_t n;                         // B * S * heads
   int64_t S;
   int32_t heads;
+  int32_t flat;
 };
 
 struct Place {
@@ -37,6 +39,7 @@ struct Place {
 };
 
 __device__ __forceinline__ Place place(const Rows& R, int64_t row) {
+  if (R.flat) return Place{0, row, 0};
   // rows < 2^31: 32-bit divisions
   const uint32_t r = static_cast<uint32_t>(row), t = r / static_cast<uint32_t>(R.heads);
   Place p;
@@ -84,6 +87,15 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c, flo
   }
 }
 
+// Weight and bias of vector c (1 and 0 where there are none).
+template <class T, int VEC>
+__device__ __forceinline__ void weights(const FwdArgs& a, int c, int nv, float (&w)[VEC], float (&b)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) w[j] = 1.0f, b[j] = 0.0f;
+  if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, c * VEC, w);
+  if (a.b && c < nv) load_weight<T, VEC>(a.b, a.w_f32, c * VEC, b);
+}
+
 template <int LANES>
 __device__ __forceinline__ float lane_sum(float x) {
 #pragma unroll
@@ -104,89 +116,99 @@ __device__ __forceinline__ float block_sum(float x, float* buf) {
 }
 
 // ------------------------------------------------------------------ forward
-// E vectors of VEC elements per thread: vector i of thread t is i * TPR + t,
-// TPR the threads of a row (LANES of a warp, or the block).
-template <class T, int VEC, int E, int LANES, int MAXT>
+// A row is spread over TPR threads (LANES of a warp, or the block), E vectors of
+// VEC elements each: vector i of thread t is i * TPR + t. The row stays packed
+// in registers between its passes (sum, squares, output). U rows per group are
+// in flight at once.
+template <class T, int VEC, int E, int LANES, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
   constexpr bool kWarp = LANES <= 32;
+  constexpr int kLanes = kWarp ? LANES : 32;
   __shared__ float red[2][2][32];
   const int tpr = kWarp ? LANES : blockDim.x;
   const int t = kWarp ? threadIdx.x % LANES : threadIdx.x;
-  const int rows_per_block = kWarp ? kWarpBlock / LANES : 1;
+  const int groups = kWarp ? kWarpBlock / LANES : 1;
+  const int group = kWarp ? threadIdx.x / LANES : 0;
   const int nv = a.width / VEC;
+  // A short row's weights stay in registers; a long row's come from L1 with each row.
+  constexpr bool kKeep = E * VEC <= 8;
+  float w[kKeep ? E : 1][VEC], b[kKeep ? E : 1][VEC];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) weights<T, VEC>(a, i * tpr + t, nv, w[i], b[i]);
+  }
   int phase = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_block; r0 < a.R.n;
-       r0 += static_cast<int64_t>(gridDim.x) * rows_per_block) {
-    const int64_t row = kWarp ? r0 + threadIdx.x / LANES : r0;
-    const bool live = row < a.R.n;                 // whole lane groups; every lane takes part in the sums
-    Place p{};
-    if (live) p = place(a.R, row);
-    const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
-    float v[E][VEC];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * U;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups * U; r0 < a.R.n; r0 += step) {
+    Pack<T, VEC> k[U][E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * tpr + t;
-      if (live && c < nv) {
-        Pack<T, VEC> k;
-        k.load(x + static_cast<int64_t>(c) * VEC);
-        k.get(v[i]);
-      } else {
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r0 + u * groups + group;
+      if (row >= a.R.n) continue;
+      const T* x = static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row));
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = 0.0f;
+      for (int i = 0; i < E; ++i)
+        if (i * tpr + t < nv) k[u][i].load(x + static_cast<int64_t>(i * tpr + t) * VEC);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r0 + u * groups + group;
+      const bool live = row < a.R.n;               // whole lane groups; every lane takes part in the sums
+      float sum = 0.0f, sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (!live || i * tpr + t >= nv) continue;
+        float v[VEC];
+        k[u][i].get(v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum += v[j];
       }
-    }
-    float sum = 0.0f;
+      const float mean = (kWarp ? lane_sum<kLanes>(sum) : block_sum(sum, red[phase][0])) * a.inv_n;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+      for (int i = 0; i < E; ++i) {
+        if (!live || i * tpr + t >= nv) continue;
+        float v[VEC];
+        k[u][i].get(v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum += v[i][j];
-    const float mean = (kWarp ? lane_sum<kWarp ? LANES : 32>(sum) : block_sum(sum, red[phase][0])) * a.inv_n;
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const bool in = i * tpr + t < nv;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = v[i][j] - mean;
-        sq += in ? d * d : 0.0f;
+        for (int j = 0; j < VEC; ++j) sq = fmaf(v[j] - mean, v[j] - mean, sq);
       }
-    }
-    const float var = (kWarp ? lane_sum<kWarp ? LANES : 32>(sq) : block_sum(sq, red[phase][1])) * a.inv_n;
-    phase ^= 1;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
-    if (!live) continue;
-    T* y = static_cast<T*>(a.y) + offset(a.sy, p);
+      const float var = (kWarp ? lane_sum<kLanes>(sq) : block_sum(sq, red[phase][1])) * a.inv_n;
+      phase ^= 1;
+      const float rstd = 1.0f / sqrtf(var + a.eps);
+      if (!live) continue;
+      T* y = static_cast<T*>(a.y) + offset(a.sy, place(a.R, row));
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * tpr + t;
-      if (c >= nv) continue;
-      float w[VEC], b[VEC];
+      for (int i = 0; i < E; ++i) {
+        const int c = i * tpr + t;
+        if (c >= nv) continue;
+        float v[VEC], wl[VEC], bl[VEC];
+        if constexpr (!kKeep) weights<T, VEC>(a, c, nv, wl, bl);
+        k[u][i].get(v);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) w[j] = 1.0f, b[j] = 0.0f;
-      if (a.w) load_weight<T, VEC>(a.w, a.w_f32, c * VEC, w);
-      if (a.b) load_weight<T, VEC>(a.b, a.w_f32, c * VEC, b);
-      float o[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = fmaf((v[i][j] - mean) * rstd, w[j], b[j]);
-      Pack<T, VEC> k;
-      k.set(o);
-      k.store(y + static_cast<int64_t>(c) * VEC);
-    }
-    if (t == 0 && a.mean) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
+        for (int j = 0; j < VEC; ++j)
+          v[j] = fmaf((v[j] - mean) * rstd, kKeep ? w[kKeep ? i : 0][j] : wl[j], kKeep ? b[kKeep ? i : 0][j] : bl[j]);
+        k[u][i].set(v);
+        k[u][i].store(y + static_cast<int64_t>(c) * VEC);
+      }
+      if (t == 0 && a.mean) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+      }
     }
   }
 }
 
 // ----------------------------------------------------------------- backward
-template <class T, class G, int VEC, int E, int LANES, int MAXT>
+// Same spread. A thread keeps the weights and the running dw and db of its
+// columns, and loads the next rows while it works on the current ones.
+template <class T, class G, int VEC, int E, int LANES, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
   constexpr bool kWarp = LANES <= 32;
   __shared__ float red[2][2][32];
   const int tpr = kWarp ? LANES : blockDim.x;
   const int t = kWarp ? threadIdx.x % LANES : threadIdx.x;
-  const int rows_per_block = kWarp ? kWarpBlock / LANES : 1;
+  const int groups = kWarp ? kWarpBlock / LANES : 1;
+  const int group = kWarp ? threadIdx.x / LANES : 0;
   const int nv = a.width / VEC;
   float w[E][VEC], dw[E][VEC], db[E][VEC];
 #pragma unroll
@@ -196,82 +218,109 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
     const int c = i * tpr + t;
     if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, c * VEC, w[i]);
   }
+  Pack<T, VEC> kx[U][E];
+  Pack<G, VEC> kg[U][E];
+  float mean[U], rstd[U];
+  auto fetch = [&](int64_t r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r0 + u * groups + group;
+      mean[u] = rstd[u] = 0.0f;
+      if (row >= a.R.n) continue;
+      const Place p = place(a.R, row);
+      const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
+      const G* dy = static_cast<const G*>(a.dy) + offset(a.sdy, p);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int64_t c = i * tpr + t;
+        if (c >= nv) continue;
+        kx[u][i].load(x + c * VEC);
+        kg[u][i].load(dy + c * VEC);
+      }
+      mean[u] = a.mean[row];
+      rstd[u] = a.rstd[row];
+    }
+  };
   int phase = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_block; r0 < a.R.n;
-       r0 += static_cast<int64_t>(gridDim.x) * rows_per_block) {
-    const int64_t row = kWarp ? r0 + threadIdx.x / LANES : r0;
-    const bool live = row < a.R.n;
-    Place p{};
-    if (live) p = place(a.R, row);
-    const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
-    const G* dy = static_cast<const G*>(a.dy) + offset(a.sdy, p);
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
-    float xh[E][VEC], g[E][VEC];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * U;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups * U;
+  if (r0 < a.R.n) fetch(r0);
+  for (; r0 < a.R.n; r0 += step) {
+    // the rows stay packed between the two passes: unpacked they would not fit
+    Pack<T, VEC> cx[U][E];
+    Pack<G, VEC> cg[U][E];
+    float s1[U], s2[U], mu[U], rs[U];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * tpr + t;
-      if (live && c < nv) {
-        Pack<T, VEC> kx;
-        Pack<G, VEC> kg;
-        kx.load(x + static_cast<int64_t>(c) * VEC);
-        kg.load(dy + static_cast<int64_t>(c) * VEC);
-        kx.get(xh[i]);
-        kg.get(g[i]);
-      } else {
+    for (int u = 0; u < U; ++u) {
+      const bool live = r0 + u * groups + group < a.R.n;
+      s1[u] = s2[u] = 0.0f;
+      mu[u] = mean[u];
+      rs[u] = rstd[u];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) xh[i][j] = mean, g[i][j] = 0.0f;
+      for (int i = 0; i < E; ++i) {
+        if (!live || i * tpr + t >= nv) continue;
+        cx[u][i] = kx[u][i];
+        cg[u][i] = kg[u][i];
+        float xh[VEC], g[VEC];
+        cx[u][i].get(xh);
+        cg[u][i].get(g);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          xh[j] = (xh[j] - mu[u]) * rs[u];
+          dw[i][j] = fmaf(g[j], xh[j], dw[i][j]);
+          db[i][j] += g[j];
+          g[j] *= w[i][j];
+          s1[u] += g[j];
+          s2[u] = fmaf(g[j], xh[j], s2[u]);
+        }
       }
     }
-    float s1 = 0.0f, s2 = 0.0f;
+    // dx may lie over dy: a row is fetched and written by the same block, in that order
+    if (r0 + step < a.R.n) fetch(r0 + step);
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        xh[i][j] = (xh[i][j] - mean) * rstd;
-        dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-        db[i][j] += g[i][j];
-        g[i][j] *= w[i][j];
-        s1 += g[i][j];
-        s2 = fmaf(g[i][j], xh[i][j], s2);
-      }
-    if constexpr (kWarp) {
-      s1 = lane_sum<LANES>(s1);
-      s2 = lane_sum<LANES>(s2);
-    } else {
-      s1 = lane_sum<32>(s1);
-      s2 = lane_sum<32>(s2);
+    for (int u = 0; u < U; ++u) {
+      s1[u] = lane_sum<kWarp ? LANES : 32>(s1[u]);
+      s2[u] = lane_sum<kWarp ? LANES : 32>(s2[u]);
+    }
+    if constexpr (!kWarp) {
+      static_assert(U == 1, "one row per block");
       const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
       if (warps > 1) {
         if (lane == 0) {
-          red[phase][0][threadIdx.x >> 5] = s1;
-          red[phase][1][threadIdx.x >> 5] = s2;
+          red[phase][0][threadIdx.x >> 5] = s1[0];
+          red[phase][1][threadIdx.x >> 5] = s2[0];
         }
         __syncthreads();
-        s1 = lane_sum<32>(lane < warps ? red[phase][0][lane] : 0.0f);
-        s2 = lane_sum<32>(lane < warps ? red[phase][1][lane] : 0.0f);
+        s1[0] = lane_sum<32>(lane < warps ? red[phase][0][lane] : 0.0f);
+        s2[0] = lane_sum<32>(lane < warps ? red[phase][1][lane] : 0.0f);
         phase ^= 1;
       }
     }
-    s1 *= a.inv_n;
-    s2 *= a.inv_n;
-    if (!live) continue;
-    const int64_t od = offset(a.sdx, p);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * tpr + t;
-      if (c >= nv) continue;
-      float o[VEC];
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r0 + u * groups + group;
+      if (row >= a.R.n) continue;
+      const float c1 = s1[u] * a.inv_n, c2 = s2[u] * a.inv_n;
+      const int64_t od = offset(a.sdx, place(a.R, row));
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = rstd * (g[i][j] - fmaf(xh[i][j], s2, s1));
-      const int64_t at = od + static_cast<int64_t>(c) * VEC;
-      if (a.dx_f32) {
-        Pack<float, VEC> k;
-        k.set(o);
-        k.store(static_cast<float*>(a.dx) + at);
-      } else {
-        Pack<T, VEC> k;
-        k.set(o);
-        k.store(static_cast<T*>(a.dx) + at);
+      for (int i = 0; i < E; ++i) {
+        const int c = i * tpr + t;
+        if (c >= nv) continue;
+        float o[VEC], g[VEC];
+        cx[u][i].get(o);
+        cg[u][i].get(g);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] = rs[u] * (g[j] * w[i][j] - fmaf((o[j] - mu[u]) * rs[u], c2, c1));
+        const int64_t at = od + static_cast<int64_t>(c) * VEC;
+        if (a.dx_f32) {
+          Pack<float, VEC> k;
+          k.set(o);
+          k.store(static_cast<float*>(a.dx) + at);
+        } else {
+          Pack<T, VEC> k;
+          k.set(o);
+          k.store(static_cast<T*>(a.dx) + at);
+        }
       }
     }
   }
@@ -283,7 +332,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
     for (int i = threadIdx.x; i < 2 * LANES * E * VEC; i += kWarpBlock) (&acc[0][0])[i] = 0.0f;
     for (int gidx = 0; gidx < kWarpBlock / LANES; ++gidx) {
       __syncthreads();
-      if (static_cast<int>(threadIdx.x) / LANES != gidx) continue;
+      if (group != gidx) continue;
 #pragma unroll
       for (int i = 0; i < E; ++i)
 #pragma unroll
@@ -335,24 +384,33 @@ norm_sum_kernel(const float* __restrict__ part, int n_part, int width, float* __
 
 // ------------------------------------------------------------------ launches
 // Few vectors of the widest aligned access: lanes of one warp per row. Else one
-// block per row with 8 elements per thread, up to 640 threads (102 registers
-// each) for widths to 5120 and 1024 threads to 8192, then 16 elements per thread.
+// block per row with `ept` elements per thread.
 struct Shape {
   int vec, lanes;         // lanes 64: one block per row
-  int ept, most;          // elements per thread, thread bound of the kernel variant
+  int ept;
   int threads, rows_per_block;
 };
+constexpr int kFwdU = 4, kBwdU = 2;   // rows in flight per lane group of the short-row kernels
 
-Shape shape_of(int width, int vec) {
+Shape shape_of(int width, int vec, int ept, int u) {
   const int nv = width / vec;
   if (nv <= 32) {
     const int lanes = nv <= 16 ? 16 : 32;
-    return Shape{vec, lanes, vec, kWarpBlock, kWarpBlock, kWarpBlock / lanes};
+    return Shape{vec, lanes, vec, kWarpBlock, kWarpBlock / lanes * u};
   }
-  const int ept = width <= 8192 ? 8 : 16;
   const int e = ept / vec;
-  return Shape{vec, 64, ept, width <= 5120 ? 640 : 1024, ((nv + e - 1) / e + 31) / 32 * 32, 1};
+  return Shape{vec, 64, ept, ((nv + e - 1) / e + 31) / 32 * 32, 1};
 }
+
+// Forward: 32 elements per thread (four 16-byte loads of bf16 in flight) once
+// the rows fill the GPU; few rows are spread over more threads.
+int fwd_ept(int width, int64_t rows) {
+  if (width > 8192) return rows >= 512 ? 32 : 16;
+  return rows >= 512 && width >= 2048 ? 32 : 8;
+}
+// Backward: 16 elements per thread, so that weights, dw, db, two rows and the
+// next rows' packed data fit its registers; 8 for narrow rows.
+int bwd_ept(int width) { return width > 1024 ? 16 : 8; }
 
 int sm_count() {
   int dev = 0, n = 0;
@@ -364,7 +422,7 @@ int sm_count() {
 constexpr int kMaxSms = 160;                        // the workspace is sized for this many
 // Blocks of the backward kernel: a partial row each, so no more than fill the GPU.
 int bwd_blocks(int64_t rows, const Shape& s) {
-  const int per_sm = std::max(1, std::min(8, 1024 / s.threads));
+  const int per_sm = std::max(1, std::min(8, 640 / s.threads));
   const int64_t most = static_cast<int64_t>(std::min(sm_count(), kMaxSms)) * per_sm;
   return static_cast<int>(std::min<int64_t>((rows + s.rows_per_block - 1) / s.rows_per_block, most));
 }
@@ -373,20 +431,38 @@ template <class T, int VEC>
 void fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
   const int64_t groups = (a.R.n + s.rows_per_block - 1) / s.rows_per_block;
   const int blocks = static_cast<int>(std::min<int64_t>(groups, 1 << 20));
-  if (s.lanes == 16) norm_fwd_kernel<T, VEC, 1, 16, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.lanes == 32) norm_fwd_kernel<T, VEC, 1, 32, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.ept == 16) norm_fwd_kernel<T, VEC, 16 / VEC, 64, 1024><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.most == 1024) norm_fwd_kernel<T, VEC, 8 / VEC, 64, 1024><<<blocks, s.threads, 0, stream>>>(a);
-  else norm_fwd_kernel<T, VEC, 8 / VEC, 64, 640><<<blocks, s.threads, 0, stream>>>(a);
+  const int waves = static_cast<int>(std::min<int64_t>(groups, sm_count() * 8));
+  if (s.lanes == 16) norm_fwd_kernel<T, VEC, 1, 16, kFwdU, kWarpBlock><<<waves, s.threads, 0, stream>>>(a);
+  else if (s.lanes == 32) norm_fwd_kernel<T, VEC, 1, 32, kFwdU, kWarpBlock><<<waves, s.threads, 0, stream>>>(a);
+  else if (s.ept == 32) norm_fwd_kernel<T, VEC, 32 / VEC, 64, 1, 512><<<blocks, s.threads, 0, stream>>>(a);
+  else if (s.ept == 16) norm_fwd_kernel<T, VEC, 16 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
+  else norm_fwd_kernel<T, VEC, 8 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
 }
 
 template <class T, class G, int VEC>
 void bwd_launch(const Shape& s, const BwdArgs& a, int blocks, cudaStream_t stream) {
-  if (s.lanes == 16) norm_bwd_kernel<T, G, VEC, 1, 16, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.lanes == 32) norm_bwd_kernel<T, G, VEC, 1, 32, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.ept == 16) norm_bwd_kernel<T, G, VEC, 16 / VEC, 64, 1024><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.most == 1024) norm_bwd_kernel<T, G, VEC, 8 / VEC, 64, 1024><<<blocks, s.threads, 0, stream>>>(a);
-  else norm_bwd_kernel<T, G, VEC, 8 / VEC, 64, 640><<<blocks, s.threads, 0, stream>>>(a);
+  if (s.lanes == 16) norm_bwd_kernel<T, G, VEC, 1, 16, kBwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
+  else if (s.lanes == 32) norm_bwd_kernel<T, G, VEC, 1, 32, kBwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
+  else if (s.ept == 8) norm_bwd_kernel<T, G, VEC, 8 / VEC, 64, 1, 640><<<blocks, s.threads, 0, stream>>>(a);
+  else if (s.threads <= 640) norm_bwd_kernel<T, G, VEC, 16 / VEC, 64, 1, 640><<<blocks, s.threads, 0, stream>>>(a);
+  else norm_bwd_kernel<T, G, VEC, 16 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
+}
+
+// Rows at one stride in all views: [1, n, 1].
+bool flat_rows(const Strides& st, int32_t B, int64_t S, int32_t heads, int64_t* stride) {
+  *stride = heads > 1 ? st.h : S > 1 ? st.s : st.b;
+  if (heads > 1 && S > 1 && st.s != heads * st.h) return false;
+  return B == 1 || (heads == 1 && S == 1) || st.b == *stride * heads * S;
+}
+
+template <class... V>
+void flatten(Rows* R, int32_t B, int64_t S, V*... views) {
+  int64_t stride[sizeof...(V)];
+  int i = 0;
+  if (!(flat_rows(*views, B, S, R->heads, &stride[i++]) && ...)) return;
+  i = 0;
+  ((*views = Strides{0, stride[i++], 0}), ...);
+  R->flat = 1;
 }
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -407,6 +483,7 @@ vsa_status check_rows(int32_t B, int64_t S, int32_t heads, int32_t width, Rows* 
   R->n = static_cast<int64_t>(B) * S * heads;
   R->S = S;
   R->heads = heads;
+  R->flat = 0;
   return VSA_OK;
 }
 
@@ -442,12 +519,13 @@ vsa_status vsa_layer_norm_fwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.rstd = rstd;
   a.sx = view_strides(x, B, S);
   a.sy = view_strides(y, B, S);
+  flatten(&a.R, B, S, &a.sx, &a.sy);
   a.width = width;
   a.eps = eps;
   a.inv_n = 1.0f / static_cast<float>(width);
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(y, a.sy, vec, width);
-  const Shape s = shape_of(width, wide ? vec : 1);
+  const Shape s = shape_of(width, wide ? vec : 1, fwd_ept(width, a.R.n), kFwdU);
   if (x->dtype == VSA_F32) wide ? fwd_launch<float, 4>(s, a, stream) : fwd_launch<float, 1>(s, a, stream);
   else if (x->dtype == VSA_BF16) wide ? fwd_launch<bf16, 8>(s, a, stream) : fwd_launch<bf16, 1>(s, a, stream);
   else wide ? fwd_launch<f16, 8>(s, a, stream) : fwd_launch<f16, 1>(s, a, stream);
@@ -507,12 +585,13 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.sdy = view_strides(dy, B, S);
   a.sx = view_strides(x, B, S);
   a.sdx = view_strides(dx, B, S);
+  flatten(&a.R, B, S, &a.sdy, &a.sx, &a.sdx);
   a.part = dweight || dbias ? static_cast<float*>(workspace) : nullptr;
   a.width = width;
   a.inv_n = 1.0f / static_cast<float>(width);
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(dy, a.sdy, vec, width) && vec_ok(dx, a.sdx, vec, width);
-  const Shape s = shape_of(width, wide ? vec : 1);
+  const Shape s = shape_of(width, wide ? vec : 1, bwd_ept(width), kBwdU);
   const int blocks = bwd_blocks(a.R.n, s);
   const bool g32 = dy->dtype == VSA_F32;
   if (x->dtype == VSA_F32) {

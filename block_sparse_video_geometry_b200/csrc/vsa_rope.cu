@@ -30,6 +30,8 @@ constexpr int kPairs = kHeadDim / 2;
 constexpr int kChunk = 8;                        // channels per thread and step
 constexpr int kLanes = kHeadDim / kChunk;        // lanes per row
 constexpr int kRopeUnroll = 4;                   // rows in flight per thread
+constexpr int kRopeTokens = 4;                   // most tokens per block
+constexpr int kRopeMaxHeads = 8192;              // of q and of k: row numbers of a block times heads fit 32 bits
 
 struct RopeTable {
   double rate[kPairs];         // turns per position
@@ -45,6 +47,7 @@ struct RopeArgs {
   void* out[2];
   Strides si[2], so[2];
   int heads_q, heads;          // heads of q, and of q and k together
+  uint64_t per_head;           // ceil(2^32 / heads): rows of a block / heads by one multiplication
   int64_t n_tokens, S;
   const int32_t* pos;
   int64_t pos_sb;
@@ -55,6 +58,7 @@ template <class I, class O, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, int tokens_per_block) {
   extern __shared__ float2 turn[];               // [token][pair]: cos, signed sin
+  __shared__ int64_t base[kRopeTokens][4];       // element offset of each token in q, k and their outputs
   __shared__ float rows[kHalves ? kRopeThreads / kLanes * kHeadDim : 1];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_block), a.n_tokens - t0));
@@ -62,6 +66,10 @@ rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeA
     const int64_t tok = t0 + i / kPairs;
     const int p = i % kPairs;
     const int64_t b = tok / a.S, s = tok - b * a.S;
+    if (p < 4) {
+      const Strides st = p == 0 ? a.si[0] : p == 1 ? a.si[1] : p == 2 ? a.so[0] : a.so[1];
+      base[i / kPairs][p] = b * st.b + s * st.s;
+    }
     const double t = static_cast<double>(a.pos[b * a.pos_sb + 3 * s + tab.axis[p]]) * tab.rate[p];
     float sn, cs;
     sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &cs);
@@ -78,24 +86,23 @@ rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeA
   const int n_rows = nt * a.heads;
   // Every lane runs every step (the exchange synchronises warps); rows past the
   // end are neither read nor written.
-  for (int base = 0; base < n_rows; base += kGroups * kRopeUnroll) {
+  for (int row0 = 0; row0 < n_rows; row0 += kGroups * kRopeUnroll) {
     Pack<I, kChunk> x[kRopeUnroll];
     O* dst[kRopeUnroll];
     int tk[kRopeUnroll];
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      const int r = base + u * kGroups + group;
+      const int r = row0 + u * kGroups + group;
       dst[u] = nullptr;
       tk[u] = 0;
       if (r >= n_rows) continue;
-      tk[u] = r / a.heads;
+      tk[u] = static_cast<int>(static_cast<uint32_t>(r) * a.per_head >> 32);
       const int hh = r - tk[u] * a.heads;
-      const int w = hh >= a.heads_q;
+      const bool w = hh >= a.heads_q;
       const int64_t h = w ? hh - a.heads_q : hh;
-      const int64_t tok = t0 + tk[u], b = tok / a.S, s = tok - b * a.S;
-      const Strides si = w ? a.si[1] : a.si[0], so = w ? a.so[1] : a.so[0];
-      x[u].load(static_cast<const I*>(w ? a.in[1] : a.in[0]) + b * si.b + s * si.s + h * si.h + c0);
-      dst[u] = static_cast<O*>(w ? a.out[1] : a.out[0]) + b * so.b + s * so.s + h * so.h + c0;
+      const int64_t* at = base[tk[u]] + w;
+      x[u].load(static_cast<const I*>(w ? a.in[1] : a.in[0]) + at[0] + h * (w ? a.si[1].h : a.si[0].h) + c0);
+      dst[u] = static_cast<O*>(w ? a.out[1] : a.out[0]) + at[2] + h * (w ? a.so[1].h : a.so[0].h) + c0;
     }
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
@@ -229,7 +236,7 @@ vsa_status rope_call(const char* where, const vsa_rope* rope, int32_t B, int64_t
     if (st == VSA_OK) st = check_view(out[w], B, S, kHeadDim, 16, true);
     if (st != VSA_OK) return st;
     if (in[w]->heads != out[w]->heads) return VSA_ERR_INVALID_ARG;
-    if (in[w]->heads > 65535) return VSA_ERR_UNSUPPORTED;
+    if (in[w]->heads > kRopeMaxHeads) return VSA_ERR_UNSUPPORTED;
   }
   if (B == 0 || S == 0) return VSA_OK;
   if (!pos || reinterpret_cast<uintptr_t>(pos) % 4) return VSA_ERR_INVALID_ARG;
@@ -249,12 +256,13 @@ vsa_status rope_call(const char* where, const vsa_rope* rope, int32_t B, int64_t
     }
     a.heads_q = in[w]->heads;
     a.heads = together ? q->heads + k->heads : in[w]->heads;
+    a.per_head = ((uint64_t{1} << 32) + a.heads - 1) / a.heads;
     a.S = S;
     a.n_tokens = S * B;
     a.pos = pos;
     a.pos_sb = B > 1 ? pos_sb : 0;
     a.sign = sign;
-    const int tpb = a.n_tokens >= 4096 ? 4 : 1;
+    const int tpb = a.n_tokens >= 4096 ? kRopeTokens : 1;
     const int blocks = static_cast<int>((a.n_tokens + tpb - 1) / tpb);
     const bool halves = rope->pairing == VSA_ROPE_HALVES;
     if (in[w]->dtype == VSA_F32) rope_launch_in<float>(out[w]->dtype, tab, a, halves, tpb, blocks, stream);
