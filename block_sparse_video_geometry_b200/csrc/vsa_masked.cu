@@ -1,0 +1,909 @@
+// Dense attention with capped scores, a distance bias, document and prefix
+// masks: forward pass.
+//
+// Mathematics, per row: x_j = log2(e) * score_j, running maximum m and sum
+// l = sum 2^(x_j - m), O = sum 2^(x_j - m) v_j; out = O / l, lse = ln2 (m + log2 l).
+// Partial results over parts of the key axis join by their lse.
+//
+// Bound: tensor pipe (4 * 128 FLOP per visible pair) next to the exponentials
+// (one per pair; two more operations of that unit with a cap); one query over a
+// long cache: HBM (k and v read once).
+//
+// Design. A block owns 256 rows of one head as two M = 128 tiles and walks the
+// key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
+// 32 KB stages; two warps issue the products, one per query tile; two groups of
+// four warps run the softmax, a thread per row. S of a tile and P over it share
+// TMEM columns, so the tensor pipe works on one query tile while the other's
+// softmax runs: S(j) -> P(j) (bf16, A operand from TMEM) -> O += P(j) V(j), and
+// S(j + 1) behind it. The softmax's reference is raised, and O rescaled in TMEM,
+// only when a row's sum of P in a tile passes 2^8.
+// Few rows (a new token over a cache): the heads that share a key head are
+// packed into one tile, the two slots take the key tiles in turn with the same
+// queries, and the key axis is split over blocks; a second kernel joins the
+// parts.
+// Tiles that no row of the block sees are skipped: by arithmetic for causal
+// masks, by a list that plan_kernel makes from the tiles' document ranges.
+// Every wait is bounded (see vsa_masked_attn_status).
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "sm100.cuh"
+#include "vec.cuh"
+#include "vsa_masked.h"
+
+namespace vsa {
+namespace masked {
+
+using namespace sm100;
+
+// ------------------------------------------------------------------- host
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  return n;
+}
+
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+vsa_status encode(CUtensorMap* map, const void* data, int64_t S, int64_t heads, int64_t B, int64_t ss, int64_t sh,
+                  int64_t sb) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return cuda_fail("cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ss) * 2, static_cast<cuuint64_t>(sh) * 2,
+                                 static_cast<cuuint64_t>(sb) * 2};
+  const cuuint32_t box[4] = {64, kRows, 1, 1}, one[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(data), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? VSA_OK : cuda_fail("cuTensorMapEncodeTiled refused a view");
+}
+
+}  // namespace
+
+// A dimension of size 1 or stride 0 (broadcast) is given to the map with extent
+// 1; the kernels use coordinate 0 for it.
+vsa_status make_map(CUtensorMap* map, const vsa_view* v, int32_t B, int32_t S) {
+  const Strides st = view_strides(v, B, S);
+  return encode(map, v->data, S, st.h ? v->heads : 1, st.b ? B : 1, S > 1 ? st.s : kHeadDim, st.h ? st.h : kHeadDim,
+                st.b ? st.b : kHeadDim);
+}
+
+vsa_status make_map(CUtensorMap* map, const uint16_t* copy, int32_t B, int32_t S, int32_t heads) {
+  const int64_t row = static_cast<int64_t>(heads) * kHeadDim;
+  return encode(map, copy, S, heads, B, row, kHeadDim, row * S);
+}
+
+vsa_status check(const vsa_mask* m, const vsa_mask_terms* t, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq, int32_t Hk,
+                 Problem* p) {
+  if (!m || (m->mode != VSA_MASK_FULL && m->mode != VSA_MASK_CAUSAL)) return VSA_ERR_INVALID_ARG;
+  if (m->documents != 0 && m->documents != 1) return VSA_ERR_INVALID_ARG;
+  if (!std::isfinite(m->scale) || !std::isfinite(m->softcap) || m->softcap < 0.0f) return VSA_ERR_INVALID_ARG;
+  if (B < 0 || Sq < 0 || Sk < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk) return VSA_ERR_INVALID_ARG;
+  if (B > 65535 || Hq > 65535 || Sq > kMaxPositions || Sk > kMaxPositions) return VSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * Hq * tiles(std::max(Sq, Sk)) > INT32_MAX / 32) return VSA_ERR_UNSUPPORTED;
+  *p = Problem{};
+  p->B = B;
+  p->Hq = Hq;
+  p->Hk = Hk;
+  p->group = Hq / Hk;
+  p->Sq = Sq;
+  p->Sk = Sk;
+  p->off = Sk - Sq;
+  p->nkt = tiles(Sk);
+  p->causal = m->mode == VSA_MASK_CAUSAL;
+  p->documents = m->documents;
+  p->masked = m->documents || (p->causal && Sq > 1);
+  p->scale = m->scale > 0.0f ? m->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(kHeadDim)));
+  p->cap = m->softcap;
+  if (!t) return m->documents ? VSA_ERR_INVALID_ARG : VSA_OK;
+  const bool empty = B == 0 || Sq == 0 || Sk == 0;
+  if (!empty && m->documents != (t->doc_q != nullptr)) return VSA_ERR_INVALID_ARG;
+  if (!empty && m->documents != (t->doc_k != nullptr)) return VSA_ERR_INVALID_ARG;
+  if (t->prefix && !p->causal) return VSA_ERR_INVALID_ARG;
+  for (const void* x : {static_cast<const void*>(t->doc_q), static_cast<const void*>(t->doc_k),
+                        static_cast<const void*>(t->prefix), static_cast<const void*>(t->slopes)})
+    if (reinterpret_cast<uintptr_t>(x) % 4) return VSA_ERR_INVALID_ARG;
+  if (m->documents && B > 1 && (t->doc_q_stride_b < 0 || t->doc_k_stride_b < 0)) return VSA_ERR_INVALID_ARG;
+  p->doc_q = t->doc_q;
+  p->doc_k = t->doc_k;
+  p->doc_q_sb = B > 1 ? t->doc_q_stride_b : 0;
+  p->doc_k_sb = B > 1 ? t->doc_k_stride_b : 0;
+  p->prefix = t->prefix;
+  p->slopes = t->slopes;
+  return VSA_OK;
+}
+
+vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, bool output) {
+  const vsa_status st = check_view(v, B, S, kHeadDim, 16, output);
+  if (st != VSA_OK) return st;
+  if (v->heads != heads || v->dtype != VSA_BF16) return VSA_ERR_INVALID_ARG;
+  if (S > 1 && B > 0 && v->stride_s == 0) return VSA_ERR_UNSUPPORTED;
+  // a tensor map's strides stay below 2^40 bytes
+  const Strides s = view_strides(v, B, S);
+  for (int64_t x : {s.b, s.s, s.h})
+    if (x >= (int64_t{1} << 39)) return VSA_ERR_UNSUPPORTED;
+  return VSA_OK;
+}
+
+// ------------------------------------------------------------- small kernels
+namespace {
+
+// One block per (tile, head, batch entry): rows with an infinity or NaN, and the
+// tile's copy without them if there is one. HBM bound: x read once.
+__global__ void __launch_bounds__(256)
+scan_kernel(const uint16_t* __restrict__ x, Strides st, int S, Clean c) {
+  const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  __shared__ uint32_t bad[4];
+  if (threadIdx.x < 4) bad[threadIdx.x] = 0;
+  __syncthreads();
+  const int n = min(kRows, S - tile * kRows);
+  const uint16_t* base = x + b * st.b + h * st.h + static_cast<int64_t>(tile) * kRows * st.s;
+  uint4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 256 + threadIdx.x, r = e >> 4;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (r < n) w[i] = *reinterpret_cast<const uint4*>(base + r * st.s + (e & 15) * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (i * 256 + threadIdx.x) >> 4;
+    bool any = false;
+    for (uint32_t v : {w[i].x, w[i].y, w[i].z, w[i].w})
+      any |= (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+    if (any) atomicOr(&bad[r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
+  const uint4 m = make_uint4(bad[0], bad[1], bad[2], bad[3]);
+  if (threadIdx.x == 0) c.bad[(static_cast<size_t>(b) * gridDim.y + h) * gridDim.x + tile] = m;
+  if (!(m.x | m.y | m.z | m.w)) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 256 + threadIdx.x, r = e >> 4;
+    if (r >= n) continue;
+    if ((bad[r >> 5] >> (r & 31)) & 1u) w[i] = make_uint4(0, 0, 0, 0);
+    const size_t row = (static_cast<size_t>(b) * S + tile * kRows + r) * gridDim.y + h;
+    *reinterpret_cast<uint4*>(c.copy + row * kHeadDim + (e & 15) * 8) = w[i];
+  }
+}
+
+// Smallest and largest document of positions [i0, i0 + n) of a row of ids
+// (INT_MAX, -1 when all are padding) and whether one is padding; one warp.
+struct Range {
+  int lo, hi, pad;
+};
+__device__ __forceinline__ Range doc_range(const int32_t* ids, int i0, int n) {
+  Range r{INT_MAX, -1, 0};
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    const int d = ids[i0 + i];
+    if (d >= 0) {
+      r.lo = min(r.lo, d);
+      r.hi = max(r.hi, d);
+    } else {
+      r.pad = 1;
+    }
+  }
+  r.lo = __reduce_min_sync(0xffffffffu, r.lo);
+  r.hi = __reduce_max_sync(0xffffffffu, r.hi);
+  r.pad = __reduce_or_sync(0xffffffffu, r.pad);
+  return r;
+}
+
+// Document ranges of the key tiles: [B][nkt].
+__global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Problem p, int4* __restrict__ range) {
+  const int tile = blockIdx.x * 4 + (threadIdx.x >> 5), b = blockIdx.y;
+  if (tile >= p.nkt) return;
+  const Range r = doc_range(p.doc_k + b * p.doc_k_sb, tile * kRows, min(kRows, p.Sk - tile * kRows));
+  if ((threadIdx.x & 31) == 0) range[static_cast<size_t>(b) * p.nkt + tile] = make_int4(r.lo, r.hi, r.pad, 0);
+}
+
+// Key tiles that some row of a query block sees, ascending, with a flag per
+// query tile where its documents do not cover the whole tile pair. One block per
+// (query block, batch entry).
+constexpr int kPartial0 = 1 << 29, kPartial1 = 1 << 30, kTileMask = kPartial0 - 1;
+__global__ void __launch_bounds__(256)
+plan_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, int rows_per_tile, int n_blocks,
+            int32_t* __restrict__ count, int32_t* __restrict__ list) {
+  const int qb = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int4 q[2];
+  __shared__ int n_warp[8];
+  // rows_per_tile = 0: both tiles hold all queries
+  if (warp < 2) {
+    const int i0 = rows_per_tile ? (qb * 2 + warp) * rows_per_tile : 0;
+    const int n = rows_per_tile ? max(0, min(rows_per_tile, p.Sq - i0)) : p.Sq;
+    const Range r = doc_range(p.doc_q + b * p.doc_q_sb, min(i0, p.Sq), n);
+    if (lane == 0) q[warp] = make_int4(r.lo, r.hi, r.pad, n > 0 ? p.limit(b, i0 + n - 1) : -1);
+  }
+  __syncthreads();
+  int total = 0;
+  int32_t* out = list + (static_cast<size_t>(b) * n_blocks + qb) * p.nkt;
+  for (int t0 = 0; t0 < p.nkt; t0 += 256) {
+    const int kt = t0 + threadIdx.x;
+    int rec = -1;
+    if (kt < p.nkt) {
+      const int4 k = range[static_cast<size_t>(b) * p.nkt + kt];
+      bool any = false;
+      int flags = 0;
+      for (int t = 0; t < 2; ++t) {
+        const int4 r = q[t];
+        any |= k.x <= r.y && r.x <= k.y && kt * kRows <= r.w;
+        if (!(k.x == k.y && r.x == r.y && k.x == r.x && !k.z && !r.z)) flags |= t ? kPartial1 : kPartial0;
+      }
+      if (any) rec = kt | flags;
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, rec >= 0);
+    if (lane == 0) n_warp[warp] = __popc(vote);
+    __syncthreads();
+    int at = total;
+    for (int w = 0; w < 8; ++w) {
+      at += w < warp ? n_warp[w] : 0;
+      total += n_warp[w];
+    }
+    if (rec >= 0) out[at + __popc(vote & ((1u << lane) - 1u))] = rec;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) count[static_cast<size_t>(b) * n_blocks + qb] = total;
+}
+
+// --------------------------------------------------------------- main kernel
+constexpr int kStages = 5;
+constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpMma = 9;          // warps 0-7: softmax; 9, 10: products of query tile 0, 1
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;          // S of tile t: 128 t; O of tile t: 256 + 128 t
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, 0, 1);
+constexpr float kSumLimit = 256.0f;                 // 2^8: see the softmax step
+
+struct Smem {
+  uint8_t q[2][kTileBytes];
+  uint8_t kv[kStages][kTileBytes];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Args {
+  Problem p;
+  const uint16_t* q;
+  Strides sq;
+  int32_t k_h, k_b, v_h, v_b;        // 1: the map has that dimension, 0: broadcast
+  Clean clean_v;                     // bad == null: v is not scanned
+  uint16_t* out;
+  Strides so;
+  float* lse;
+  const int32_t* count;              // plan of visible tiles, or null
+  const int32_t* list;
+  int32_t packed;                    // rows = (head of the group, query), unit = key head; else unit = query head
+  int32_t units, rows, n_blocks;     // rows of a unit, blocks of 256 of them
+  int32_t one_tile;                  // rows <= 128: both slots hold the same rows and take turns over the key tiles
+  int32_t splits, parts;             // parts = splits, times 2 with one_tile
+  float* part_o;                     // [part][B][Hq][Sq][128], or null (parts == 1)
+  float* part_lse;                   // [part][B][Hq][Sq], log2
+  int* err;
+};
+
+__device__ __forceinline__ bool bounded_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
+  bool ok = mbar_wait(smem_u32(&bar), parity, &sm.abort, kTimeoutNs);
+  if (!ok) {
+    if (atomicExch(err, VSA_ERR_TIMEOUT) == 0) atomicAdd(err + 1, 1);
+    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+  }
+  return ok;
+}
+// Every lane waits; the warp leaves together.
+__device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, bounded_wait(sm, bar, parity, err));
+}
+
+template <bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_vc) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {          // swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicExch(a.err, VSA_ERR_UNSUPPORTED);
+    return;
+  }
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const Problem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool one = a.one_tile;
+
+  // block -> (query block, split, unit, batch entry); late query blocks, the
+  // longest under a causal mask, first
+  int id = blockIdx.x;
+  const int per = a.units * p.B * a.splits;
+  const int qb = a.n_blocks - 1 - id / per;
+  id %= per;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int unit = id % a.units, b = id / a.units;
+  const int hk = a.packed ? unit : unit / p.group;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one product warp, or by both
+    }
+    mbar_init(smem_u32(&sm.q_full), 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&sm.s_full[t]), 1);
+      mbar_init(smem_u32(&sm.p_full[t]), 4);
+      mbar_init(smem_u32(&sm.o_full[t]), 1);
+      mbar_init(smem_u32(&sm.drain[t]), 1);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // key tiles of this block: entries [s0, s1) of its list (or the numbers themselves)
+  const size_t plan_row = static_cast<size_t>(b) * a.n_blocks + qb;
+  int n_all;
+  if (a.count) {
+    n_all = a.count[plan_row];
+  } else {
+    const int last = a.packed ? p.Sq - 1 : min(qb * 256 + 255, p.Sq - 1);
+    n_all = max(0, p.limit(b, last) + kRows) / kRows;     // tiles up to the last row's limit (none: below 0)
+  }
+  const int32_t* list = a.count ? a.list + plan_row * p.nkt : nullptr;
+  const int s0 = static_cast<int>(static_cast<int64_t>(n_all) * split / a.splits);
+  const int s1 = static_cast<int>(static_cast<int64_t>(n_all) * (split + 1) / a.splits);
+  const int n = s1 - s0;
+  const uint4* bad = a.clean_v.bad ? a.clean_v.bad + (static_cast<size_t>(b) * p.Hk + hk) * p.nkt : nullptr;
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      prefetch_map(&map_k);
+      prefetch_map(&map_v);
+      bool ok = true;
+      int e = 0;
+      for (; ok && e < 2 * n; ++e) {
+        const int st = e % kStages, rec = list ? list[s0 + (e >> 1)] : s0 + (e >> 1);
+        const int kt = rec & kTileMask;
+        if (e >= kStages && !(ok = bounded_wait(sm, sm.empty[st], (e / kStages - 1) & 1, a.err))) break;
+        const CUtensorMap* map = e & 1 ? &map_v : &map_k;
+        int h = (e & 1 ? a.v_h : a.k_h) ? hk : 0, bb = (e & 1 ? a.v_b : a.k_b) ? b : 0;
+        if ((e & 1) && bad) {
+          const uint4 m = bad[kt];
+          if (m.x | m.y | m.z | m.w) map = &map_vc, h = hk, bb = b;
+        }
+        const uint32_t bar = smem_u32(&sm.full[st]), dst = smem_u32(sm.kv[st]);
+        mbar_arrive_expect_tx(bar, kTileBytes);
+        tma_load_4d(dst, map, 0, kt * kRows, h, bb, bar);
+        tma_load_4d(dst + kTileBytes / 2, map, 64, kt * kRows, h, bb, bar);
+      }
+      if (!ok)                                             // every issued copy lands before the block exits
+        for (int i = max(0, e - kStages); i < e; ++i)
+          mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    const int t = warp - kWarpMma;
+    if (lane == 0) {
+      const uint32_t ts = tmem + kColS + 128 * t, to = tmem + kColO + 128 * t;
+      const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
+      bool ok = bounded_wait(sm, sm.q_full, 0, a.err);
+      const int step = one ? 2 : 1;
+      int i = 0;                                           // this slot's step number
+      // S(j) = Q K(j)^T: 16 channels per K step, 32 B inside a swizzled row of the d half kk / 4
+      auto scores = [&](int j) {
+        const int e = 2 * j, st = e % kStages;
+        if (!bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err)) return false;
+        tc_fence_after();
+        const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss(ts, qd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
+                  kIdescS, kk > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&sm.s_full[t]));
+        umma_commit(smem_u32(&sm.empty[st]));
+        return true;
+      };
+      int j = one ? t : 0;
+      if (ok && j < n) ok = scores(j);
+      for (; ok && j < n; j += step, ++i) {
+        const int e = 2 * j + 1, st = e % kStages;
+        if (!(ok = bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
+        if (!(ok = bounded_wait(sm, sm.p_full[t], i & 1, a.err))) break;
+        tc_fence_after();
+        // V as MN-major B: d halves 16 KB apart, 16 keys = 2 KB per K step; P (A,
+        // over its scores): 16 keys = 8 columns of bf16 pairs
+        const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]), 16384, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts(to, ts + kk * 8, vd + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&sm.empty[st]));
+        if (j + step < n) ok = scores(j + step);
+        else umma_commit(smem_u32(&sm.o_full[t]));
+      }
+      if (!ok) {
+        umma_commit(smem_u32(&sm.drain[t]));
+        mbar_wait(smem_u32(&sm.drain[t]), 0, nullptr, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    const int t = warp >> 2;                               // tile (or slot)
+    const int r = threadIdx.x & 127;                       // row of the tile = TMEM lane
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t ts = lane_addr + kColS + 128 * t, to = lane_addr + kColO + 128 * t;
+    const int tile_row0 = qb * 256 + (one ? 0 : t * 128);
+    // rows of Q into shared memory, 16 lanes per row (rows past the end: zero)
+    if (!one || t == 0) {
+      for (int it = 0; it < 16; ++it) {
+        const int e = it * 128 + r, rr = e >> 4, c = e & 15;
+        const int row = tile_row0 + rr;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (row < a.rows) {
+          const int g = a.packed ? row / p.Sq : 0, i = a.packed ? row - g * p.Sq : row;
+          const int h = a.packed ? hk * p.group + g : unit;
+          w = *reinterpret_cast<const uint4*>(a.q + b * a.sq.b + i * a.sq.s + h * a.sq.h + c * 8);
+        }
+        *reinterpret_cast<uint4*>(sm.q[t] + (c >> 3) * 16384 + rr * 128 + ((c & 7) ^ (rr & 7)) * 16) = w;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+
+    const int row = tile_row0 + r;
+    const bool live = row < a.rows;
+    const int g = a.packed ? row / p.Sq : 0;
+    const int i_q = min(a.packed ? row - g * p.Sq : row, p.Sq - 1);
+    const int h = a.packed ? min(hk * p.group + g, p.Hq - 1) : unit;
+    const int lim = p.limit(b, i_q);
+    // smallest limit of the tile's rows: tiles up to there are seen by all of them
+    const int lim0 = p.limit(b, a.packed ? 0 : min(tile_row0, p.Sq - 1));
+    const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
+    const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float c = p.scale * kLog2e;                      // raw score -> log2 units
+    const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+    const float cap2 = kCap ? p.cap * kLog2e : 0.0f, in2 = kCap ? 2.0f * c / p.cap : 0.0f;
+    const float c_exp = kCap || kBias ? 1.0f : c;          // factor still to apply inside the exponential
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    const int step = one ? 2 : 1;
+    int i = 0;
+    for (int j = one ? t : 0; j < n; j += step, ++i) {
+      const int rec = list ? list[s0 + j] : s0 + j;
+      const int kt = rec & kTileMask, k0 = kt * kRows;
+      const bool part_doc = rec & (t ? kPartial1 : kPartial0);
+      const bool partial = part_doc || k0 + kRows - 1 > lim0;
+      uint4 bm = make_uint4(0, 0, 0, 0);
+      if (bad) bm = bad[kt];
+      const bool flagged = bm.x | bm.y | bm.z | bm.w;
+      if (!(ok = warp_wait(sm, sm.s_full[t], i & 1, a.err))) break;
+      tc_fence_after();
+      // scores of columns [32 q4, 32 q4 + 32) in place: cap, bias, mask
+      auto finish = [&](int q4, float (&x)[32]) {
+        const int col = 32 * q4;
+        if constexpr (kCap) {
+          // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = fmaf(__fdividef(-2.0f, 1.0f + ex2_approx(x[u] * in2)), cap2, cap2);
+        }
+        if constexpr (kBias) {
+          const float d0 = static_cast<float>(i_q + p.off - k0 - col);
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            x[u] = fmaf(-slope, fabsf(d0 - static_cast<float>(u)), kCap ? x[u] : x[u] * c);
+        }
+        if (partial) {
+          const int lc = lim - k0 - col;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = u <= lc ? x[u] : -INFINITY;
+          if (part_doc) {
+            const bool seeing = doc >= 0;
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const int d = __ldg(dk + min(k0 + col + u, p.Sk - 1));
+              x[u] = seeing && d == doc ? x[u] : -INFINITY;
+            }
+          }
+        }
+        if (flagged) {
+          // a visible key whose v holds an infinity or NaN makes the row NaN (its v is zero in the copy)
+          const uint32_t bits = q4 == 0 ? bm.x : q4 == 1 ? bm.y : q4 == 2 ? bm.z : bm.w;
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (((bits >> u) & 1u) && x[u] != -INFINITY) x[u] = NAN;
+        }
+      };
+      // P (bf16 pairs) against the reference m, and its 32-bit sum
+      uint32_t w[4][16];
+      auto exponentials = [&]() {
+        const float ms = m == -INFINITY ? 0.0f : m;
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float x[2][32];
+        tmem_ld32x32f(ts, x[0]);
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          float(&y)[32] = x[q4 & 1];
+          tmem_wait_ld32(y);
+          if (q4 < 3) tmem_ld32x32f(ts + 32 * (q4 + 1), x[(q4 + 1) & 1]);
+          finish(q4, y);
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float p0 = ex2_approx(fmaf(y[2 * u], c_exp, -ms));
+            const float p1 = ex2_approx(fmaf(y[2 * u + 1], c_exp, -ms));
+            ls[u & 3] += p0 + p1;
+            w[q4][u] = pack_bf16x2(p0, p1);
+          }
+        }
+        return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      };
+      // The reference m is a maximum of some earlier tile: while a row's sum of P
+      // stays within 2^8, so does every P, and neither the tile's maximum nor a
+      // rescale of O is needed. Otherwise (and on the first visible key) the
+      // exact maximum is formed, O and l are rescaled and P is formed again. S(j)
+      // complete means O of step j - 1 complete (one issuing thread, in order).
+      float psum = 0.0f;
+      if (!__any_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
+      else psum = INFINITY;
+      if (__any_sync(0xffffffffu, !(psum <= kSumLimit))) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int q4 = 0; q4 < 4; ++q4) {
+          float x[32];
+          tmem_ld32x32f(ts + 32 * q4, x);
+          tmem_wait_ld32(x);
+          finish(q4, x);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) top = fmaxf(top, x[u]);
+        }
+        top *= c_exp;
+        const bool grow = top > m;
+        const float f = grow ? ex2_approx(m - top) : 1.0f;   // m = -inf: 0, and l and O are 0
+        if (grow) m = top;
+        l *= f;
+        if (i > 0) {
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            float o[32];
+            tmem_ld32x32f(to + 32 * q4, o);
+            tmem_wait_ld32(o);
+            uint32_t ow[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) ow[u] = __float_as_uint(o[u] * f);
+            tmem_st32x32(to + 32 * q4, ow);
+          }
+        }
+        psum = exponentials();
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) tmem_st32x16(ts + 16 * q4, w[q4]);
+      l += psum;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t]));
+    }
+    // ---------------------------------------------------------- epilogue
+    if (ok && i > 0 && (ok = warp_wait(sm, sm.o_full[t], 0, a.err))) tc_fence_after();
+    if (ok && !(one && t == 1 && a.parts == 1)) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+      const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.Sq + i_q;
+      const int part = one ? split * 2 + t : split;
+      const size_t all = static_cast<size_t>(p.B) * p.Hq * p.Sq;
+      if (live) {
+        if (a.part_o) a.part_lse[part * all + at] = lse2;
+        else a.lse[at] = lse2 * 0.6931471805599453f;
+      }
+#pragma unroll 1
+      for (int q4 = 0; q4 < 4; ++q4) {
+        float o[32];
+        __syncwarp();
+        if (i > 0) {
+          tmem_ld32x32f(to + 32 * q4, o);
+          tmem_wait_ld32(o);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0.0f;
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
+        if (a.part_o) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (part * all + at) * kHeadDim + 32 * q4);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + 32 * q4);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                                pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// out and lse from the parts over the key axis: one warp per row.
+__global__ void __launch_bounds__(256)
+join_kernel(const __grid_constant__ Args a) {
+  const size_t all = static_cast<size_t>(a.p.B) * a.p.Hq * a.p.Sq;
+  const size_t at = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (at >= all) return;
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  bool nan = false;
+  for (int s = lane; s < a.parts; s += 32) {
+    const float x = a.part_lse[s * all + at];
+    top = fmaxf(top, x);
+    nan |= isnan(x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (__any_sync(0xffffffffu, nan)) top = NAN;
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < a.parts; ++s) {
+    const float w = exp2f(a.part_lse[s * all + at] - ref);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * all + at) * kHeadDim + lane * 4);
+    sum += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int i = static_cast<int>(at % a.p.Sq);
+  const size_t bh = at / a.p.Sq;
+  const int h = static_cast<int>(bh % a.p.Hq);
+  const int64_t b = static_cast<int64_t>(bh / a.p.Hq);
+  *reinterpret_cast<uint2*>(a.out + b * a.so.b + i * a.so.s + h * a.so.h + lane * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (lane == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
+
+// out = 0 and lse = -inf of every row (no keys).
+__global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Args a) {
+  const size_t all = static_cast<size_t>(a.p.B) * a.p.Hq * a.p.Sq;
+  const size_t at = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (at >= all) return;
+  const int lane = threadIdx.x & 31;
+  const int i = static_cast<int>(at % a.p.Sq);
+  const size_t bh = at / a.p.Sq;
+  const int h = static_cast<int>(bh % a.p.Hq);
+  const int64_t b = static_cast<int64_t>(bh / a.p.Hq);
+  *reinterpret_cast<uint2*>(a.out + b * a.so.b + i * a.so.s + h * a.so.h + lane * 4) = make_uint2(0u, 0u);
+  if (lane == 0) a.lse[at] = -INFINITY;
+}
+
+// How the rows are laid over blocks, and how often the key axis is split.
+struct Layout {
+  int32_t packed, units, rows, n_blocks, one_tile, splits, parts;
+};
+
+// The heads of a group share a tile when all their queries fit one block. The
+// key axis is split where blocks are too few: the count that leaves the last
+// block finished first, a block costing its key tiles and about four more
+// (start, epilogue), a split also the joining pass.
+Layout layout_of(const Problem& p) {
+  Layout L{};
+  L.packed = p.group > 1 && static_cast<int64_t>(p.group) * p.Sq <= 256;
+  L.units = L.packed ? p.Hk : p.Hq;
+  L.rows = L.packed ? p.group * p.Sq : p.Sq;
+  L.n_blocks = (L.rows + 255) / 256;
+  L.one_tile = L.rows <= kRows;
+  const int64_t ctas = static_cast<int64_t>(L.n_blocks) * L.units * p.B, sms = sm_count();
+  const int per_tile = L.one_tile ? 2 : 4;               // cost of a key tile: one slot's work, or both
+  double best = 1e300;
+  L.splits = 1;
+  for (int s = 1; s <= 64 && s <= std::max(1, p.nkt / 2); ++s) {
+    const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
+    const double t = waves * (per_tile * ((p.nkt + s - 1) / s) + 16.0) + (s > 1 ? 16.0 : 0.0);
+    if (t < best * 0.97) {
+      best = t;
+      L.splits = s;
+    }
+  }
+  L.parts = L.splits * (L.one_tile ? 2 : 1);
+  if (L.one_tile && p.nkt == 1) L.parts = 1;             // one key tile: the second slot has no work
+  return L;
+}
+
+struct Workspace {
+  size_t range, count, list, bad, copy, part_o, part_lse, total;
+};
+
+Workspace workspace_of(const Problem& p, const Layout& L) {
+  Workspace w{};
+  size_t off = kHeader;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t b = static_cast<size_t>(p.B), nkt = static_cast<size_t>(p.nkt), nb = static_cast<size_t>(L.n_blocks);
+  if (p.documents) {
+    w.range = take(b * nkt * sizeof(int4));
+    w.count = take(b * nb * sizeof(int32_t));
+    w.list = take(b * nb * nkt * sizeof(int32_t));
+  }
+  if (p.masked) {
+    w.bad = take(b * p.Hk * nkt * sizeof(uint4));
+    w.copy = take(b * p.Sk * p.Hk * kHeadDim * 2);
+  }
+  if (L.parts > 1) {
+    const size_t rows = b * p.Hq * p.Sq * static_cast<size_t>(L.parts);
+    w.part_o = take(rows * kHeadDim * sizeof(float));
+    w.part_lse = take(rows * sizeof(float));
+  }
+  w.total = off;
+  return w;
+}
+
+template <bool kCap, bool kBias>
+vsa_status launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mvc,
+                  cudaStream_t stream) {
+  const auto kernel = masked_fwd_kernel<kCap, kBias>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: shared memory", e);
+  kernel<<<a.n_blocks * a.units * a.p.B * a.splits, kThreads, sizeof(Smem), stream>>>(a, mk, mv, mvc);
+  return VSA_OK;
+}
+
+}  // namespace
+
+vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream) {
+  const dim3 grid(tiles(S), x->heads, B);
+  scan_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x->data), view_strides(x, B, S), S, c);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn: scan", e);
+}
+
+}  // namespace masked
+}  // namespace vsa
+
+using namespace vsa;
+using namespace vsa::masked;
+
+extern "C" {
+
+vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
+                                          int32_t Hk, size_t* bytes) {
+  if (!bytes) return VSA_ERR_INVALID_ARG;
+  Problem p;
+  vsa_mask m = mask ? *mask : vsa_mask{};
+  const int32_t documents = m.documents;
+  if (documents != 0 && documents != 1) return VSA_ERR_INVALID_ARG;
+  m.documents = 0;                                        // the tensors are not at hand yet
+  const vsa_status st = check(mask ? &m : nullptr, nullptr, B, Sq, Sk, Hq, Hk, &p);
+  if (st != VSA_OK) return st;
+  p.documents = documents;
+  p.masked |= documents;
+  *bytes = workspace_of(p, layout_of(p)).total;
+  return VSA_OK;
+}
+
+vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
+                               const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
+                               float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !k || !v || !out) return VSA_ERR_INVALID_ARG;
+  Args a{};
+  vsa_status st = check(mask, terms, B, Sq, Sk, q->heads, k->heads, &a.p);
+  if (st == VSA_OK) st = check_tensor(q, B, Sq, q->heads, false);
+  if (st == VSA_OK) st = check_tensor(k, B, Sk, k->heads, false);
+  if (st == VSA_OK) st = check_tensor(v, B, Sk, k->heads, false);
+  if (st == VSA_OK) st = check_tensor(out, B, Sq, q->heads, true);
+  if (st != VSA_OK) return st;
+  if (reinterpret_cast<uintptr_t>(lse) % 4) return VSA_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256) return VSA_ERR_INVALID_ARG;
+  const masked::Layout L = layout_of(a.p);
+  const Workspace w = workspace_of(a.p, L);
+  if (workspace_bytes < w.total) return VSA_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = static_cast<char*>(workspace);
+  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);   // this call's status word
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: cudaMemsetAsync", e);
+  if (B == 0 || Sq == 0) return VSA_OK;
+  if (!lse) return VSA_ERR_INVALID_ARG;
+  a.out = static_cast<uint16_t*>(out->data);
+  a.so = view_strides(out, B, Sq);
+  a.lse = lse;
+  const int row_blocks = static_cast<int>((static_cast<int64_t>(B) * q->heads * Sq + 7) / 8);
+  if (Sk == 0) {
+    empty_kernel<<<row_blocks, 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_fwd", e);
+  }
+  CUtensorMap mk, mv, mvc;
+  st = make_map(&mk, k, B, Sk);
+  if (st == VSA_OK) st = make_map(&mv, v, B, Sk);
+  if (st != VSA_OK) return st;
+  mvc = mv;
+  a.q = static_cast<const uint16_t*>(q->data);
+  a.sq = view_strides(q, B, Sq);
+  const Strides sk = view_strides(k, B, Sk), sv = view_strides(v, B, Sk);
+  a.k_h = sk.h != 0;
+  a.k_b = sk.b != 0;
+  a.v_h = sv.h != 0;
+  a.v_b = sv.b != 0;
+  a.packed = L.packed;
+  a.units = L.units;
+  a.rows = L.rows;
+  a.n_blocks = L.n_blocks;
+  a.one_tile = L.one_tile;
+  a.splits = L.splits;
+  a.parts = L.parts;
+  a.err = reinterpret_cast<int*>(ws);
+  if (L.parts > 1) {
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  }
+  if (a.p.documents) {
+    int4* range = reinterpret_cast<int4*>(ws + w.range);
+    a.count = reinterpret_cast<int32_t*>(ws + w.count);
+    a.list = reinterpret_cast<int32_t*>(ws + w.list);
+    range_kernel<<<dim3((a.p.nkt + 3) / 4, B), 128, 0, stream>>>(a.p, range);
+    plan_kernel<<<dim3(L.n_blocks, B), 256, 0, stream>>>(a.p, range, L.packed || L.one_tile ? 0 : kRows, L.n_blocks,
+                                                         reinterpret_cast<int32_t*>(ws + w.count),
+                                                         reinterpret_cast<int32_t*>(ws + w.list));
+  }
+  if (a.p.masked) {
+    a.clean_v = Clean{reinterpret_cast<uint4*>(ws + w.bad), reinterpret_cast<uint16_t*>(ws + w.copy)};
+    st = make_map(&mvc, a.clean_v.copy, B, Sk, k->heads);
+    if (st == VSA_OK) st = scan(v, B, Sk, a.clean_v, stream);
+    if (st != VSA_OK) return st;
+  }
+  const bool cap = a.p.cap > 0.0f, bias = a.p.slopes != nullptr;
+  st = cap ? (bias ? launch<true, true>(a, mk, mv, mvc, stream) : launch<true, false>(a, mk, mv, mvc, stream))
+           : (bias ? launch<false, true>(a, mk, mv, mvc, stream) : launch<false, false>(a, mk, mv, mvc, stream));
+  if (st != VSA_OK) return st;
+  if (L.parts > 1) join_kernel<<<row_blocks, 256, 0, stream>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_fwd", e);
+}
+
+vsa_status vsa_masked_attn_status(const void* workspace, cudaStream_t stream) {
+  if (!workspace) return VSA_ERR_INVALID_ARG;
+  int32_t status = 0;
+  cudaError_t e = cudaMemcpyAsync(&status, workspace, sizeof(status), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_status", e);
+  return static_cast<vsa_status>(status);
+}
+
+}  // extern "C"

@@ -1,0 +1,68 @@
+// Shared parts of the dense masked attention's forward and backward pass: the
+// workspace's plan of visible tiles, the copies of rows with infinities or NaN,
+// tensor maps and launch helpers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "vsa_internal.h"
+
+namespace vsa {
+namespace masked {
+
+constexpr int kRows = 128;                  // rows of a query or key tile
+constexpr size_t kHeader = 256;             // status word, count of failed calls
+constexpr uint32_t kTileBytes = 32768;      // 128 rows x 128 bf16: [d half][row][128 B], swizzled
+constexpr uint64_t kTimeoutNs = 4000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int kMaxPositions = 1 << 24;      // 32-bit floats hold every distance
+
+// A call's shape and mask as the kernels read them.
+struct Problem {
+  int32_t B, Hq, Hk, group;                 // group = Hq / Hk
+  int32_t Sq, Sk, off;                      // off = Sk - Sq: key position of query 0
+  int32_t nkt;                              // key tiles
+  int32_t causal, documents;
+  int32_t masked;                           // some pair may be invisible (rows may need clean copies)
+  const int32_t *doc_q, *doc_k;
+  int64_t doc_q_sb, doc_k_sb;
+  const int32_t* prefix;
+  const float* slopes;
+  float scale, cap;
+
+  // Last key position that query i sees by order.
+  __device__ __forceinline__ int limit(int b, int i) const {
+    if (!causal) return Sk - 1;
+    const int p = prefix ? prefix[b] : 0;
+    return min(max(i + off, p - 1), Sk - 1);
+  }
+};
+
+// Rows of a tensor that hold an infinity or NaN, per 128-row tile, and copies of
+// those tiles with such rows zeroed: a product over a tile multiplies masked
+// entries by 0, which must not meet one.
+struct Clean {
+  uint4* bad;                               // [B][heads][tiles] bit r: row r of the tile is bad; null: not scanned
+  uint16_t* copy;                           // [B][S][heads][128]; only tiles with a bad row are written
+};
+
+inline int tiles(int n) { return (n + kRows - 1) / kRows; }
+
+// cuTensorMapEncodeTiled over a view: boxes of 64 channels x 128 rows of one
+// head and batch entry, 128-byte swizzled, rows past S read as zero.
+vsa_status make_map(CUtensorMap* map, const vsa_view* v, int32_t B, int32_t S);
+vsa_status make_map(CUtensorMap* map, const uint16_t* copy, int32_t B, int32_t S, int32_t heads);
+
+// Validation shared by both passes; fills `p`.
+vsa_status check(const vsa_mask* mask, const vsa_mask_terms* t, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
+                 int32_t Hk, Problem* p);
+vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, bool output);
+
+// Scans x for rows with infinities or NaN (see Clean).
+vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream);
+
+int sm_count();
+
+}  // namespace masked
+}  // namespace vsa

@@ -24,6 +24,7 @@ COARSE_MEAN, COARSE_REWEIGHT = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 ROPE_ADJACENT, ROPE_HALVES = 0, 1
+MASK_FULL, MASK_CAUSAL = 0, 1
 TILE, HEAD_DIM = 64, 128
 MAX_NORM_WIDTH = 16384
 MAX_EXTRA_TOKENS = 64
@@ -65,6 +66,16 @@ class Rope(ctypes.Structure):
     _fields_ = [("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
                 ("pairing", ctypes.c_int32), ("theta", ctypes.c_double), ("scale_t", ctypes.c_double),
                 ("scale_h", ctypes.c_double), ("scale_w", ctypes.c_double)]
+
+
+class Mask(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("documents", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float)]
+
+
+class MaskTerms(ctypes.Structure):
+    _fields_ = [("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p), ("doc_q_stride_b", ctypes.c_int64),
+                ("doc_k_stride_b", ctypes.c_int64), ("prefix", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
 
 
 _lib = None
@@ -112,6 +123,11 @@ _SIGNATURES = {
     "vsa_layer_norm_fwd": (_I32, [_I32, _I64, _I32, _V, _P, _P, _I32, ctypes.c_float, _V, _P, _P, _P]),
     "vsa_layer_norm_bwd_workspace_size": (_I32, [_I32, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "vsa_layer_norm_bwd": (_I32, [_I32, _I64, _I32, _V, _V, _P, _I32, _P, _P, _V, _P, _P, _P, _SZ, _P]),
+    "vsa_masked_attn_workspace_size": (_I32, [ctypes.POINTER(Mask), _I32, _I32, _I32, _I32, _I32,
+                                              ctypes.POINTER(_SZ)]),
+    "vsa_masked_attn_fwd": (_I32, [ctypes.POINTER(Mask), ctypes.POINTER(MaskTerms), _I32, _I32, _I32, _V, _V, _V, _V,
+                                   _P, _P, _SZ, _P]),
+    "vsa_masked_attn_status": (_I32, [_P, _P]),
     "vsa_status_string": (ctypes.c_char_p, [_I32]),
     "vsa_version": (_I32, []),
     "vsa_last_error_detail": (ctypes.c_char_p, []),
@@ -544,6 +560,99 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, str
                                         _vector(dweight, N, "dweight", f32), _vector(dbias, N, "dbias", f32),
                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                         _stream_handle(stream)), "vsa_layer_norm_bwd")
+
+
+def make_mask(causal: bool = False, softcap: float = 0.0, scale: float = 0.0, documents: bool = False) -> Mask:
+    """Parameters of the dense masked attention; see vsa_mask in vsa.h. MaskedAttention sets `documents` by itself."""
+    return Mask(MASK_CAUSAL if causal else MASK_FULL, int(documents), scale, softcap)
+
+
+def _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes):
+    import torch
+    if (doc_q is None) != (doc_k is None) or bool(mask.documents) != (doc_q is not None):
+        raise ValueError("doc_q and doc_k come together, with a mask of documents")
+    t = MaskTerms()
+    for name, d, n in (("doc_q", doc_q, Sq), ("doc_k", doc_k, Sk)):
+        if d is None:
+            continue
+        if d.dtype != torch.int32 or tuple(d.shape) != (B, n) or (n > 1 and d.stride(1) != 1):
+            raise ValueError("%s must be int32 [B, %d], contiguous in its last dimension" % (name, n))
+        setattr(t, name, d.data_ptr())
+        setattr(t, name + "_stride_b", d.stride(0))
+    t.prefix = _vector(prefix, B, "prefix", (torch.int32,))
+    t.slopes = _vector(slopes, Hq, "slopes", (torch.float32,))
+    return t
+
+
+def _attn_shapes(q, k, v):
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[-1] != HEAD_DIM or k.shape[-1] != HEAD_DIM \
+            or q.shape[0] != k.shape[0] or k.shape[2] == 0 or q.shape[2] % k.shape[2]:
+        raise ValueError("q must be [B, Sq, Hq, 128], k and v [B, Sk, Hk, 128] with Hq a multiple of Hk")
+    return q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2]
+
+
+def masked_attn_workspace_size(mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int) -> int:
+    n = _SZ()
+    _check(lib().vsa_masked_attn_workspace_size(ctypes.byref(mask), B, Sq, Sk, Hq, Hk, ctypes.byref(n)),
+           "vsa_masked_attn_workspace_size")
+    return n.value
+
+
+def masked_attn_fwd(mask: Mask, q, k, v, out, lse, workspace, doc_q=None, doc_k=None, prefix=None, slopes=None,
+                    stream=None) -> None:
+    """vsa_masked_attn_fwd on torch tensors: bf16 q, out [B, Sq, Hq, 128], k, v [B, Sk, Hk, 128], lse float32
+    [B, Hq, Sq]; doc_q int32 [B, Sq] and doc_k int32 [B, Sk] (mask.documents), prefix int32 [B], slopes float32 [Hq]."""
+    import torch
+    B, Sq, Sk, Hq, Hk = _attn_shapes(q, k, v)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
+    with _On(q, k, v, out, lse, workspace, doc_q, doc_k, prefix, slopes):
+        _check(lib().vsa_masked_attn_fwd(ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v),
+                                         _view(out), _vector(lse, B * Hq * Sq, "lse", (torch.float32,)),
+                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                         _stream_handle(stream)), "vsa_masked_attn_fwd")
+
+
+def masked_attn_status(workspace, stream=None) -> int:
+    """Synchronises the stream; the status of the latest masked attention call on `workspace` (OK or ERR_TIMEOUT)."""
+    return lib().vsa_masked_attn_status(workspace.data_ptr(), _stream_handle(stream))
+
+
+class MaskedAttention:
+    """Dense attention of one shape and mask with its workspaces (allocated by the first call that needs them, so
+    run one call before a capture)."""
+
+    def __init__(self, mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int, device="cuda"):
+        self.shape, self.device = (B, Sq, Sk, Hq, Hk), device
+        self.masks = [Mask(mask.mode, d, mask.scale, mask.softcap) for d in (0, 1)]
+        for m in self.masks:
+            masked_attn_workspace_size(m, *self.shape)       # refuses a shape or mask at once
+        self.ws_fwd = {}
+
+    def _workspace(self, held, size, documents):
+        import torch
+        if documents not in held:
+            held[documents] = torch.empty(size(self.masks[documents], *self.shape), dtype=torch.uint8, device=self.device)
+        return held[documents]
+
+    def _own_shape(self, q, k, v):
+        if _attn_shapes(q, k, v) != self.shape:
+            raise ValueError("made for B, Sq, Sk, Hq, Hk = %s, called with %s" % (self.shape, _attn_shapes(q, k, v)))
+
+    def forward(self, q, k, v, out=None, lse=None, doc_q=None, doc_k=None, prefix=None, slopes=None, stream=None):
+        """masked_attn_fwd; returns (out, lse)."""
+        import torch
+        self._own_shape(q, k, v)
+        B, Sq, _, Hq, _ = self.shape
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        d = int(doc_q is not None)
+        masked_attn_fwd(self.masks[d], q, k, v, out, lse, self._workspace(self.ws_fwd, masked_attn_workspace_size, d),
+                        doc_q, doc_k, prefix, slopes, stream)
+        return out, lse
 
 
 def debug_inject_wait_timeout(timeout_ns):

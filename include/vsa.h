@@ -579,6 +579,78 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
                               const vsa_view* dx, float* dweight, float* dbias, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Dense attention with masks                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Which keys a query sees by order. Query i of Sq stands at key position
+ * i + Sk - Sq (the queries are the last Sq of the Sk positions). FULL: every
+ * key. CAUSAL: key j <= i + Sk - Sq, and every key j < prefix[b]. */
+typedef enum { VSA_MASK_FULL = 0, VSA_MASK_CAUSAL = 1 } vsa_mask_mode;
+
+/* Parameters of the dense call: scores s = scale <q, k>; with softcap c > 0
+ * s = c tanh(s / c); with slopes s -= slope[head] |i + Sk - Sq - j|; then the
+ * mask and the softmax.
+ *  scale    : <= 0 selects 1/sqrt(128).
+ *  softcap  : 0 (none) or > 0.
+ *  documents: 1 when doc_q and doc_k are given, else 0. */
+typedef struct {
+  int32_t mode;
+  int32_t documents;
+  float scale;
+  float softcap;
+} vsa_mask;
+
+/* The mask's and bias' tensors (device memory).
+ *  doc_q, doc_k : int32 [B, Sq] and [B, Sk], contiguous in the last dimension,
+ *                 batch strides in elements (0: shared). A pair is visible
+ *                 where the two are equal and not negative (negative: padding);
+ *                 both NULL unless vsa_mask.documents.
+ *  prefix       : int32 [B] or NULL (0); CAUSAL only. Any value: keys of
+ *                 [0, prefix) are visible to every query of the batch entry.
+ *  slopes       : float [Hq] or NULL (no bias). */
+typedef struct {
+  const int32_t* doc_q;
+  const int32_t* doc_k;
+  int64_t doc_q_stride_b, doc_k_stride_b;
+  const int32_t* prefix;
+  const float* slopes;
+} vsa_mask_terms;
+
+vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
+                                          int32_t Hk, size_t* bytes);
+
+/* vsa_masked_attn_fwd: exact attention of q [B, Sq, Hq, 128] over k, v
+ * [B, Sk, Hk, 128], query head h reading key head h / (Hq / Hk): the dense call
+ * for the cases that the sparse call refuses, for packed clips (documents), for
+ * padding and for causal video behind a bidirectional prefix; one query over a
+ * long cache splits the key axis over the GPU.
+ *  q, k, v, out : bf16; data and strides 16-byte multiples; Hq a multiple of
+ *                 Hk. Batch and head dimensions of inputs may be broadcast.
+ *  lse          : float [B, Hq, Sq] out, contiguous: natural log of the sum of
+ *                 exp(s) over the visible keys; -inf for a row that sees none,
+ *                 whose output is 0.
+ *  workspace    : vsa_masked_attn_workspace_size bytes, 256-byte aligned: a
+ *                 256-byte header with this call's status word (see
+ *                 vsa_masked_attn_status), the visible tiles, partial results;
+ *                 written before it is read. Two calls that may overlap need
+ *                 two workspaces.
+ * Masked keys do not reach a row whatever they hold: infinities and NaN in
+ * their k and v change nothing. A row that sees a key with an infinity or NaN
+ * in its v is NaN throughout when the call masks anything.
+ * Scores, softmax statistics and sums are 32-bit; the probabilities enter the
+ * second tensor-core product as bf16 (the output's own rounding). B, Sq,
+ * Sk >= 0; at most 65535 batch entries and heads, and 2^24 positions
+ * (UNSUPPORTED beyond, and for an input whose sequence stride is 0). */
+vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
+                               const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
+                               float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Synchronises `stream` and reads the status word that the latest
+ * vsa_masked_attn_fwd or vsa_masked_attn_bwd left in `workspace`: VSA_OK or
+ * VSA_ERR_TIMEOUT (a bounded wait ran out; the outputs are incomplete). */
+vsa_status vsa_masked_attn_status(const void* workspace, cudaStream_t stream);
+
 const char* vsa_status_string(vsa_status status);
 
 /* Text of the most recent VSA_ERR_CUDA returned on the calling thread (the
