@@ -210,28 +210,46 @@ __device__ __forceinline__ Range doc_range(const int32_t* ids, int i0, int n) {
   return r;
 }
 
-// Document ranges of the key tiles: [B][nkt].
-__global__ void __launch_bounds__(128) range_kernel(const __grid_constant__ Problem p, int4* __restrict__ range) {
+// Document ranges of the tiles of ids [B, S]: [B][tiles].
+__global__ void __launch_bounds__(128)
+range_kernel(const int32_t* __restrict__ ids, int64_t sb, int S, int n_tiles, int4* __restrict__ range) {
   const int tile = blockIdx.x * 4 + (threadIdx.x >> 5), b = blockIdx.y;
-  if (tile >= p.nkt) return;
-  const Range r = doc_range(p.doc_k + b * p.doc_k_sb, tile * kRows, min(kRows, p.Sk - tile * kRows));
-  if ((threadIdx.x & 31) == 0) range[static_cast<size_t>(b) * p.nkt + tile] = make_int4(r.lo, r.hi, r.pad, 0);
+  if (tile >= n_tiles) return;
+  const Range r = doc_range(ids + b * sb, tile * kRows, min(kRows, S - tile * kRows));
+  if ((threadIdx.x & 31) == 0) range[static_cast<size_t>(b) * n_tiles + tile] = make_int4(r.lo, r.hi, r.pad, 0);
 }
 
-// Key tiles that some row of a query block sees, ascending, with a flag per
-// query tile where its documents do not cover the whole tile pair. One block per
-// (query block, batch entry).
-constexpr int kPartial0 = 1 << 29, kPartial1 = 1 << 30, kTileMask = kPartial0 - 1;
+__device__ __forceinline__ bool meet(int4 a, int4 b) { return a.x <= b.y && b.x <= a.y; }
+__device__ __forceinline__ bool same(int4 a, int4 b) { return a.x == a.y && b.x == b.y && a.x == b.x && !a.z && !b.z; }
+
+// Appends the records (>= 0) of a block's 256 threads to `out` from `total`, in
+// thread order; returns the new total.
+__device__ __forceinline__ int append(int rec, int total, int32_t* out, int* n_warp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t vote = __ballot_sync(0xffffffffu, rec >= 0);
+  if (lane == 0) n_warp[warp] = __popc(vote);
+  __syncthreads();
+  int at = total;
+  for (int w = 0; w < 8; ++w) {
+    at += w < warp ? n_warp[w] : 0;
+    total += n_warp[w];
+  }
+  if (rec >= 0) out[at + __popc(vote & ((1u << lane) - 1u))] = rec;
+  __syncthreads();
+  return total;
+}
+
+// Key tiles that some row of a query block sees, ascending. One block per (query
+// block, batch entry).
 __global__ void __launch_bounds__(256)
-plan_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, int rows_per_tile, int n_blocks,
+plan_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, PlanRows rows, int n_blocks,
             int32_t* __restrict__ count, int32_t* __restrict__ list) {
   const int qb = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int4 q[2];
   __shared__ int n_warp[8];
-  // rows_per_tile = 0: both tiles hold all queries
   if (warp < 2) {
-    const int i0 = rows_per_tile ? (qb * 2 + warp) * rows_per_tile : 0;
-    const int n = rows_per_tile ? max(0, min(rows_per_tile, p.Sq - i0)) : p.Sq;
+    const int i0 = rows == kPlanAll ? 0 : rows == kPlanPairs ? (qb * 2 + warp) * kRows : qb * kRows;
+    const int n = rows == kPlanAll ? p.Sq : max(0, min(kRows, p.Sq - i0));
     const Range r = doc_range(p.doc_q + b * p.doc_q_sb, min(i0, p.Sq), n);
     if (lane == 0) q[warp] = make_int4(r.lo, r.hi, r.pad, n > 0 ? p.limit(b, i0 + n - 1) : -1);
   }
@@ -246,24 +264,37 @@ plan_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, i
       bool any = false;
       int flags = 0;
       for (int t = 0; t < 2; ++t) {
-        const int4 r = q[t];
-        any |= k.x <= r.y && r.x <= k.y && kt * kRows <= r.w;
-        if (!(k.x == k.y && r.x == r.y && k.x == r.x && !k.z && !r.z)) flags |= t ? kPartial1 : kPartial0;
+        any |= meet(k, q[t]) && kt * kRows <= q[t].w;
+        if (!same(k, q[t])) flags |= t ? kPartial1 : kPartial0;
       }
       if (any) rec = kt | flags;
     }
-    const uint32_t vote = __ballot_sync(0xffffffffu, rec >= 0);
-    if (lane == 0) n_warp[warp] = __popc(vote);
-    __syncthreads();
-    int at = total;
-    for (int w = 0; w < 8; ++w) {
-      at += w < warp ? n_warp[w] : 0;
-      total += n_warp[w];
-    }
-    if (rec >= 0) out[at + __popc(vote & ((1u << lane) - 1u))] = rec;
-    __syncthreads();
+    total = append(rec, total, out, n_warp);
   }
   if (threadIdx.x == 0) count[static_cast<size_t>(b) * n_blocks + qb] = total;
+}
+
+// Query tiles that see some key of a key tile, ascending. One block per (key
+// tile, batch entry).
+__global__ void __launch_bounds__(256)
+plan_keys_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, const int4* __restrict__ range_q,
+                 int nqt, int32_t* __restrict__ count, int32_t* __restrict__ list) {
+  const int kt = blockIdx.x, b = blockIdx.y;
+  __shared__ int n_warp[8];
+  const int4 k = range[static_cast<size_t>(b) * p.nkt + kt];
+  int total = 0;
+  int32_t* out = list + (static_cast<size_t>(b) * p.nkt + kt) * nqt;
+  for (int t0 = 0; t0 < nqt; t0 += 256) {
+    const int qt = t0 + threadIdx.x;
+    int rec = -1;
+    if (qt < nqt) {
+      const int4 q = range_q[static_cast<size_t>(b) * nqt + qt];
+      if (meet(k, q) && kt * kRows <= p.limit(b, min((qt + 1) * kRows, p.Sq) - 1))
+        rec = qt | (same(k, q) ? 0 : kPartial0);
+    }
+    total = append(rec, total, out, n_warp);
+  }
+  if (threadIdx.x == 0) count[static_cast<size_t>(b) * p.nkt + kt] = total;
 }
 
 // --------------------------------------------------------------- main kernel
@@ -788,6 +819,18 @@ vsa_status launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, c
 
 }  // namespace
 
+void plan(const Problem& p, PlanRows rows, int n_blocks, int4* range, int32_t* count, int32_t* list,
+          cudaStream_t stream) {
+  range_kernel<<<dim3((p.nkt + 3) / 4, p.B), 128, 0, stream>>>(p.doc_k, p.doc_k_sb, p.Sk, p.nkt, range);
+  plan_kernel<<<dim3(n_blocks, p.B), 256, 0, stream>>>(p, range, rows, n_blocks, count, list);
+}
+
+void plan_keys(const Problem& p, const int4* range, int4* range_q, int32_t* count, int32_t* list, cudaStream_t stream) {
+  const int nqt = tiles(p.Sq);
+  range_kernel<<<dim3((nqt + 3) / 4, p.B), 128, 0, stream>>>(p.doc_q, p.doc_q_sb, p.Sq, nqt, range_q);
+  plan_keys_kernel<<<dim3(p.nkt, p.B), 256, 0, stream>>>(p, range, range_q, nqt, count, list);
+}
+
 vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream) {
   const dim3 grid(tiles(S), x->heads, B);
   scan_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x->data), view_strides(x, B, S), S, c);
@@ -877,10 +920,8 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
     int4* range = reinterpret_cast<int4*>(ws + w.range);
     a.count = reinterpret_cast<int32_t*>(ws + w.count);
     a.list = reinterpret_cast<int32_t*>(ws + w.list);
-    range_kernel<<<dim3((a.p.nkt + 3) / 4, B), 128, 0, stream>>>(a.p, range);
-    plan_kernel<<<dim3(L.n_blocks, B), 256, 0, stream>>>(a.p, range, L.packed || L.one_tile ? 0 : kRows, L.n_blocks,
-                                                         reinterpret_cast<int32_t*>(ws + w.count),
-                                                         reinterpret_cast<int32_t*>(ws + w.list));
+    plan(a.p, L.packed || L.one_tile ? kPlanAll : kPlanPairs, L.n_blocks, range,
+         reinterpret_cast<int32_t*>(ws + w.count), reinterpret_cast<int32_t*>(ws + w.list), stream);
   }
   if (a.p.masked) {
     a.clean_v = Clean{reinterpret_cast<uint4*>(ws + w.bad), reinterpret_cast<uint16_t*>(ws + w.copy)};

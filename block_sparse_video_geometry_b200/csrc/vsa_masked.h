@@ -62,6 +62,19 @@ vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, 
 // Scans x for rows with infinities or NaN (see Clean).
 vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream);
 
+// Records of a list of visible tiles: the tile, and where documents hide part of
+// it from query tile 0 or 1 of the block.
+constexpr int kPartial0 = 1 << 29, kPartial1 = 1 << 30, kTileMask = kPartial0 - 1;
+
+// Visible key tiles of query blocks (documents only). `range`: [B][nkt] scratch;
+// count [B][n_blocks], list [B][n_blocks][nkt] out.
+enum PlanRows { kPlanPairs, kPlanAll, kPlanSingle };   // two tiles a block, all queries in one block, one tile a block
+void plan(const Problem& p, PlanRows rows, int n_blocks, int4* range, int32_t* count, int32_t* list,
+          cudaStream_t stream);
+// Visible query tiles of key tiles: range_q [B][nqt] scratch, `range` filled by
+// plan(); count [B][nkt], list [B][nkt][nqt] out.
+void plan_keys(const Problem& p, const int4* range, int4* range_q, int32_t* count, int32_t* list, cudaStream_t stream);
+
 int sm_count();
 
 }  // namespace masked

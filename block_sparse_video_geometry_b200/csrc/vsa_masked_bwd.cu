@@ -1,0 +1,853 @@
+// Dense attention with capped scores, a distance bias, document and prefix
+// masks: backward pass.
+//
+// Mathematics: P = exp(s - lse) from the forward's lse, D = sum_d dO O,
+// dS = P (dO V^T - D) (times 1 - tanh^2 under a cap), dV = P^T dO,
+// dK = scale dS^T Q, dQ = scale dS K.
+//
+// Bound: tensor pipe. The formulas need five products per visible pair; the two
+// kernels here run seven (S and dO V^T once per side), so that every sum stays
+// in one block's TMEM in a fixed order: no atomics, equal inputs give equal bits,
+// and dQ needs no 32-bit traffic through memory.
+//
+// Design.
+//  * dkv_kernel: a block owns 128 keys of a key head (TMEM lane = key) and walks
+//    the query tiles that see them, for every query head of the group:
+//    S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and
+//    dS^T (bf16) as A operands in TMEM over their own 32-bit columns. Two warps
+//    issue products, one S^T and dV, one dP^T and dK; each rewrites its columns
+//    behind its own accumulation, in issue order. Eight warps (two per lane
+//    quadrant, 64 query columns each) turn S^T into P^T while dP^T and dK run, and
+//    dP^T into dS^T while dV and the next S^T run.
+//  * dq_kernel: a block owns 128 queries of a head (lane = query) and walks the
+//    key tiles: S = Q K^T, dP = dO V^T, dQ += dS K, dS in two buffers of its own.
+// Both read their tiles by TMA, two stages each. D and lse in log2 units come from
+// prepare_kernel; rows without visible keys get lse = +inf there, so that P = 0.
+// Every wait is bounded (see vsa_masked_attn_status).
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "sm100.cuh"
+#include "vec.cuh"
+#include "vsa_masked.h"
+
+namespace vsa {
+namespace masked {
+namespace {
+
+using namespace sm100;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------ prepare
+// D and lse2 of every row, [B][Hq][nqt * 128]; rows past Sq: D = 0, lse2 = inf.
+// 16 lanes per row. HBM bound: out and dout read once.
+struct PrepArgs {
+  const uint16_t *out, *dout;
+  Strides so, sd;
+  const float* lse;
+  int32_t B, Hq, Sq, padded;
+  float *lse2, *delta;
+};
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+    s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepArgs a) {
+  const int i = blockIdx.x * 16 + (threadIdx.x >> 4), h = blockIdx.y, c = threadIdx.x & 15;
+  const int64_t b = blockIdx.z;
+  float d = 0.0f, l = INFINITY;
+  if (i < a.Sq) {
+    const uint4 o = *reinterpret_cast<const uint4*>(a.out + b * a.so.b + i * a.so.s + h * a.so.h + c * 8);
+    const uint4 g = *reinterpret_cast<const uint4*>(a.dout + b * a.sd.b + i * a.sd.s + h * a.sd.h + c * 8);
+    d = dot8(o, g);
+    l = a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Sq + i] * kLog2e;
+    if (l == -INFINITY) l = INFINITY;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (c == 0 && i < a.padded) {
+    const size_t at = (static_cast<size_t>(b) * a.Hq + h) * a.padded + i;
+    a.delta[at] = d;
+    a.lse2[at] = l;
+  }
+}
+
+// ------------------------------------------------------------------- shared
+constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpX = 9, kWarpY = 10;     // warps 0-7: elementwise work
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdescKK = idesc_bf16_f32(128, 128, 0, 0);   // A and B K-major
+constexpr uint32_t kIdescKM = idesc_bf16_f32(128, 128, 0, 1);   // A K-major (TMEM), B MN-major
+
+struct Smem {
+  uint8_t own[2][kTileBytes];                // dkv: K, V; dq: Q, dO
+  uint8_t ring_a[2][kTileBytes];             // dkv: Q; dq: K
+  uint8_t ring_b[2][kTileBytes];             // dkv: dO; dq: V
+  float lse2[2][kRows], delta[2][kRows];     // dkv: of the Q stage's rows
+  uint64_t own_full, a_full[2], a_empty[2], b_full[2], b_empty[2];
+  uint64_t s_full, s_done, dp_full, ds_done, acc[2], drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Args {
+  Problem p;
+  Clean clean_a, clean_b;                    // of ring_a's and ring_b's tensors, or null
+  int32_t a_h, a_b, b_h, b_b;                // 1: the map has that dimension, 0: broadcast
+  int32_t o1_h, o1_b, o2_h, o2_b;            // the same of the block's own two tensors
+  const float *lse2, *delta;                 // [B][Hq][padded]
+  int32_t padded, nqt;
+  const int32_t *count, *list;               // visible tiles of the other side, or null
+  uint16_t *out1, *out2;                     // dkv: dk, dv; dq: dq
+  Strides so1, so2;
+  int* err;
+};
+
+__device__ __forceinline__ bool bounded_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
+  const bool ok = mbar_wait(smem_u32(&bar), parity, &sm.abort, kTimeoutNs);
+  if (!ok) {
+    if (atomicExch(err, VSA_ERR_TIMEOUT) == 0) atomicAdd(err + 1, 1);
+    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+  }
+  return ok;
+}
+__device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, bounded_wait(sm, bar, parity, err));
+}
+
+// D (+)= A B^T over 128 channels, both K-major tiles in shared memory (32 B per
+// K step inside a swizzled row, d halves 16 KB apart).
+__device__ __forceinline__ void product_kk(uint32_t d, const uint8_t* x, const uint8_t* y) {
+  const uint64_t xd = smem_desc_sw128(smem_u32(x), 16, 1024), yd = smem_desc_sw128(smem_u32(y), 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_ss(d, xd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, yd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kIdescKK,
+            kk > 0 ? 1u : 0u);
+}
+
+// D += A B over 128 rows of B (MN-major: 16 rows = 2 KB per K step, d halves 16 KB
+// apart); A in TMEM as bf16 pairs, 8 columns per K step, rows 64-127 at `half`.
+__device__ __forceinline__ void product_km(uint32_t d, uint32_t x, int half, const uint8_t* y, bool add) {
+  const uint64_t yd = smem_desc_sw128(smem_u32(y), 16384, 1024);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_ts(d, x + (kk >> 2) * half + (kk & 3) * 8, yd + kk * (2048 >> 4), kIdescKM, add || kk > 0 ? 1u : 0u);
+}
+
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int row, int h, int b, uint64_t& bar) {
+  const uint32_t d = smem_u32(dst), f = smem_u32(&bar);
+  tma_load_4d(d, map, 0, row, h, b, f);
+  tma_load_4d(d + kTileBytes / 2, map, 64, row, h, b, f);
+}
+
+__device__ __forceinline__ bool any(uint4 m) { return m.x | m.y | m.z | m.w; }
+
+// 64 columns of 32-bit sums times `f` as bf16 into a row (or zeros).
+__device__ __forceinline__ void write_half_row(uint32_t taddr, bool have, float f, bool live, uint16_t* row) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    float o[32];
+    __syncwarp();
+    if (have) {
+      tmem_ld32x32f(taddr + 32 * c, o);
+      tmem_wait_ld32(o);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 32; ++u) o[u] = 0.0f;
+    }
+    if (live) {
+      uint4* dst = reinterpret_cast<uint4*>(row + 32 * c);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        dst[u] = make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
+                            pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f),
+                            pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
+    }
+  }
+}
+
+template <class Init>
+__device__ __forceinline__ uint32_t set_up(Smem& sm, Init init) {
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&sm.own_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.a_full[i]), 1);
+      mbar_init(smem_u32(&sm.a_empty[i]), 1);
+      mbar_init(smem_u32(&sm.b_full[i]), 1);
+      mbar_init(smem_u32(&sm.acc[i]), 1);
+      mbar_init(smem_u32(&sm.drain[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.s_full), 1);
+    mbar_init(smem_u32(&sm.s_done), 8);
+    mbar_init(smem_u32(&sm.dp_full), 1);
+    mbar_init(smem_u32(&sm.ds_done), 8);
+    init();
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if ((threadIdx.x >> 5) == kWarpX) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return sm.tmem_base;
+}
+
+__device__ __forceinline__ void finish(uint32_t tmem) {
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == kWarpX) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Scores of 32 columns in place -> P against `ref` (one value, or one per
+// column), and into `w` P times the cap's derivative.
+template <bool kCap, bool kBias, class Ref>
+__device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const Problem& p, float c, float slope,
+                                              float d0, float dir, Ref ref) {
+  const float cap2 = kCap ? p.cap * kLog2e : 0.0f, in2 = kCap ? 2.0f * c / p.cap : 0.0f;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    float s = x[u], t = 0.0f;
+    if constexpr (kCap) {
+      t = 1.0f + __fdividef(-2.0f, 1.0f + ex2_approx(s * in2));
+      s = cap2 * t;
+    } else if constexpr (kBias) {
+      s *= c;
+    }
+    if constexpr (kBias) s = fmaf(-slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), s);
+    const float e = ex2_approx(kCap || kBias ? s - ref(u) : fmaf(s, c, -ref(u)));
+    x[u] = e;
+    w[u] = kCap ? e * fmaf(-t, t, 1.0f) : e;
+  }
+}
+
+// ----------------------------------------------------------------- dK and dV
+template <bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
+           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
+           const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_qc,
+           const __grid_constant__ CUtensorMap map_oc) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) atomicExch(a.err, VSA_ERR_UNSUPPORTED);
+    return;
+  }
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const Problem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = p.Hk * p.B, kt = blockIdx.x / per;       // early key tiles, the longest under a causal mask, first
+  const int hk = blockIdx.x % per % p.Hk, b = blockIdx.x % per / p.Hk;
+  const int k0 = kt * kRows;
+  const uint32_t tmem = set_up(sm, [&] {
+    mbar_init(smem_u32(&sm.b_empty[0]), 2);                // dO is read by dP^T and by dV
+    mbar_init(smem_u32(&sm.b_empty[1]), 2);
+  });
+  constexpr uint32_t kColS = 0, kColDp = 128, kColDv = 256, kColDk = 384;
+
+  // query tiles: `len` of them for each query head of the group
+  const size_t row = static_cast<size_t>(b) * p.nkt + kt;
+  const int prefix = p.causal && p.prefix ? p.prefix[b] : 0;
+  int first = 0, len = 0;
+  if (a.count) {
+    len = a.count[row];
+  } else {
+    if (p.causal && prefix <= k0) first = max(0, k0 - p.off) / kRows;
+    len = max(0, a.nqt - first);
+  }
+  const int32_t* list = a.count ? a.list + row * a.nqt : nullptr;
+  const int n = len * p.group;
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      bool ok = true;
+      mbar_arrive_expect_tx(smem_u32(&sm.own_full), 2 * kTileBytes);
+      load_tile(sm.own[0], &map_k, k0, a.o1_h ? hk : 0, a.o1_b ? b : 0, sm.own_full);
+      load_tile(sm.own[1], &map_v, k0, a.o2_h ? hk : 0, a.o2_b ? b : 0, sm.own_full);
+      int j = 0;
+      for (; ok && j < n; ++j) {
+        const int st = j & 1, g = j / len, idx = j - g * len, h = hk * p.group + g;
+        const int qt = (list ? list[idx] : first + idx) & kTileMask;
+        const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
+        if (j >= 2 && !(ok = bounded_wait(sm, sm.a_empty[st], (j / 2 - 1) & 1, a.err))) break;
+        const bool bad_q = a.clean_a.bad && any(a.clean_a.bad[tile]);
+        mbar_arrive_expect_tx(smem_u32(&sm.a_full[st]), kTileBytes + 2 * kRows * 4);
+        load_tile(sm.ring_a[st], bad_q ? &map_qc : &map_q, qt * kRows, bad_q || a.a_h ? h : 0, bad_q || a.a_b ? b : 0,
+                  sm.a_full[st]);
+        const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + qt * kRows;
+        bulk_load(smem_u32(sm.lse2[st]), a.lse2 + at, kRows * 4, smem_u32(&sm.a_full[st]));
+        bulk_load(smem_u32(sm.delta[st]), a.delta + at, kRows * 4, smem_u32(&sm.a_full[st]));
+        if (j >= 2 && !(ok = bounded_wait(sm, sm.b_empty[st], (j / 2 - 1) & 1, a.err))) {
+          ++j;                                             // its Q is in flight; its dO is not
+          break;
+        }
+        const bool bad_o = a.clean_b.bad && any(a.clean_b.bad[tile]);
+        mbar_arrive_expect_tx(smem_u32(&sm.b_full[st]), kTileBytes);
+        load_tile(sm.ring_b[st], bad_o ? &map_oc : &map_o, qt * kRows, bad_o || a.b_h ? h : 0, bad_o || a.b_b ? b : 0,
+                  sm.b_full[st]);
+      }
+      if (!ok || n == 0) {                                 // every issued copy lands before the block exits
+        mbar_wait(smem_u32(&sm.own_full), 0, nullptr, kDrainNs);
+        for (int i = max(0, j - 3); i < j; ++i) {
+          mbar_wait(smem_u32(&sm.a_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+          mbar_wait(smem_u32(&sm.b_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpX || warp == kWarpY) {
+    const bool x = warp == kWarpX;
+    if (lane == 0 && n > 0) {
+      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
+      uint64_t* src_full = x ? sm.a_full : sm.b_full;      // S^T reads Q, dP^T reads dO
+      auto scores = [&](int j) {
+        const int st = j & 1;
+        if (!bounded_wait(sm, src_full[st], (j / 2) & 1, a.err)) return false;
+        tc_fence_after();
+        product_kk(tmem + (x ? kColS : kColDp), sm.own[x ? 0 : 1], x ? sm.ring_a[st] : sm.ring_b[st]);
+        umma_commit(smem_u32(x ? &sm.s_full : &sm.dp_full));
+        if (!x) umma_commit(smem_u32(&sm.b_empty[st]));
+        return true;
+      };
+      if (ok) ok = scores(0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int st = j & 1;
+        uint64_t* other_full = x ? sm.b_full : sm.a_full;  // dV reads dO, dK reads Q
+        if (!(ok = bounded_wait(sm, other_full[st], (j / 2) & 1, a.err))) break;
+        if (!(ok = bounded_wait(sm, x ? sm.s_done : sm.ds_done, j & 1, a.err))) break;
+        tc_fence_after();
+        product_km(tmem + (x ? kColDv : kColDk), tmem + (x ? kColS : kColDp), 64, x ? sm.ring_b[st] : sm.ring_a[st],
+                   j > 0);
+        umma_commit(smem_u32(x ? &sm.b_empty[st] : &sm.a_empty[st]));
+        if (j + 1 < n) ok = scores(j + 1);
+        else umma_commit(smem_u32(&sm.acc[x ? 0 : 1]));
+      }
+      if (!ok) {
+        umma_commit(smem_u32(&sm.drain[x ? 0 : 1]));
+        mbar_wait(smem_u32(&sm.drain[x ? 0 : 1]), 0, nullptr, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    const int quad = warp & 3, half = warp >> 2;           // 64 query columns per warp
+    const int key = k0 + quad * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t ts = lane_addr + kColS + 64 * half, tp = lane_addr + kColDp + 64 * half;
+    const float c = p.scale * kLog2e;
+    // first query that sees this key by order
+    const int i_min = !p.causal || key < prefix ? INT32_MIN : key - p.off;
+    const int doc = p.documents && key < p.Sk ? p.doc_k[b * p.doc_k_sb + key] : -1;
+    const int32_t* dq = p.documents ? p.doc_q + b * p.doc_q_sb : nullptr;
+    bool ok = true;
+    int j = 0;
+    for (; j < n; ++j) {
+      const int st = j & 1, g = j / len, idx = j - g * len, h = hk * p.group + g;
+      const int rec = list ? list[idx] : first + idx;
+      const int qt = rec & kTileMask, q0 = qt * kRows;
+      const bool part_doc = rec & kPartial0;
+      const bool partial = part_doc || (p.causal && prefix < k0 + kRows && q0 + p.off < k0 + kRows - 1);
+      const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
+      uint4 bm = make_uint4(0, 0, 0, 0);
+      if (a.clean_a.bad) {
+        const uint4 m1 = a.clean_a.bad[tile], m2 = a.clean_b.bad[tile];
+        bm = make_uint4(m1.x | m2.x, m1.y | m2.y, m1.z | m2.z, m1.w | m2.w);
+      }
+      const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+      if (!(ok = warp_wait(sm, sm.a_full[st], (j / 2) & 1, a.err))) break;     // lse and D
+      if (!(ok = warp_wait(sm, sm.s_full, j & 1, a.err))) break;
+      tc_fence_after();
+      // visible columns of chunk q2 as a bit mask; only where some pair is hidden
+      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      if (partial) {
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const int i0 = q0 + 64 * half + 32 * q2;
+          uint32_t m = 0;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) m |= (i0 + u >= i_min ? 1u : 0u) << u;
+          if (part_doc) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const int d = __ldg(dq + min(i0 + u, p.Sq - 1));
+              if (!(d == doc && d >= 0)) m &= ~(1u << u);
+            }
+          }
+          see[q2] = m;
+        }
+      }
+      const uint32_t bad[2] = {half ? bm.z : bm.x, half ? bm.w : bm.y};
+      float w[2][32];
+#pragma unroll
+      for (int q2 = 0; q2 < 2; ++q2) {
+        float x[32];
+        tmem_ld32x32f(ts + 32 * q2, x);
+        tmem_wait_ld32(x);
+        const float* lse = sm.lse2[st] + 64 * half + 32 * q2;
+        const float d0 = static_cast<float>(q0 + p.off + 64 * half + 32 * q2 - key);
+        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, 1.0f, [&](int u) { return lse[u]; });
+        if (partial) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
+        }
+        if (bad[q2]) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if ((bad[q2] & see[q2]) >> u & 1u) x[u] = w[q2][u] = NAN;
+        }
+        uint32_t pw[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+        // queries 64 half + [32 q2, + 32): 16 columns of pairs, in this warp's own half of the scores
+        tmem_st32x16(ts + 16 * q2, pw);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.s_done));
+      if (!(ok = warp_wait(sm, sm.dp_full, j & 1, a.err))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q2 = 0; q2 < 2; ++q2) {
+        float x[32];
+        tmem_ld32x32f(tp + 32 * q2, x);
+        tmem_wait_ld32(x);
+        const float* dl = sm.delta[st] + 64 * half + 32 * q2;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) x[u] = w[q2][u] * (x[u] - dl[u]);
+        if (partial) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
+        }
+        uint32_t pw[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+        tmem_st32x16(tp + 16 * q2, pw);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done));
+    }
+    if (ok && n > 0) {
+      ok = warp_wait(sm, sm.acc[0], 0, a.err) && warp_wait(sm, sm.acc[1], 0, a.err);
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool live = key < p.Sk;
+      const int64_t kk = live ? key : 0;
+      write_half_row(lane_addr + kColDk + 64 * half, n > 0, p.scale, live,
+                     a.out1 + b * a.so1.b + kk * a.so1.s + hk * a.so1.h + 64 * half);
+      write_half_row(lane_addr + kColDv + 64 * half, n > 0, 1.0f, live,
+                     a.out2 + b * a.so2.b + kk * a.so2.s + hk * a.so2.h + 64 * half);
+    }
+  }
+  finish(tmem);
+}
+
+// ------------------------------------------------------------------------ dQ
+template <bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_q,
+          const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_k,
+          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kc) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) atomicExch(a.err, VSA_ERR_UNSUPPORTED);
+    return;
+  }
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const Problem& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = p.Hq * p.B, qt = a.nqt - 1 - blockIdx.x / per;   // late query tiles first
+  const int h = blockIdx.x % per % p.Hq, b = blockIdx.x % per / p.Hq, hk = h / p.group;
+  const int q0 = qt * kRows;
+  const uint32_t tmem = set_up(sm, [&] {
+    mbar_init(smem_u32(&sm.b_empty[0]), 1);
+    mbar_init(smem_u32(&sm.b_empty[1]), 1);
+  });
+  constexpr uint32_t kColS = 0, kColDp = 128, kColDq = 256, kColDs = 384;   // dS: two buffers of 64 columns
+
+  const size_t row = static_cast<size_t>(b) * a.nqt + qt;
+  const int n = a.count ? a.count[row] : max(0, p.limit(b, min(q0 + kRows, p.Sq) - 1) + kRows) / kRows;
+  const int32_t* list = a.count ? a.list + row * p.nkt : nullptr;
+  const uint4* bad = a.clean_a.bad ? a.clean_a.bad + (static_cast<size_t>(b) * p.Hk + hk) * p.nkt : nullptr;
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      bool ok = true;
+      mbar_arrive_expect_tx(smem_u32(&sm.own_full), 2 * kTileBytes);
+      load_tile(sm.own[0], &map_q, q0, a.o1_h ? h : 0, a.o1_b ? b : 0, sm.own_full);
+      load_tile(sm.own[1], &map_o, q0, a.o2_h ? h : 0, a.o2_b ? b : 0, sm.own_full);
+      int j = 0;
+      for (; ok && j < n; ++j) {
+        const int st = j & 1, kt = (list ? list[j] : j) & kTileMask;
+        if (j >= 2 && !(ok = bounded_wait(sm, sm.b_empty[st], (j / 2 - 1) & 1, a.err))) break;
+        mbar_arrive_expect_tx(smem_u32(&sm.b_full[st]), kTileBytes);
+        load_tile(sm.ring_b[st], &map_v, kt * kRows, a.b_h ? hk : 0, a.b_b ? b : 0, sm.b_full[st]);
+        if (j >= 2 && !(ok = bounded_wait(sm, sm.a_empty[st], (j / 2 - 1) & 1, a.err))) {
+          ++j;
+          break;
+        }
+        const bool bad_k = bad && any(bad[kt]);
+        mbar_arrive_expect_tx(smem_u32(&sm.a_full[st]), kTileBytes);
+        load_tile(sm.ring_a[st], bad_k ? &map_kc : &map_k, kt * kRows, bad_k || a.a_h ? hk : 0,
+                  bad_k || a.a_b ? b : 0, sm.a_full[st]);
+      }
+      if (!ok || n == 0) {
+        mbar_wait(smem_u32(&sm.own_full), 0, nullptr, kDrainNs);
+        for (int i = max(0, j - 3); i < j; ++i) {
+          mbar_wait(smem_u32(&sm.a_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+          mbar_wait(smem_u32(&sm.b_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpX) {
+    if (lane == 0 && n > 0) {
+      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = bounded_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        if (j > 0 && !(ok = bounded_wait(sm, sm.s_done, (j - 1) & 1, a.err))) break;    // S(j - 1) was read
+        tc_fence_after();
+        product_kk(tmem + kColS, sm.own[0], sm.ring_a[j & 1]);
+        umma_commit(smem_u32(&sm.s_full));
+      }
+      if (!ok) {
+        umma_commit(smem_u32(&sm.drain[0]));
+        mbar_wait(smem_u32(&sm.drain[0]), 0, nullptr, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpY) {
+    if (lane == 0 && n > 0) {
+      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
+      auto dp = [&](int j) {
+        if (!bounded_wait(sm, sm.b_full[j & 1], (j / 2) & 1, a.err)) return false;
+        tc_fence_after();
+        product_kk(tmem + kColDp, sm.own[1], sm.ring_b[j & 1]);
+        umma_commit(smem_u32(&sm.dp_full));
+        umma_commit(smem_u32(&sm.b_empty[j & 1]));
+        return true;
+      };
+      if (ok) ok = dp(0);
+      for (int j = 0; ok && j < n; ++j) {
+        // dS(j) written means dP(j) read; dP(j + 1) goes first, so that the next
+        // elementwise step waits for one product only
+        if (!(ok = bounded_wait(sm, sm.ds_done, j & 1, a.err))) break;
+        tc_fence_after();
+        if (j + 1 < n && !(ok = dp(j + 1))) break;
+        if (!(ok = bounded_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        product_km(tmem + kColDq, tmem + kColDs + 64 * (j & 1), 32, sm.ring_a[j & 1], j > 0);
+        umma_commit(smem_u32(&sm.a_empty[j & 1]));
+      }
+      umma_commit(smem_u32(ok ? &sm.acc[0] : &sm.drain[1]));
+      if (!ok) mbar_wait(smem_u32(&sm.drain[1]), 0, nullptr, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    const int quad = warp & 3, half = warp >> 2;           // 64 key columns per warp
+    const int i_q = min(q0 + quad * 32 + lane, p.Sq - 1);
+    const bool live = q0 + quad * 32 + lane < p.Sq;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t ts = lane_addr + kColS + 64 * half, tp = lane_addr + kColDp + 64 * half;
+    const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + q0 + quad * 32 + lane;
+    const float lse2 = a.lse2[at], delta = a.delta[at];
+    const float c = p.scale * kLog2e, slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+    const int lim = p.limit(b, i_q), lim0 = p.limit(b, q0);
+    const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
+    const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int rec = list ? list[j] : j;
+      const int kt = rec & kTileMask, k0 = kt * kRows;
+      const bool part_doc = rec & kPartial0;
+      const bool partial = part_doc || k0 + kRows - 1 > lim0;
+      uint4 bm = make_uint4(0, 0, 0, 0);
+      if (bad) bm = bad[kt];
+      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      if (partial) {
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const int col = k0 + 64 * half + 32 * q2;
+          uint32_t m = 0;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) m |= (col + u <= lim ? 1u : 0u) << u;
+          if (part_doc) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const int d = __ldg(dk + min(col + u, p.Sk - 1));
+              if (!(d == doc && d >= 0)) m &= ~(1u << u);
+            }
+          }
+          see[q2] = m;
+        }
+      }
+      const uint32_t bb[2] = {half ? bm.z : bm.x, half ? bm.w : bm.y};
+      if (!(ok = warp_wait(sm, sm.s_full, j & 1, a.err))) break;
+      tc_fence_after();
+      float w[2][32];
+#pragma unroll
+      for (int q2 = 0; q2 < 2; ++q2) {
+        float x[32];
+        tmem_ld32x32f(ts + 32 * q2, x);
+        tmem_wait_ld32(x);
+        if (q2 == 1) {                                     // S(j) is in registers: S(j + 1) may replace it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.s_done));
+        }
+        const float d0 = static_cast<float>(i_q + p.off - k0 - 64 * half - 32 * q2);
+        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, -1.0f, [&](int) { return lse2; });
+      }
+      if (!(ok = warp_wait(sm, sm.dp_full, j & 1, a.err))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q2 = 0; q2 < 2; ++q2) {
+        float x[32];
+        tmem_ld32x32f(tp + 32 * q2, x);
+        tmem_wait_ld32(x);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) x[u] = w[q2][u] * (x[u] - delta);
+        if (partial) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
+        }
+        if (bb[q2]) {                                      // a visible key with an infinity or NaN in its k
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if ((bb[q2] & see[q2]) >> u & 1u) x[u] = NAN;
+        }
+        uint32_t pw[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+        tmem_st32x16(lane_addr + kColDs + 64 * (j & 1) + 32 * half + 16 * q2, pw);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done));
+    }
+    if (ok && n > 0) {
+      ok = warp_wait(sm, sm.acc[0], 0, a.err);
+      tc_fence_after();
+    }
+    if (ok)
+      write_half_row(lane_addr + kColDq + 64 * half, n > 0, p.scale, live,
+                     a.out1 + b * a.so1.b + i_q * a.so1.s + h * a.so1.h + 64 * half);
+  }
+  finish(tmem);
+}
+
+// Zeros of [B, S, heads, 128] (no keys, or no queries).
+__global__ void __launch_bounds__(256) zero_kernel(uint16_t* x, Strides st, int S, int heads, int64_t n) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // 16-byte piece
+  if (e >= n) return;
+  const int64_t r = e >> 4, h = r % heads, t = r / heads;
+  *reinterpret_cast<uint4*>(x + t / S * st.b + t % S * st.s + h * st.h + (e & 15) * 8) = make_uint4(0, 0, 0, 0);
+}
+
+void zero(const vsa_view* v, int32_t B, int32_t S, cudaStream_t stream) {
+  const int64_t n = static_cast<int64_t>(B) * S * v->heads * 16;
+  if (n)
+    zero_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(static_cast<uint16_t*>(v->data),
+                                                                            view_strides(v, B, S), S, v->heads, n);
+}
+
+struct Workspace {
+  size_t lse2, delta, range, range_q, count_q, list_q, count_k, list_k;
+  size_t bad_q, bad_o, bad_k, copy_q, copy_o, copy_k, total;
+};
+
+Workspace workspace_of(const Problem& p) {
+  Workspace w{};
+  size_t off = kHeader;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t b = static_cast<size_t>(p.B), nkt = static_cast<size_t>(p.nkt), nqt = static_cast<size_t>(tiles(p.Sq));
+  w.lse2 = take(b * p.Hq * nqt * kRows * sizeof(float));
+  w.delta = take(b * p.Hq * nqt * kRows * sizeof(float));
+  if (p.documents) {
+    w.range = take(b * nkt * sizeof(int4));
+    w.range_q = take(b * nqt * sizeof(int4));
+    w.count_q = take(b * nqt * sizeof(int32_t));
+    w.list_q = take(b * nqt * nkt * sizeof(int32_t));
+    w.count_k = take(b * nkt * sizeof(int32_t));
+    w.list_k = take(b * nkt * nqt * sizeof(int32_t));
+  }
+  if (p.masked) {
+    w.bad_q = take(b * p.Hq * nqt * sizeof(uint4));
+    w.bad_o = take(b * p.Hq * nqt * sizeof(uint4));
+    w.bad_k = take(b * p.Hk * nkt * sizeof(uint4));
+    w.copy_q = take(b * p.Sq * p.Hq * kHeadDim * 2);
+    w.copy_o = take(b * p.Sq * p.Hq * kHeadDim * 2);
+    w.copy_k = take(b * p.Sk * p.Hk * kHeadDim * 2);
+  }
+  w.total = off;
+  return w;
+}
+
+struct Maps {
+  CUtensorMap q, k, v, o, qc, oc, kc;
+};
+
+template <bool kCap, bool kBias>
+vsa_status launch(const Args& dkv, const Args& dq, const Maps& m, cudaStream_t stream) {
+  const auto k1 = dkv_kernel<kCap, kBias>;
+  const auto k2 = dq_kernel<kCap, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: shared memory", e);
+  const Problem& p = dkv.p;
+  k1<<<p.nkt * p.Hk * p.B, kThreads, sizeof(Smem), stream>>>(dkv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+  k2<<<dq.nqt * p.Hq * p.B, kThreads, sizeof(Smem), stream>>>(dq, m.q, m.o, m.k, m.v, m.kc);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_bwd", e);
+}
+
+}  // namespace
+}  // namespace masked
+}  // namespace vsa
+
+using namespace vsa;
+using namespace vsa::masked;
+
+extern "C" {
+
+vsa_status vsa_masked_attn_bwd_workspace_size(const vsa_mask* mask, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
+                                              int32_t Hk, size_t* bytes) {
+  if (!bytes || !mask || (mask->documents != 0 && mask->documents != 1)) return VSA_ERR_INVALID_ARG;
+  Problem p;
+  vsa_mask m = *mask;
+  m.documents = 0;                                        // the tensors are not at hand yet
+  const vsa_status st = check(&m, nullptr, B, Sq, Sk, Hq, Hk, &p);
+  if (st != VSA_OK) return st;
+  p.documents = mask->documents;
+  p.masked |= mask->documents;
+  *bytes = workspace_of(p).total;
+  return VSA_OK;
+}
+
+vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
+                               const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
+                               const float* lse, const vsa_view* dout, const vsa_view* dq, const vsa_view* dk,
+                               const vsa_view* dv, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !k || !v || !out || !dout || !dq || !dk || !dv) return VSA_ERR_INVALID_ARG;
+  Problem p;
+  vsa_status st = check(mask, terms, B, Sq, Sk, q->heads, k->heads, &p);
+  for (const vsa_view* x : {q, out, dout})
+    if (st == VSA_OK) st = check_tensor(x, B, Sq, q->heads, false);
+  for (const vsa_view* x : {k, v})
+    if (st == VSA_OK) st = check_tensor(x, B, Sk, k->heads, false);
+  if (st == VSA_OK) st = check_tensor(dq, B, Sq, q->heads, true);
+  for (const vsa_view* x : {dk, dv})
+    if (st == VSA_OK) st = check_tensor(x, B, Sk, k->heads, true);
+  if (st != VSA_OK) return st;
+  if (reinterpret_cast<uintptr_t>(lse) % 4) return VSA_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256) return VSA_ERR_INVALID_ARG;
+  const Workspace w = workspace_of(p);
+  if (workspace_bytes < w.total) return VSA_ERR_WORKSPACE_TOO_SMALL;
+  char* ws = static_cast<char*>(workspace);
+  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);   // this call's status word
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: cudaMemsetAsync", e);
+  if (B == 0 || Sq == 0 || Sk == 0) {
+    zero(dq, B, Sq, stream);
+    zero(dk, B, Sk, stream);
+    zero(dv, B, Sk, stream);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_bwd", e);
+  }
+  if (!lse) return VSA_ERR_INVALID_ARG;
+
+  Maps m;
+  if ((st = make_map(&m.q, q, B, Sq)) != VSA_OK || (st = make_map(&m.k, k, B, Sk)) != VSA_OK ||
+      (st = make_map(&m.v, v, B, Sk)) != VSA_OK || (st = make_map(&m.o, dout, B, Sq)) != VSA_OK)
+    return st;
+  m.qc = m.q;
+  m.oc = m.o;
+  m.kc = m.k;
+  const int nqt = tiles(Sq);
+  PrepArgs pa{};
+  pa.out = static_cast<const uint16_t*>(out->data);
+  pa.dout = static_cast<const uint16_t*>(dout->data);
+  pa.so = view_strides(out, B, Sq);
+  pa.sd = view_strides(dout, B, Sq);
+  pa.lse = lse;
+  pa.B = B;
+  pa.Hq = p.Hq;
+  pa.Sq = Sq;
+  pa.padded = nqt * kRows;
+  pa.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  pa.delta = reinterpret_cast<float*>(ws + w.delta);
+  prepare_kernel<<<dim3(nqt * kRows / 16, p.Hq, B), 256, 0, stream>>>(pa);
+
+  Args g{};
+  g.p = p;
+  g.lse2 = pa.lse2;
+  g.delta = pa.delta;
+  g.padded = pa.padded;
+  g.nqt = nqt;
+  g.err = reinterpret_cast<int*>(ws);
+  const Strides sq = view_strides(q, B, Sq), sd = pa.sd, sk = view_strides(k, B, Sk), sv = view_strides(v, B, Sk);
+  Args kv = g, qq = g;
+  kv.a_h = qq.o1_h = sq.h != 0;
+  kv.a_b = qq.o1_b = sq.b != 0;
+  kv.b_h = qq.o2_h = sd.h != 0;
+  kv.b_b = qq.o2_b = sd.b != 0;
+  kv.o1_h = qq.a_h = sk.h != 0;
+  kv.o1_b = qq.a_b = sk.b != 0;
+  kv.o2_h = qq.b_h = sv.h != 0;
+  kv.o2_b = qq.b_b = sv.b != 0;
+  kv.out1 = static_cast<uint16_t*>(dk->data);
+  kv.so1 = view_strides(dk, B, Sk);
+  kv.out2 = static_cast<uint16_t*>(dv->data);
+  kv.so2 = view_strides(dv, B, Sk);
+  qq.out1 = static_cast<uint16_t*>(dq->data);
+  qq.so1 = view_strides(dq, B, Sq);
+  if (p.documents) {
+    int4* range = reinterpret_cast<int4*>(ws + w.range);
+    int32_t *cq = reinterpret_cast<int32_t*>(ws + w.count_q), *lq = reinterpret_cast<int32_t*>(ws + w.list_q);
+    int32_t *ck = reinterpret_cast<int32_t*>(ws + w.count_k), *lk = reinterpret_cast<int32_t*>(ws + w.list_k);
+    plan(p, kPlanSingle, nqt, range, cq, lq, stream);
+    plan_keys(p, range, reinterpret_cast<int4*>(ws + w.range_q), ck, lk, stream);
+    qq.count = cq;
+    qq.list = lq;
+    kv.count = ck;
+    kv.list = lk;
+  }
+  if (p.masked) {
+    kv.clean_a = Clean{reinterpret_cast<uint4*>(ws + w.bad_q), reinterpret_cast<uint16_t*>(ws + w.copy_q)};
+    kv.clean_b = Clean{reinterpret_cast<uint4*>(ws + w.bad_o), reinterpret_cast<uint16_t*>(ws + w.copy_o)};
+    qq.clean_a = Clean{reinterpret_cast<uint4*>(ws + w.bad_k), reinterpret_cast<uint16_t*>(ws + w.copy_k)};
+    if ((st = make_map(&m.qc, kv.clean_a.copy, B, Sq, p.Hq)) != VSA_OK ||
+        (st = make_map(&m.oc, kv.clean_b.copy, B, Sq, p.Hq)) != VSA_OK ||
+        (st = make_map(&m.kc, qq.clean_a.copy, B, Sk, p.Hk)) != VSA_OK)
+      return st;
+    if ((st = scan(q, B, Sq, kv.clean_a, stream)) != VSA_OK || (st = scan(dout, B, Sq, kv.clean_b, stream)) != VSA_OK ||
+        (st = scan(k, B, Sk, qq.clean_a, stream)) != VSA_OK)
+      return st;
+  }
+  const bool cap = p.cap > 0.0f, bias = p.slopes != nullptr;
+  if (cap) return bias ? launch<true, true>(kv, qq, m, stream) : launch<true, false>(kv, qq, m, stream);
+  return bias ? launch<false, true>(kv, qq, m, stream) : launch<false, false>(kv, qq, m, stream);
+}
+
+}  // extern "C"

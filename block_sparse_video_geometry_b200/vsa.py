@@ -127,6 +127,10 @@ _SIGNATURES = {
                                               ctypes.POINTER(_SZ)]),
     "vsa_masked_attn_fwd": (_I32, [ctypes.POINTER(Mask), ctypes.POINTER(MaskTerms), _I32, _I32, _I32, _V, _V, _V, _V,
                                    _P, _P, _SZ, _P]),
+    "vsa_masked_attn_bwd_workspace_size": (_I32, [ctypes.POINTER(Mask), _I32, _I32, _I32, _I32, _I32,
+                                                  ctypes.POINTER(_SZ)]),
+    "vsa_masked_attn_bwd": (_I32, [ctypes.POINTER(Mask), ctypes.POINTER(MaskTerms), _I32, _I32, _I32, _V, _V, _V, _V,
+                                   _P, _V, _V, _V, _V, _P, _SZ, _P]),
     "vsa_masked_attn_status": (_I32, [_P, _P]),
     "vsa_status_string": (ctypes.c_char_p, [_I32]),
     "vsa_version": (_I32, []),
@@ -614,6 +618,32 @@ def masked_attn_fwd(mask: Mask, q, k, v, out, lse, workspace, doc_q=None, doc_k=
                                          _stream_handle(stream)), "vsa_masked_attn_fwd")
 
 
+def masked_attn_bwd_workspace_size(mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int) -> int:
+    n = _SZ()
+    _check(lib().vsa_masked_attn_bwd_workspace_size(ctypes.byref(mask), B, Sq, Sk, Hq, Hk, ctypes.byref(n)),
+           "vsa_masked_attn_bwd_workspace_size")
+    return n.value
+
+
+def masked_attn_bwd(mask: Mask, q, k, v, out, lse, dout, dq, dk, dv, workspace, doc_q=None, doc_k=None, prefix=None,
+                    slopes=None, stream=None) -> None:
+    """vsa_masked_attn_bwd on torch tensors: bf16 dq, dk, dv shaped like q, k, v from masked_attn_fwd's inputs, its out
+    and lse, and dout (bf16, out's shape)."""
+    import torch
+    B, Sq, Sk, Hq, Hk = _attn_shapes(q, k, v)
+    if out.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape:
+        raise ValueError("out, dout and dq must have q's shape")
+    if dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("dk and dv must have k's shape")
+    terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
+    with _On(q, k, v, out, lse, dout, dq, dk, dv, workspace, doc_q, doc_k, prefix, slopes):
+        _check(lib().vsa_masked_attn_bwd(ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v),
+                                         _view(out), _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), _view(dout),
+                                         _view(dq), _view(dk), _view(dv), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+               "vsa_masked_attn_bwd")
+
+
 def masked_attn_status(workspace, stream=None) -> int:
     """Synchronises the stream; the status of the latest masked attention call on `workspace` (OK or ERR_TIMEOUT)."""
     return lib().vsa_masked_attn_status(workspace.data_ptr(), _stream_handle(stream))
@@ -628,7 +658,7 @@ class MaskedAttention:
         self.masks = [Mask(mask.mode, d, mask.scale, mask.softcap) for d in (0, 1)]
         for m in self.masks:
             masked_attn_workspace_size(m, *self.shape)       # refuses a shape or mask at once
-        self.ws_fwd = {}
+        self.ws_fwd, self.ws_bwd = {}, {}      # by whether documents are given
 
     def _workspace(self, held, size, documents):
         import torch
@@ -653,6 +683,19 @@ class MaskedAttention:
         masked_attn_fwd(self.masks[d], q, k, v, out, lse, self._workspace(self.ws_fwd, masked_attn_workspace_size, d),
                         doc_q, doc_k, prefix, slopes, stream)
         return out, lse
+
+    def backward(self, q, k, v, out, lse, dout, dq=None, dk=None, dv=None, doc_q=None, doc_k=None, prefix=None,
+                 slopes=None, stream=None):
+        """masked_attn_bwd; returns (dq, dk, dv)."""
+        import torch
+        self._own_shape(q, k, v)
+        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if g is None else g
+                      for g, x in ((dq, q), (dk, k), (dv, v)))
+        d = int(doc_q is not None)
+        masked_attn_bwd(self.masks[d], q, k, v, out, lse, dout, dq, dk, dv,
+                        self._workspace(self.ws_bwd, masked_attn_bwd_workspace_size, d), doc_q, doc_k, prefix, slopes,
+                        stream)
+        return dq, dk, dv
 
 
 def debug_inject_wait_timeout(timeout_ns):

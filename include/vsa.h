@@ -646,6 +646,28 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
                                const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
                                float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+vsa_status vsa_masked_attn_bwd_workspace_size(const vsa_mask* mask, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
+                                              int32_t Hk, size_t* bytes);
+
+/* vsa_masked_attn_bwd: the gradients of sum(out * dout) for
+ * vsa_masked_attn_fwd with the same mask, terms, q, k and v.
+ *  out, lse   : that call's outputs.
+ *  dout       : bf16 like out.
+ *  dq, dk, dv : bf16 like q, k, v; a key head's dk and dv sum over the query
+ *               heads that read it. Every element is written; a row that sees
+ *               nothing, or that nothing sees, gets 0. The slopes get no
+ *               gradient.
+ *  workspace  : vsa_masked_attn_bwd_workspace_size bytes, 256-byte aligned.
+ * With P = exp(s - lse) and D = sum(dout * out): dS = P (dout v - D), times
+ * 1 - tanh^2 under a cap; dq = scale dS k, dk = scale dS^T q, dv = P^T dout. P and
+ * dS enter the products as bf16, every sum is 32-bit and in a fixed order: equal
+ * inputs give equal bits. Masked rows that hold infinities or NaN change
+ * nothing, as in the forward pass. */
+vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
+                               const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
+                               const float* lse, const vsa_view* dout, const vsa_view* dq, const vsa_view* dk,
+                               const vsa_view* dv, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream` and reads the status word that the latest
  * vsa_masked_attn_fwd or vsa_masked_attn_bwd left in `workspace`: VSA_OK or
  * VSA_ERR_TIMEOUT (a bounded wait ran out; the outputs are incomplete). */
