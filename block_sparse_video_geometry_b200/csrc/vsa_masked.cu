@@ -11,7 +11,7 @@
 //
 // Design. A block owns 256 rows of one head as two M = 128 tiles and walks the
 // key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
-// 32 KB stages; two warps issue the products, one per query tile; two groups of
+// 32 KB stages; one warp issues the products, the two tiles in turn; two groups of
 // four warps run the softmax, a thread per row. S of a tile and P over it share
 // TMEM columns, so the tensor pipe works on one query tile while the other's
 // softmax runs: S(j) -> P(j) (bf16, A operand from TMEM) -> O += P(j) V(j), and
@@ -299,8 +299,8 @@ plan_keys_kernel(const __grid_constant__ Problem p, const int4* __restrict__ ran
 
 // --------------------------------------------------------------- main kernel
 constexpr int kStages = 5;
-constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9;          // warps 0-7: softmax; 9, 10: products of query tile 0, 1
+constexpr int kThreads = 320;
+constexpr int kWarpLoad = 8, kWarpMma = 9;          // warps 0-7: softmax
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;          // S of tile t: 128 t; O of tile t: 256 + 128 t
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
@@ -311,7 +311,7 @@ struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain[2];
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem_base;
   int abort;
 };
@@ -377,14 +377,14 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 1);
-      mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one product warp, or by both
+      mbar_init(smem_u32(&sm.empty[i]), 1);
     }
     mbar_init(smem_u32(&sm.q_full), 8);
+    mbar_init(smem_u32(&sm.drain), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&sm.s_full[t]), 1);
       mbar_init(smem_u32(&sm.p_full[t]), 4);
       mbar_init(smem_u32(&sm.o_full[t]), 1);
-      mbar_init(smem_u32(&sm.drain[t]), 1);
     }
     sm.abort = 0;
     fence_mbar_init();
@@ -410,6 +410,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int32_t* list = a.count ? a.list + plan_row * p.nkt : nullptr;
   const int s0 = static_cast<int>(static_cast<int64_t>(n_all) * split / a.splits);
   const int s1 = static_cast<int>(static_cast<int64_t>(n_all) * (split + 1) / a.splits);
+  // last tile first: under a distance bias the largest scores are near the
+  // query, and a reference found there rarely has to be raised
   const int n = s1 - s0;
   const uint4* bad = a.clean_v.bad ? a.clean_v.bad + (static_cast<size_t>(b) * p.Hk + hk) * p.nkt : nullptr;
 
@@ -420,7 +422,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       bool ok = true;
       int e = 0;
       for (; ok && e < 2 * n; ++e) {
-        const int st = e % kStages, rec = list ? list[s0 + (e >> 1)] : s0 + (e >> 1);
+        const int st = e % kStages, rec = list ? list[s1 - 1 - (e >> 1)] : s1 - 1 - (e >> 1);
         const int kt = rec & kTileMask;
         if (e >= kStages && !(ok = bounded_wait(sm, sm.empty[st], (e / kStages - 1) & 1, a.err))) break;
         const CUtensorMap* map = e & 1 ? &map_v : &map_k;
@@ -439,48 +441,55 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
-    const int t = warp - kWarpMma;
+  } else if (warp == kWarpMma) {
     if (lane == 0) {
-      const uint32_t ts = tmem + kColS + 128 * t, to = tmem + kColO + 128 * t;
-      const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
       bool ok = bounded_wait(sm, sm.q_full, 0, a.err);
-      const int step = one ? 2 : 1;
-      int i = 0;                                           // this slot's step number
-      // S(j) = Q K(j)^T: 16 channels per K step, 32 B inside a swizzled row of the d half kk / 4
-      auto scores = [&](int j) {
+      // S(j) = Q K(j)^T of slot t: 16 channels per K step, 32 B inside a swizzled
+      // row of the d half kk / 4. A stage is free once every slot that reads it has.
+      auto scores = [&](int t, int j) {
         const int e = 2 * j, st = e % kStages;
         if (!bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err)) return false;
         tc_fence_after();
+        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
         const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_ss(ts, qd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
-                  kIdescS, kk > 0 ? 1u : 0u);
+          umma_ss(tmem + kColS + 128 * t, qd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
+                  kd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kIdescS, kk > 0 ? 1u : 0u);
         umma_commit(smem_u32(&sm.s_full[t]));
-        umma_commit(smem_u32(&sm.empty[st]));
+        if (one || t == 1) umma_commit(smem_u32(&sm.empty[st]));
         return true;
       };
-      int j = one ? t : 0;
-      if (ok && j < n) ok = scores(j);
-      for (; ok && j < n; j += step, ++i) {
-        const int e = 2 * j + 1, st = e % kStages;
-        if (!(ok = bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
-        if (!(ok = bounded_wait(sm, sm.p_full[t], i & 1, a.err))) break;
-        tc_fence_after();
-        // V as MN-major B: d halves 16 KB apart, 16 keys = 2 KB per K step; P (A,
-        // over its scores): 16 keys = 8 columns of bf16 pairs
-        const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]), 16384, 1024);
+      // The slots take turns in one thread, so that the products of one run while
+      // the other is in its softmax: ..., O0 += P0 V, S0', O1 += P1 V, S1', ...
+      // (with an issuing thread per slot the two fell into step and tensor pipe
+      // and softmax took turns: 5250 cycles a step instead of 3100).
+      const int step = one ? 2 : 1;
+      for (int t = 0; ok && t < 2; ++t)
+        if ((one ? t : 0) < n) ok = scores(t, one ? t : 0);
+      for (int j = 0, i = 0; ok && j < n; j += step, ++i) {
+        for (int t = 0; ok && t < 2; ++t) {
+          const int jt = one ? j + t : j;                  // this slot's key tile
+          if (jt >= n) break;
+          const int e = 2 * jt + 1, st = e % kStages;
+          if (!(ok = bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
+          if (!(ok = bounded_wait(sm, sm.p_full[t], i & 1, a.err))) break;
+          tc_fence_after();
+          // V as MN-major B: d halves 16 KB apart, 16 keys = 2 KB per K step; P (A,
+          // over its scores): 16 keys = 8 columns of bf16 pairs
+          const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]), 16384, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(to, ts + kk * 8, vd + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0 ? 1u : 0u);
-        umma_commit(smem_u32(&sm.empty[st]));
-        if (j + step < n) ok = scores(j + step);
-        else umma_commit(smem_u32(&sm.o_full[t]));
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, vd + kk * (2048 >> 4), kIdescPV,
+                    i > 0 || kk > 0 ? 1u : 0u);
+          if (one || t == 1) umma_commit(smem_u32(&sm.empty[st]));
+          if (jt + step < n) ok = scores(t, jt + step);
+          else umma_commit(smem_u32(&sm.o_full[t]));
+        }
       }
       if (!ok) {
-        umma_commit(smem_u32(&sm.drain[t]));
-        mbar_wait(smem_u32(&sm.drain[t]), 0, nullptr, kDrainNs);
+        umma_commit(smem_u32(&sm.drain));
+        mbar_wait(smem_u32(&sm.drain), 0, nullptr, kDrainNs);
       }
     }
     __syncwarp();
@@ -528,7 +537,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int step = one ? 2 : 1;
     int i = 0;
     for (int j = one ? t : 0; j < n; j += step, ++i) {
-      const int rec = list ? list[s0 + j] : s0 + j;
+      const int rec = list ? list[s1 - 1 - j] : s1 - 1 - j;
       const int kt = rec & kTileMask, k0 = kt * kRows;
       const bool part_doc = rec & (t ? kPartial1 : kPartial0);
       const bool partial = part_doc || k0 + kRows - 1 > lim0;
@@ -543,7 +552,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         if constexpr (kCap) {
           // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
 #pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = fmaf(__fdividef(-2.0f, 1.0f + ex2_approx(x[u] * in2)), cap2, cap2);
+          for (int u = 0; u < 32; ++u) x[u] = fmaf(rcp_approx(1.0f + ex2_approx(x[u] * in2)), -2.0f * cap2, cap2);
         }
         if constexpr (kBias) {
           const float d0 = static_cast<float>(i_q + p.off - k0 - col);

@@ -225,7 +225,7 @@ __device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], co
   for (int u = 0; u < 32; ++u) {
     float s = x[u], t = 0.0f;
     if constexpr (kCap) {
-      t = 1.0f + __fdividef(-2.0f, 1.0f + ex2_approx(s * in2));
+      t = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(s * in2)), 1.0f);
       s = cap2 * t;
     } else if constexpr (kBias) {
       s *= c;
