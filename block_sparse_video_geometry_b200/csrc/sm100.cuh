@@ -270,10 +270,74 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// True in one lane of a converged warp, the same one each time. Instructions
+// under it (tensor core, copies, commits) issue at their own rate: an MMA behind
+// `lane == 0` held the thread 54 cycles, here 33.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b32 r;\n\telect.sync r|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Two 32-bit floats in one register pair, and the operations on both at once.
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^x of two floats on the FMA pipe: x = n + f with n the nearest whole number
+// (found by adding 1.5 * 2^23) and f in [-1/2, 1/2], 2^f by a polynomial of
+// degree 5 with relative error below 2^-22 (least squares with weights driven to
+// equal extrema, p(0) = 1), times 2^n. x is limited to -127 from below, where the
+// result is 0; NaN stays NaN. x < 127.
+__device__ __forceinline__ void ex2_poly_f32x2(uint64_t x, float& a, float& b) {
+  float x0, x1;
+  unpack_f32x2(x, x0, x1);
+  asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(x0) : "f"(x0));
+  asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(x1) : "f"(x1));
+  x = pack_f32x2(x0, x1);
+  const uint64_t magic = pack_f32x2(12582912.0f, 12582912.0f), minus = pack_f32x2(-12582912.0f, -12582912.0f);
+  const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);
+  const uint64_t r = add_f32x2(x, magic);
+  const uint64_t f = fma_f32x2(add_f32x2(r, minus), neg, x);
+  uint64_t p = pack_f32x2(0.00132647343f, 0.00132647343f);
+  p = fma_f32x2(p, f, pack_f32x2(0.00967151485f, 0.00967151485f));
+  p = fma_f32x2(p, f, pack_f32x2(0.0555073358f, 0.0555073358f));
+  p = fma_f32x2(p, f, pack_f32x2(0.240222424f, 0.240222424f));
+  p = fma_f32x2(p, f, pack_f32x2(0.693147004f, 0.693147004f));
+  p = fma_f32x2(p, f, one);
+  float r0, r1;
+  unpack_f32x2(r, r0, r1);
+  const float s0 = __uint_as_float((__float_as_uint(r0) << 23) + 0x3F800000u);   // 2^n, 0 for n = -127
+  const float s1 = __uint_as_float((__float_as_uint(r1) << 23) + 0x3F800000u);
+  unpack_f32x2(mul_f32x2(p, pack_f32x2(s0, s1)), a, b);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

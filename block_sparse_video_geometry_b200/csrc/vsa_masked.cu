@@ -12,11 +12,10 @@
 // Design. A block owns 256 rows of one head as two M = 128 tiles and walks the
 // key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
 // 32 KB stages; one warp issues the products, the two tiles in turn; two groups of
-// four warps run the softmax, a thread per row. S of a tile and P over it share
-// TMEM columns, so the tensor pipe works on one query tile while the other's
-// softmax runs: S(j) -> P(j) (bf16, A operand from TMEM) -> O += P(j) V(j), and
-// S(j + 1) behind it. The softmax's reference is raised, and O rescaled in TMEM,
-// only when a row's sum of P in a tile passes 2^8.
+// four warps run the softmax, a thread per row. Scores come in two buffers of 64
+// keys per query tile; P (bf16, the A operand of O += P V) overwrites its scores
+// in TMEM, and the next scores follow behind that product. The softmax's reference is raised, and O rescaled in TMEM,
+// only when a row's sum of P in a tile passes 2^32.
 // Few rows (a new token over a cache): the heads that share a key head are
 // packed into one tile, the two slots take the key tiles in turn with the same
 // queries, and the key axis is split over blocks; a second kernel joins the
@@ -299,19 +298,19 @@ plan_keys_kernel(const __grid_constant__ Problem p, const int4* __restrict__ ran
 
 // --------------------------------------------------------------- main kernel
 constexpr int kStages = 5;
-constexpr int kThreads = 320;
-constexpr int kWarpLoad = 8, kWarpMma = 9;          // warps 0-7: softmax
+constexpr int kThreads = 352;
+constexpr int kWarpLoad = 8, kWarpMma = 9;          // warps 0-7: softmax; 9, 10: products of slot 0, 1
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;          // S of tile t: 128 t; O of tile t: 256 + 128 t
-constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
+constexpr uint32_t kColS = 0, kColO = 256;          // score buffer hb of slot t: 128 t + 64 hb; O of slot t: 256 + 128 t
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, 0, 1);
-constexpr float kSumLimit = 256.0f;                 // 2^8: see the softmax step
+constexpr float kSumLimit = 4294967296.0f;          // 2^32: see the softmax step
 
 struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], drain[2];   // [slot][score buffer]
   uint32_t tmem_base;
   int abort;
 };
@@ -377,14 +376,16 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 1);
-      mbar_init(smem_u32(&sm.empty[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one slot, or by both
     }
     mbar_init(smem_u32(&sm.q_full), 8);
-    mbar_init(smem_u32(&sm.drain), 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&sm.s_full[t]), 1);
-      mbar_init(smem_u32(&sm.p_full[t]), 4);
-      mbar_init(smem_u32(&sm.o_full[t]), 1);
+      for (int hb = 0; hb < 2; ++hb) {
+        mbar_init(smem_u32(&sm.s_full[t][hb]), 1);
+        mbar_init(smem_u32(&sm.p_full[t][hb]), 4);
+      }
+      mbar_init(smem_u32(&sm.pv_done[t]), 1);
+      mbar_init(smem_u32(&sm.drain[t]), 1);
     }
     sm.abort = 0;
     fence_mbar_init();
@@ -415,19 +416,27 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int n = s1 - s0;
   const uint4* bad = a.clean_v.bad ? a.clean_v.bad + (static_cast<size_t>(b) * p.Hk + hk) * p.nkt : nullptr;
 
+  // Stage of K or V of key tile j in loading order. With one tile the slots hold
+  // two key tiles' scores at a time, so K runs two tiles ahead of V.
+  const int ahead = one ? 2 : 1;
+  auto place_k = [&](int j) { return j + max(0, j - ahead + 1); };
+  auto place_v = [&](int j) { return j + min(n, j + ahead); };
+
   if (warp == kWarpLoad) {
     if (lane == 0) {
       prefetch_map(&map_k);
       prefetch_map(&map_v);
       bool ok = true;
-      int e = 0;
-      for (; ok && e < 2 * n; ++e) {
-        const int st = e % kStages, rec = list ? list[s1 - 1 - (e >> 1)] : s1 - 1 - (e >> 1);
-        const int kt = rec & kTileMask;
+      int e = 0, kj = 0, vj = 0;
+      for (; e < 2 * n; ++e) {
+        // the order in which the products use them: K up to `ahead` tiles before V
+        const bool is_v = kj == min(n, vj + ahead);
+        const int st = e % kStages, j = is_v ? vj++ : kj++;
+        const int kt = (list ? list[s1 - 1 - j] : s1 - 1 - j) & kTileMask;
         if (e >= kStages && !(ok = bounded_wait(sm, sm.empty[st], (e / kStages - 1) & 1, a.err))) break;
-        const CUtensorMap* map = e & 1 ? &map_v : &map_k;
-        int h = (e & 1 ? a.v_h : a.k_h) ? hk : 0, bb = (e & 1 ? a.v_b : a.k_b) ? b : 0;
-        if ((e & 1) && bad) {
+        const CUtensorMap* map = is_v ? &map_v : &map_k;
+        int h = (is_v ? a.v_h : a.k_h) ? hk : 0, bb = (is_v ? a.v_b : a.k_b) ? b : 0;
+        if (is_v && bad) {
           const uint4 m = bad[kt];
           if (m.x | m.y | m.z | m.w) map = &map_vc, h = hk, bb = b;
         }
@@ -441,56 +450,61 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      bool ok = bounded_wait(sm, sm.q_full, 0, a.err);
-      // S(j) = Q K(j)^T of slot t: 16 channels per K step, 32 B inside a swizzled
-      // row of the d half kk / 4. A stage is free once every slot that reads it has.
-      auto scores = [&](int t, int j) {
-        const int e = 2 * j, st = e % kStages;
-        if (!bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err)) return false;
-        tc_fence_after();
-        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
-        const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]), 16, 1024);
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // One issuing warp per slot: while one waits, the other's products run. (One
+    // warp for both lost the 100 cycles of every wait to the tensor pipe: 1214 us
+    // instead of 868 for 8192 x 24 heads.) Each slot has two score buffers of 64
+    // keys, so that the next scores are there when its softmax ends one buffer;
+    // with one buffer of 128 keys the chain S, softmax, P V of a slot bounded a step
+    // (910 us).
+    const int t = warp - kWarpMma;
+    const uint32_t ts = tmem + kColS + 128 * t, to = tmem + kColO + 128 * t;
+    const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
+    bool ok = warp_wait(sm, sm.q_full, 0, a.err);
+    // S(j, hb) = Q K^T over half hb of key tile j: 16 channels per K step, 32 B
+    // inside a swizzled row of the d half kk / 4; 64 key rows = 8 KB.
+    auto scores = [&](int j, int hb) {
+      const int e = place_k(j), st = e % kStages;
+      if (hb == 0 && !warp_wait(sm, sm.full[st], (e / kStages) & 1, a.err)) return false;
+      tc_fence_after();
+      const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]) + 8192 * hb, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_ss(tmem + kColS + 128 * t, qd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
+          umma_ss(ts + 64 * hb, qd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
                   kd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kIdescS, kk > 0 ? 1u : 0u);
-        umma_commit(smem_u32(&sm.s_full[t]));
-        if (one || t == 1) umma_commit(smem_u32(&sm.empty[st]));
-        return true;
-      };
-      // The slots take turns in one thread, so that the products of one run while
-      // the other is in its softmax: ..., O0 += P0 V, S0', O1 += P1 V, S1', ...
-      // (with an issuing thread per slot the two fell into step and tensor pipe
-      // and softmax took turns: 5250 cycles a step instead of 3100).
-      const int step = one ? 2 : 1;
-      for (int t = 0; ok && t < 2; ++t)
-        if ((one ? t : 0) < n) ok = scores(t, one ? t : 0);
-      for (int j = 0, i = 0; ok && j < n; j += step, ++i) {
-        for (int t = 0; ok && t < 2; ++t) {
-          const int jt = one ? j + t : j;                  // this slot's key tile
-          if (jt >= n) break;
-          const int e = 2 * jt + 1, st = e % kStages;
-          if (!(ok = bounded_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
-          if (!(ok = bounded_wait(sm, sm.p_full[t], i & 1, a.err))) break;
-          tc_fence_after();
-          // V as MN-major B: d halves 16 KB apart, 16 keys = 2 KB per K step; P (A,
-          // over its scores): 16 keys = 8 columns of bf16 pairs
-          const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]), 16384, 1024);
+        umma_commit(smem_u32(&sm.s_full[t][hb]));
+        if (hb == 1) umma_commit(smem_u32(&sm.empty[st]));
+      }
+      __syncwarp();
+      return true;
+    };
+    const int step = one ? 2 : 1, j0 = one ? t : 0;
+    if (ok && j0 < n) ok = scores(j0, 0) && scores(j0, 1);
+    for (int j = j0, i = 0; ok && j < n; j += step, ++i) {
+      const int e = place_v(j), st = e % kStages;
+      if (!(ok = warp_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
+#pragma unroll 1
+      for (int hb = 0; hb < 2; ++hb) {
+        if (!(ok = warp_wait(sm, sm.p_full[t][hb], i & 1, a.err))) break;
+        tc_fence_after();
+        // V as MN-major B: d halves 16 KB apart, 16 keys = 2 KB per K step; P (A,
+        // over its scores): 16 keys = 8 columns of bf16 pairs
+        const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]) + 8192 * hb, 16384, 1024);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, vd + kk * (2048 >> 4), kIdescPV,
-                    i > 0 || kk > 0 ? 1u : 0u);
-          if (one || t == 1) umma_commit(smem_u32(&sm.empty[st]));
-          if (jt + step < n) ok = scores(t, jt + step);
-          else umma_commit(smem_u32(&sm.o_full[t]));
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(to, ts + 64 * hb + kk * 8, vd + kk * (2048 >> 4), kIdescPV, i > 0 || hb > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(smem_u32(&sm.pv_done[t]));
+          if (hb == 1) umma_commit(smem_u32(&sm.empty[st]));
         }
+        __syncwarp();
+        if (j + step < n && !(ok = scores(j + step, hb))) break;
       }
-      if (!ok) {
-        umma_commit(smem_u32(&sm.drain));
-        mbar_wait(smem_u32(&sm.drain), 0, nullptr, kDrainNs);
-      }
+    }
+    if (!ok && elect_one()) {
+      umma_commit(smem_u32(&sm.drain[t]));
+      mbar_wait(smem_u32(&sm.drain[t]), 0, nullptr, kDrainNs);
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -544,114 +558,138 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       uint4 bm = make_uint4(0, 0, 0, 0);
       if (bad) bm = bad[kt];
       const bool flagged = bm.x | bm.y | bm.z | bm.w;
-      if (!(ok = warp_wait(sm, sm.s_full[t], i & 1, a.err))) break;
-      tc_fence_after();
-      // scores of columns [32 q4, 32 q4 + 32) in place: cap, bias, mask
-      auto finish = [&](int q4, float (&x)[32]) {
-        const int col = 32 * q4;
-        if constexpr (kCap) {
-          // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+      for (int hb = 0; hb < 2; ++hb) {
+        const uint32_t tb = ts + 64 * hb;                    // this half's scores
+        if (!(ok = warp_wait(sm, sm.s_full[t][hb], i & 1, a.err))) break;
+        tc_fence_after();
+        // scores of key columns [32 q4, 32 q4 + 32) in place: cap, bias, mask
+        auto finish = [&](int q4, float (&x)[32]) {
+          const int col = 32 * q4;
+          if constexpr (kCap) {
+            // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
 #pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = fmaf(rcp_approx(1.0f + ex2_approx(x[u] * in2)), -2.0f * cap2, cap2);
-        }
-        if constexpr (kBias) {
-          const float d0 = static_cast<float>(i_q + p.off - k0 - col);
+            for (int u = 0; u < 32; ++u) x[u] = fmaf(rcp_approx(1.0f + ex2_approx(x[u] * in2)), -2.0f * cap2, cap2);
+          }
+          if constexpr (kBias) {
+            const float d0 = static_cast<float>(i_q + p.off - k0 - col);
 #pragma unroll
-          for (int u = 0; u < 32; ++u)
-            x[u] = fmaf(-slope, fabsf(d0 - static_cast<float>(u)), kCap ? x[u] : x[u] * c);
-        }
-        if (partial) {
-          const int lc = lim - k0 - col;
+            for (int u = 0; u < 32; ++u)
+              x[u] = fmaf(-slope, fabsf(d0 - static_cast<float>(u)), kCap ? x[u] : x[u] * c);
+          }
+          if (partial) {
+            const int lc = lim - k0 - col;
 #pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = u <= lc ? x[u] : -INFINITY;
-          if (part_doc) {
-            const bool seeing = doc >= 0;
+            for (int u = 0; u < 32; ++u) x[u] = u <= lc ? x[u] : -INFINITY;
+            if (part_doc) {
+              const bool seeing = doc >= 0;
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int d = __ldg(dk + min(k0 + col + u, p.Sk - 1));
-              x[u] = seeing && d == doc ? x[u] : -INFINITY;
+              for (int u = 0; u < 32; ++u) {
+                const int d = __ldg(dk + min(k0 + col + u, p.Sk - 1));
+                x[u] = seeing && d == doc ? x[u] : -INFINITY;
+              }
             }
           }
-        }
-        if (flagged) {
-          // a visible key whose v holds an infinity or NaN makes the row NaN (its v is zero in the copy)
-          const uint32_t bits = q4 == 0 ? bm.x : q4 == 1 ? bm.y : q4 == 2 ? bm.z : bm.w;
+          if (flagged) {
+            // a visible key whose v holds an infinity or NaN makes the row NaN (its v is zero in the copy)
+            const uint32_t bits = q4 == 0 ? bm.x : q4 == 1 ? bm.y : q4 == 2 ? bm.z : bm.w;
 #pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if (((bits >> u) & 1u) && x[u] != -INFINITY) x[u] = NAN;
-        }
-      };
-      // P (bf16 pairs) against the reference m, and its 32-bit sum
-      uint32_t w[4][16];
-      auto exponentials = [&]() {
-        const float ms = m == -INFINITY ? 0.0f : m;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        float x[2][32];
-        tmem_ld32x32f(ts, x[0]);
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          float(&y)[32] = x[q4 & 1];
-          tmem_wait_ld32(y);
-          if (q4 < 3) tmem_ld32x32f(ts + 32 * (q4 + 1), x[(q4 + 1) & 1]);
-          finish(q4, y);
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const float p0 = ex2_approx(fmaf(y[2 * u], c_exp, -ms));
-            const float p1 = ex2_approx(fmaf(y[2 * u + 1], c_exp, -ms));
-            ls[u & 3] += p0 + p1;
-            w[q4][u] = pack_bf16x2(p0, p1);
+            for (int u = 0; u < 32; ++u)
+              if (((bits >> u) & 1u) && x[u] != -INFINITY) x[u] = NAN;
           }
-        }
-        return (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      };
-      // The reference m is a maximum of some earlier tile: while a row's sum of P
-      // stays within 2^8, so does every P, and neither the tile's maximum nor a
-      // rescale of O is needed. Otherwise (and on the first visible key) the
-      // exact maximum is formed, O and l are rescaled and P is formed again. S(j)
-      // complete means O of step j - 1 complete (one issuing thread, in order).
-      float psum = 0.0f;
-      if (!__any_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
-      else psum = INFINITY;
-      if (__any_sync(0xffffffffu, !(psum <= kSumLimit))) {
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int q4 = 0; q4 < 4; ++q4) {
-          float x[32];
-          tmem_ld32x32f(ts + 32 * q4, x);
-          tmem_wait_ld32(x);
-          finish(q4, x);
+        };
+        // P (bf16 pairs) against the reference m, and its 32-bit sum
+        uint32_t w[2][16];
+        auto exponentials = [&]() {
+          const float ms = m == -INFINITY ? 0.0f : m;
+          const uint64_t c2 = pack_f32x2(c_exp, c_exp), ms2 = pack_f32x2(-ms, -ms);
+          uint64_t ls[2] = {0, 0};
+          float x[2][32];
+          tmem_ld32x32f(tb, x[0]);
+          tmem_wait_ld32(x[0]);
+          tmem_ld32x32f(tb + 32, x[1]);
 #pragma unroll
-          for (int u = 0; u < 32; ++u) top = fmaxf(top, x[u]);
-        }
-        top *= c_exp;
-        const bool grow = top > m;
-        const float f = grow ? ex2_approx(m - top) : 1.0f;   // m = -inf: 0, and l and O are 0
-        if (grow) m = top;
-        l *= f;
-        if (i > 0) {
-#pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
-            float o[32];
-            tmem_ld32x32f(to + 32 * q4, o);
-            tmem_wait_ld32(o);
-            uint32_t ow[32];
+          for (int q2 = 0; q2 < 2; ++q2) {
+            float(&y)[32] = x[q2];
+            if (q2) tmem_wait_ld32(y);
+            finish(2 * hb + q2, y);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) ow[u] = __float_as_uint(o[u] * f);
-            tmem_st32x32(to + 32 * q4, ow);
+            for (int u = 0; u < 16; ++u) {
+              // a quarter of the exponentials on the FMA pipe: 868 -> 834 us for 8192 x 24
+              // heads (an eighth 848, three eighths 862)
+              float p0, p1;
+              const uint64_t arg = fma_f32x2(pack_f32x2(y[2 * u], y[2 * u + 1]), c2, ms2);
+              if (u % 4 == 2) {
+                ex2_poly_f32x2(arg, p0, p1);
+              } else {
+                unpack_f32x2(arg, p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+              }
+              ls[u & 1] = add_f32x2(ls[u & 1], pack_f32x2(p0, p1));
+              w[q2][u] = pack_bf16x2(p0, p1);
+            }
           }
+          float s0, s1;
+          unpack_f32x2(add_f32x2(ls[0], ls[1]), s0, s1);
+          return s0 + s1;
+        };
+        // The reference m is a maximum of some earlier half tile. P, its sums and O
+        // are floats of the 32-bit range (bf16 has it too), so a reference that is
+        // too low costs no precision; while a row's sum of P stays within 2^32,
+        // neither a maximum nor a rescale of O is needed. Otherwise (and on the
+        // first visible key) the exact maximum is formed, O (complete up to the
+        // last half) and l are rescaled and P is formed again.
+        float psum = INFINITY;
+        if (!__any_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
+        if (__any_sync(0xffffffffu, !(psum <= kSumLimit))) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int q2 = 0; q2 < 2; ++q2) {
+            float x[32];
+            tmem_ld32x32f(tb + 32 * q2, x);
+            tmem_wait_ld32(x);
+            finish(2 * hb + q2, x);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) top = fmaxf(top, x[u]);
+          }
+          top *= c_exp;
+          const bool grow = top > m;
+          const float f = grow ? ex2_approx(m - top) : 1.0f;   // m = -inf: 0, and l and O are 0
+          if (grow) m = top;
+          l *= f;
+          const int halves = 2 * i + hb;                       // P V products so far
+          if (halves > 0) {
+            if (!(ok = warp_wait(sm, sm.pv_done[t], (halves - 1) & 1, a.err))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+              float o[32];
+              tmem_ld32x32f(to + 32 * q4, o);
+              tmem_wait_ld32(o);
+              uint32_t ow[32];
+#pragma unroll
+              for (int u = 0; u < 32; ++u) ow[u] = __float_as_uint(o[u] * f);
+              tmem_st32x32(to + 32 * q4, ow);
+            }
+          }
+          psum = exponentials();
         }
-        psum = exponentials();
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, w[q2]);
+        l += psum;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t][hb]));
       }
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) tmem_st32x16(ts + 16 * q4, w[q4]);
-      l += psum;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t]));
+      if (!ok) break;
     }
     // ---------------------------------------------------------- epilogue
-    if (ok && i > 0 && (ok = warp_wait(sm, sm.o_full[t], 0, a.err))) tc_fence_after();
+    // the last two of 2 i products (those before are complete with the last scores)
+    if (ok && i > 0) {
+      ok = warp_wait(sm, sm.pv_done[t], 0, a.err) && warp_wait(sm, sm.pv_done[t], 1, a.err);
+      tc_fence_after();
+    }
     if (ok && !(one && t == 1 && a.parts == 1)) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
