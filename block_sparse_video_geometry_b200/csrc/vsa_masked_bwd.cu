@@ -22,7 +22,7 @@
 //  * dq_kernel: a block owns 128 queries of a head (lane = query) and walks the
 //    key tiles: S = Q K^T, dP = dO V^T, dQ += dS K, dS in two buffers of its own.
 // Both read their tiles by TMA, two stages each. D and lse in log2 units come from
-// prepare_kernel; rows without visible keys get lse = +inf there, so that P = 0.
+// prepare_kernel, negated; rows without visible keys get -inf there, so that P = 0.
 // Every wait is bounded (see vsa_masked_attn_status).
 
 #include <algorithm>
@@ -42,7 +42,8 @@ using namespace sm100;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ prepare
-// D and lse2 of every row, [B][Hq][nqt * 128]; rows past Sq: D = 0, lse2 = inf.
+// Minus D and minus lse2 of every row, [B][Hq][nqt * 128]; rows past Sq, and rows
+// without visible keys: 0 and -inf, so that P = 0.
 // 16 lanes per row. HBM bound: out and dout read once.
 struct PrepArgs {
   const uint16_t *out, *dout;
@@ -66,19 +67,19 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
 __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepArgs a) {
   const int i = blockIdx.x * 16 + (threadIdx.x >> 4), h = blockIdx.y, c = threadIdx.x & 15;
   const int64_t b = blockIdx.z;
-  float d = 0.0f, l = INFINITY;
+  float d = 0.0f, l = -INFINITY;
   if (i < a.Sq) {
     const uint4 o = *reinterpret_cast<const uint4*>(a.out + b * a.so.b + i * a.so.s + h * a.so.h + c * 8);
     const uint4 g = *reinterpret_cast<const uint4*>(a.dout + b * a.sd.b + i * a.sd.s + h * a.sd.h + c * 8);
     d = dot8(o, g);
-    l = a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Sq + i] * kLog2e;
-    if (l == -INFINITY) l = INFINITY;
+    l = a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Sq + i] * -kLog2e;
+    if (l == INFINITY) l = -INFINITY;
   }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (c == 0 && i < a.padded) {
     const size_t at = (static_cast<size_t>(b) * a.Hq + h) * a.padded + i;
-    a.delta[at] = d;
+    a.delta[at] = -d;
     a.lse2[at] = l;
   }
 }
@@ -88,15 +89,17 @@ constexpr int kThreads = 384;
 constexpr int kWarpLoad = 8, kWarpX = 9, kWarpY = 10;     // warps 0-7: elementwise work
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescKK = idesc_bf16_f32(128, 128, 0, 0);   // A and B K-major
+constexpr uint32_t kIdescKK64 = idesc_bf16_f32(128, 64, 0, 0);  // 64 rows of B
 constexpr uint32_t kIdescKM = idesc_bf16_f32(128, 128, 0, 1);   // A K-major (TMEM), B MN-major
 
 struct Smem {
   uint8_t own[2][kTileBytes];                // dkv: K, V; dq: Q, dO
   uint8_t ring_a[2][kTileBytes];             // dkv: Q; dq: K
   uint8_t ring_b[2][kTileBytes];             // dkv: dO; dq: V
-  float lse2[2][kRows], delta[2][kRows];     // dkv: of the Q stage's rows
+  float lse2[2][kRows], delta[2][kRows];     // dkv: of the Q stage's rows, negated
   uint64_t own_full, a_full[2], a_empty[2], b_full[2], b_empty[2];
-  uint64_t s_full, s_done, dp_full, ds_done, acc[2], drain[2];
+  uint64_t s_full[2], s_done[2], dp_full[2], ds_done[2];   // dkv: per half of the query columns; dq: [0]
+  uint64_t acc[2], drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -106,7 +109,7 @@ struct Args {
   Clean clean_a, clean_b;                    // of ring_a's and ring_b's tensors, or null
   int32_t a_h, a_b, b_h, b_b;                // 1: the map has that dimension, 0: broadcast
   int32_t o1_h, o1_b, o2_h, o2_b;            // the same of the block's own two tensors
-  const float *lse2, *delta;                 // [B][Hq][padded]
+  const float *lse2, *delta;                 // [B][Hq][padded], negated
   int32_t padded, nqt;
   const int32_t *count, *list;               // visible tiles of the other side, or null
   uint16_t *out1, *out2;                     // dkv: dk, dv; dq: dq
@@ -126,23 +129,26 @@ __device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t& bar, uint32_t pari
   return __all_sync(0xffffffffu, bounded_wait(sm, bar, parity, err));
 }
 
-// D (+)= A B^T over 128 channels, both K-major tiles in shared memory (32 B per
-// K step inside a swizzled row, d halves 16 KB apart).
-__device__ __forceinline__ void product_kk(uint32_t d, const uint8_t* x, const uint8_t* y) {
-  const uint64_t xd = smem_desc_sw128(smem_u32(x), 16, 1024), yd = smem_desc_sw128(smem_u32(y), 16, 1024);
+// D = A B^T over 128 channels, both K-major tiles in shared memory (32 B per K step
+// inside a swizzled row, d halves 16 KB apart): all 128 rows of B, or with `half`
+// >= 0 the 64 of one half (8 KB apart) into D's columns 64 half.
+__device__ __forceinline__ void product_kk(uint32_t d, const uint8_t* x, const uint8_t* y, int half) {
+  const uint64_t xd = smem_desc_sw128(smem_u32(x), 16, 1024);
+  const uint64_t yd = smem_desc_sw128(smem_u32(y) + 8192 * max(half, 0), 16, 1024);
+  const uint32_t to = d + 64 * max(half, 0), idesc = half < 0 ? kIdescKK : kIdescKK64;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    umma_ss(d, xd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, yd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kIdescKK,
+    umma_ss(to, xd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, yd + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, idesc,
             kk > 0 ? 1u : 0u);
 }
 
-// D += A B over 128 rows of B (MN-major: 16 rows = 2 KB per K step, d halves 16 KB
-// apart); A in TMEM as bf16 pairs, 8 columns per K step, rows 64-127 at `half`.
-__device__ __forceinline__ void product_km(uint32_t d, uint32_t x, int half, const uint8_t* y, bool add) {
-  const uint64_t yd = smem_desc_sw128(smem_u32(y), 16384, 1024);
+// D += A B over 64 rows of B from row 64 half (MN-major: 16 rows = 2 KB per K step, d
+// halves 16 KB apart); A in TMEM as bf16 pairs, 8 columns per K step.
+__device__ __forceinline__ void product_km(uint32_t d, uint32_t x, const uint8_t* y, int half, bool add) {
+  const uint64_t yd = smem_desc_sw128(smem_u32(y) + 8192 * half, 16384, 1024);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_ts(d, x + (kk >> 2) * half + (kk & 3) * 8, yd + kk * (2048 >> 4), kIdescKM, add || kk > 0 ? 1u : 0u);
+  for (int kk = 0; kk < 4; ++kk)
+    umma_ts(d, x + kk * 8, yd + kk * (2048 >> 4), kIdescKM, add || kk > 0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int row, int h, int b, uint64_t& bar) {
@@ -177,8 +183,9 @@ __device__ __forceinline__ void write_half_row(uint32_t taddr, bool have, float 
   }
 }
 
+// Barriers and TMEM; `warps` elementwise warps arrive per score buffer.
 template <class Init>
-__device__ __forceinline__ uint32_t set_up(Smem& sm, Init init) {
+__device__ __forceinline__ uint32_t set_up(Smem& sm, int warps, Init init) {
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sm.own_full), 1);
     for (int i = 0; i < 2; ++i) {
@@ -188,10 +195,12 @@ __device__ __forceinline__ uint32_t set_up(Smem& sm, Init init) {
       mbar_init(smem_u32(&sm.acc[i]), 1);
       mbar_init(smem_u32(&sm.drain[i]), 1);
     }
-    mbar_init(smem_u32(&sm.s_full), 1);
-    mbar_init(smem_u32(&sm.s_done), 8);
-    mbar_init(smem_u32(&sm.dp_full), 1);
-    mbar_init(smem_u32(&sm.ds_done), 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_done[i]), warps);
+      mbar_init(smem_u32(&sm.dp_full[i]), 1);
+      mbar_init(smem_u32(&sm.ds_done[i]), warps);
+    }
     init();
     sm.abort = 0;
     fence_mbar_init();
@@ -215,25 +224,52 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
   }
 }
 
-// Scores of 32 columns in place -> P against `ref` (one value, or one per
-// column), and into `w` P times the cap's derivative.
+// Scores of 32 columns in place -> P against `ref` (minus lse in log2 units, a pair
+// of columns at a time), and into `w` P times the cap's derivative. A quarter of
+// the exponentials go to the FMA pipe.
 template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const Problem& p, float c, float slope,
                                               float d0, float dir, Ref ref) {
   const float cap2 = kCap ? p.cap * kLog2e : 0.0f, in2 = kCap ? 2.0f * c / p.cap : 0.0f;
+  const uint64_t c2 = kCap || kBias ? pack_f32x2(1.0f, 1.0f) : pack_f32x2(c, c);
 #pragma unroll
-  for (int u = 0; u < 32; ++u) {
-    float s = x[u], t = 0.0f;
-    if constexpr (kCap) {
-      t = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(s * in2)), 1.0f);
-      s = cap2 * t;
-    } else if constexpr (kBias) {
-      s *= c;
+  for (int u = 0; u < 32; u += 2) {
+    float t[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float s = x[u + i];
+      if constexpr (kCap) {
+        t[i] = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(s * in2)), 1.0f);
+        s = cap2 * t[i];
+      } else if constexpr (kBias) {
+        s *= c;
+      }
+      if constexpr (kBias) s = fmaf(-slope, fabsf(fmaf(dir, static_cast<float>(u + i), d0)), s);
+      x[u + i] = s;
     }
-    if constexpr (kBias) s = fmaf(-slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), s);
-    const float e = ex2_approx(kCap || kBias ? s - ref(u) : fmaf(s, c, -ref(u)));
-    x[u] = e;
-    w[u] = kCap ? e * fmaf(-t, t, 1.0f) : e;
+    const uint64_t arg = fma_f32x2(pack_f32x2(x[u], x[u + 1]), c2, ref(u));
+    float e0, e1;
+    if (u % 8 == 4) {
+      ex2_poly_f32x2(arg, e0, e1);
+    } else {
+      unpack_f32x2(arg, e0, e1);
+      e0 = ex2_approx(e0);
+      e1 = ex2_approx(e1);
+    }
+    x[u] = e0;
+    x[u + 1] = e1;
+    w[u] = kCap ? e0 * fmaf(-t[0], t[0], 1.0f) : e0;
+    w[u + 1] = kCap ? e1 * fmaf(-t[1], t[1], 1.0f) : e1;
+  }
+}
+
+// x = w (x - delta), delta as minus a pair of columns at a time.
+template <class Ref>
+__device__ __forceinline__ void score_gradients(float (&x)[32], const float (&w)[32], Ref minus_delta) {
+#pragma unroll
+  for (int u = 0; u < 32; u += 2) {
+    const uint64_t d = add_f32x2(pack_f32x2(x[u], x[u + 1]), minus_delta(u));
+    unpack_f32x2(mul_f32x2(pack_f32x2(w[u], w[u + 1]), d), x[u], x[u + 1]);
   }
 }
 
@@ -255,7 +291,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
   const int per = p.Hk * p.B, kt = blockIdx.x / per;       // early key tiles, the longest under a causal mask, first
   const int hk = blockIdx.x % per % p.Hk, b = blockIdx.x % per / p.Hk;
   const int k0 = kt * kRows;
-  const uint32_t tmem = set_up(sm, [&] {
+  const uint32_t tmem = set_up(sm, 4, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 2);                // dO is read by dP^T and by dV
     mbar_init(smem_u32(&sm.b_empty[1]), 2);
   });
@@ -312,33 +348,47 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     }
     __syncwarp();
   } else if (warp == kWarpX || warp == kWarpY) {
+    // X: S^T (reads Q) and dV (reads dO); Y: dP^T (reads dO) and dK (reads Q). The
+    // two halves of the query columns are pipelines of their own: the next scores
+    // of a half follow its accumulation, while the other half's warps work. (With
+    // all 128 columns at once the elementwise warps waited 1000 of 4150 cycles a
+    // step for dV and the next S^T.)
     const bool x = warp == kWarpX;
-    if (lane == 0 && n > 0) {
-      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
-      uint64_t* src_full = x ? sm.a_full : sm.b_full;      // S^T reads Q, dP^T reads dO
-      auto scores = [&](int j) {
+    if (n > 0) {
+      bool ok = warp_wait(sm, sm.own_full, 0, a.err);
+      uint64_t* src_full = x ? sm.a_full : sm.b_full;
+      uint64_t* other_full = x ? sm.b_full : sm.a_full;
+      const uint32_t ts = tmem + (x ? kColS : kColDp), to = tmem + (x ? kColDv : kColDk);
+      auto scores = [&](int j, int half) {
         const int st = j & 1;
-        if (!bounded_wait(sm, src_full[st], (j / 2) & 1, a.err)) return false;
+        if (half == 0 && !warp_wait(sm, src_full[st], (j / 2) & 1, a.err)) return false;
         tc_fence_after();
-        product_kk(tmem + (x ? kColS : kColDp), sm.own[x ? 0 : 1], x ? sm.ring_a[st] : sm.ring_b[st]);
-        umma_commit(smem_u32(x ? &sm.s_full : &sm.dp_full));
-        if (!x) umma_commit(smem_u32(&sm.b_empty[st]));
+        if (elect_one()) {
+          product_kk(ts, sm.own[x ? 0 : 1], x ? sm.ring_a[st] : sm.ring_b[st], half);
+          umma_commit(smem_u32(x ? &sm.s_full[half] : &sm.dp_full[half]));
+          if (!x && half == 1) umma_commit(smem_u32(&sm.b_empty[st]));
+        }
+        __syncwarp();
         return true;
       };
-      if (ok) ok = scores(0);
+      if (ok) ok = scores(0, 0) && scores(0, 1);
       for (int j = 0; ok && j < n; ++j) {
         const int st = j & 1;
-        uint64_t* other_full = x ? sm.b_full : sm.a_full;  // dV reads dO, dK reads Q
-        if (!(ok = bounded_wait(sm, other_full[st], (j / 2) & 1, a.err))) break;
-        if (!(ok = bounded_wait(sm, x ? sm.s_done : sm.ds_done, j & 1, a.err))) break;
-        tc_fence_after();
-        product_km(tmem + (x ? kColDv : kColDk), tmem + (x ? kColS : kColDp), 64, x ? sm.ring_b[st] : sm.ring_a[st],
-                   j > 0);
-        umma_commit(smem_u32(x ? &sm.b_empty[st] : &sm.a_empty[st]));
-        if (j + 1 < n) ok = scores(j + 1);
-        else umma_commit(smem_u32(&sm.acc[x ? 0 : 1]));
+        if (!(ok = warp_wait(sm, other_full[st], (j / 2) & 1, a.err))) break;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = warp_wait(sm, x ? sm.s_done[half] : sm.ds_done[half], j & 1, a.err))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            product_km(to, ts + 64 * half, x ? sm.ring_b[st] : sm.ring_a[st], half, j > 0 || half > 0);
+            if (half == 1) umma_commit(smem_u32(x ? &sm.b_empty[st] : &sm.a_empty[st]));
+            if (half == 1 && j + 1 == n) umma_commit(smem_u32(&sm.acc[x ? 0 : 1]));
+          }
+          __syncwarp();
+          if (j + 1 < n && !(ok = scores(j + 1, half))) break;
+        }
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         umma_commit(smem_u32(&sm.drain[x ? 0 : 1]));
         mbar_wait(smem_u32(&sm.drain[x ? 0 : 1]), 0, nullptr, kDrainNs);
       }
@@ -355,9 +405,10 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     const int doc = p.documents && key < p.Sk ? p.doc_k[b * p.doc_k_sb + key] : -1;
     const int32_t* dq = p.documents ? p.doc_q + b * p.doc_q_sb : nullptr;
     bool ok = true;
-    int j = 0;
-    for (; j < n; ++j) {
-      const int st = j & 1, g = j / len, idx = j - g * len, h = hk * p.group + g;
+    int h = hk * p.group, idx = 0;
+    for (int j = 0; j < n; ++j, ++idx) {
+      if (idx == len) idx = 0, ++h;
+      const int st = j & 1;
       const int rec = list ? list[idx] : first + idx;
       const int qt = rec & kTileMask, q0 = qt * kRows;
       const bool part_doc = rec & kPartial0;
@@ -370,7 +421,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       }
       const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
       if (!(ok = warp_wait(sm, sm.a_full[st], (j / 2) & 1, a.err))) break;     // lse and D
-      if (!(ok = warp_wait(sm, sm.s_full, j & 1, a.err))) break;
+      if (!(ok = warp_wait(sm, sm.s_full[half], j & 1, a.err))) break;
       tc_fence_after();
       // visible columns of chunk q2 as a bit mask; only where some pair is hidden
       uint32_t see[2] = {0xffffffffu, 0xffffffffu};
@@ -400,7 +451,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
         tmem_wait_ld32(x);
         const float* lse = sm.lse2[st] + 64 * half + 32 * q2;
         const float d0 = static_cast<float>(q0 + p.off + 64 * half + 32 * q2 - key);
-        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, 1.0f, [&](int u) { return lse[u]; });
+        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, 1.0f, [&](int u) { return *reinterpret_cast<const uint64_t*>(lse + u); });
         if (partial) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
@@ -419,8 +470,8 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.s_done));
-      if (!(ok = warp_wait(sm, sm.dp_full, j & 1, a.err))) break;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[half]));
+      if (!(ok = warp_wait(sm, sm.dp_full[half], j & 1, a.err))) break;
       tc_fence_after();
 #pragma unroll
       for (int q2 = 0; q2 < 2; ++q2) {
@@ -428,8 +479,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
         tmem_ld32x32f(tp + 32 * q2, x);
         tmem_wait_ld32(x);
         const float* dl = sm.delta[st] + 64 * half + 32 * q2;
-#pragma unroll
-        for (int u = 0; u < 32; ++u) x[u] = w[q2][u] * (x[u] - dl[u]);
+        score_gradients(x, w[q2], [&](int u) { return *reinterpret_cast<const uint64_t*>(dl + u); });
         if (partial) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
@@ -442,7 +492,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[half]));
     }
     if (ok && n > 0) {
       ok = warp_wait(sm, sm.acc[0], 0, a.err) && warp_wait(sm, sm.acc[1], 0, a.err);
@@ -477,7 +527,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
   const int per = p.Hq * p.B, qt = a.nqt - 1 - blockIdx.x / per;   // late query tiles first
   const int h = blockIdx.x % per % p.Hq, b = blockIdx.x % per / p.Hq, hk = h / p.group;
   const int q0 = qt * kRows;
-  const uint32_t tmem = set_up(sm, [&] {
+  const uint32_t tmem = set_up(sm, 8, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 1);
     mbar_init(smem_u32(&sm.b_empty[1]), 1);
   });
@@ -519,45 +569,59 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     }
     __syncwarp();
   } else if (warp == kWarpX) {
-    if (lane == 0 && n > 0) {
-      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
+    if (n > 0) {
+      bool ok = warp_wait(sm, sm.own_full, 0, a.err);
       for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = bounded_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
-        if (j > 0 && !(ok = bounded_wait(sm, sm.s_done, (j - 1) & 1, a.err))) break;    // S(j - 1) was read
+        if (!(ok = warp_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        if (j > 0 && !(ok = warp_wait(sm, sm.s_done[0], (j - 1) & 1, a.err))) break;    // S(j - 1) was read
         tc_fence_after();
-        product_kk(tmem + kColS, sm.own[0], sm.ring_a[j & 1]);
-        umma_commit(smem_u32(&sm.s_full));
+        if (elect_one()) {
+          product_kk(tmem + kColS, sm.own[0], sm.ring_a[j & 1], -1);
+          umma_commit(smem_u32(&sm.s_full[0]));
+        }
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         umma_commit(smem_u32(&sm.drain[0]));
         mbar_wait(smem_u32(&sm.drain[0]), 0, nullptr, kDrainNs);
       }
     }
     __syncwarp();
   } else if (warp == kWarpY) {
-    if (lane == 0 && n > 0) {
-      bool ok = bounded_wait(sm, sm.own_full, 0, a.err);
+    if (n > 0) {
+      bool ok = warp_wait(sm, sm.own_full, 0, a.err);
       auto dp = [&](int j) {
-        if (!bounded_wait(sm, sm.b_full[j & 1], (j / 2) & 1, a.err)) return false;
+        if (!warp_wait(sm, sm.b_full[j & 1], (j / 2) & 1, a.err)) return false;
         tc_fence_after();
-        product_kk(tmem + kColDp, sm.own[1], sm.ring_b[j & 1]);
-        umma_commit(smem_u32(&sm.dp_full));
-        umma_commit(smem_u32(&sm.b_empty[j & 1]));
+        if (elect_one()) {
+          product_kk(tmem + kColDp, sm.own[1], sm.ring_b[j & 1], -1);
+          umma_commit(smem_u32(&sm.dp_full[0]));
+          umma_commit(smem_u32(&sm.b_empty[j & 1]));
+        }
+        __syncwarp();
         return true;
       };
       if (ok) ok = dp(0);
       for (int j = 0; ok && j < n; ++j) {
         // dS(j) written means dP(j) read; dP(j + 1) goes first, so that the next
         // elementwise step waits for one product only
-        if (!(ok = bounded_wait(sm, sm.ds_done, j & 1, a.err))) break;
+        if (!(ok = warp_wait(sm, sm.ds_done[0], j & 1, a.err))) break;
         tc_fence_after();
         if (j + 1 < n && !(ok = dp(j + 1))) break;
-        if (!(ok = bounded_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
-        product_km(tmem + kColDq, tmem + kColDs + 64 * (j & 1), 32, sm.ring_a[j & 1], j > 0);
-        umma_commit(smem_u32(&sm.a_empty[j & 1]));
+        if (!(ok = warp_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        if (elect_one()) {
+          const uint32_t ds = tmem + kColDs + 64 * (j & 1);
+          product_km(tmem + kColDq, ds, sm.ring_a[j & 1], 0, j > 0);
+          product_km(tmem + kColDq, ds + 32, sm.ring_a[j & 1], 1, true);
+          umma_commit(smem_u32(&sm.a_empty[j & 1]));
+          if (j + 1 == n) umma_commit(smem_u32(&sm.acc[0]));
+        }
+        __syncwarp();
       }
-      umma_commit(smem_u32(ok ? &sm.acc[0] : &sm.drain[1]));
-      if (!ok) mbar_wait(smem_u32(&sm.drain[1]), 0, nullptr, kDrainNs);
+      if (!ok && elect_one()) {
+        umma_commit(smem_u32(&sm.drain[1]));
+        mbar_wait(smem_u32(&sm.drain[1]), 0, nullptr, kDrainNs);
+      }
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -567,7 +631,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t ts = lane_addr + kColS + 64 * half, tp = lane_addr + kColDp + 64 * half;
     const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + q0 + quad * 32 + lane;
-    const float lse2 = a.lse2[at], delta = a.delta[at];
+    const uint64_t lse2 = pack_f32x2(a.lse2[at], a.lse2[at]), minus_delta = pack_f32x2(a.delta[at], a.delta[at]);
     const float c = p.scale * kLog2e, slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
     const int lim = p.limit(b, i_q), lim0 = p.limit(b, q0);
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
@@ -599,7 +663,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
         }
       }
       const uint32_t bb[2] = {half ? bm.z : bm.x, half ? bm.w : bm.y};
-      if (!(ok = warp_wait(sm, sm.s_full, j & 1, a.err))) break;
+      if (!(ok = warp_wait(sm, sm.s_full[0], j & 1, a.err))) break;
       tc_fence_after();
       float w[2][32];
 #pragma unroll
@@ -610,20 +674,19 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
         if (q2 == 1) {                                     // S(j) is in registers: S(j + 1) may replace it
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.s_done));
+          if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
         }
         const float d0 = static_cast<float>(i_q + p.off - k0 - 64 * half - 32 * q2);
         probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, -1.0f, [&](int) { return lse2; });
       }
-      if (!(ok = warp_wait(sm, sm.dp_full, j & 1, a.err))) break;
+      if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
       tc_fence_after();
 #pragma unroll
       for (int q2 = 0; q2 < 2; ++q2) {
         float x[32];
         tmem_ld32x32f(tp + 32 * q2, x);
         tmem_wait_ld32(x);
-#pragma unroll
-        for (int u = 0; u < 32; ++u) x[u] = w[q2][u] * (x[u] - delta);
+        score_gradients(x, w[q2], [&](int) { return minus_delta; });
         if (partial) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
@@ -641,7 +704,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[0]));
     }
     if (ok && n > 0) {
       ok = warp_wait(sm, sm.acc[0], 0, a.err);
