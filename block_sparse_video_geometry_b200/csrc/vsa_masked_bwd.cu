@@ -21,7 +21,8 @@
 //    dP^T into dS^T while dV and the next S^T run.
 //  * dq_kernel: a block owns 128 queries of a head (lane = query) and walks the
 //    key tiles: S = Q K^T, dP = dO V^T, dQ += dS K, dS in two buffers of its own.
-// Both read their tiles by TMA, two stages each. D and lse in log2 units come from
+// Both read their tiles by TMA, three stages of the tensor that is used from the
+// scores to the accumulation, two of the other. D and lse in log2 units come from
 // prepare_kernel, negated; rows without visible keys get -inf there, so that P = 0.
 // Every wait is bounded (see vsa_masked_attn_status).
 
@@ -92,12 +93,14 @@ constexpr uint32_t kIdescKK = idesc_bf16_f32(128, 128, 0, 0);   // A and B K-maj
 constexpr uint32_t kIdescKK64 = idesc_bf16_f32(128, 64, 0, 0);  // 64 rows of B
 constexpr uint32_t kIdescKM = idesc_bf16_f32(128, 128, 0, 1);   // A K-major (TMEM), B MN-major
 
+constexpr int kStagesA = 3;
+
 struct Smem {
   uint8_t own[2][kTileBytes];                // dkv: K, V; dq: Q, dO
-  uint8_t ring_a[2][kTileBytes];             // dkv: Q; dq: K
+  uint8_t ring_a[kStagesA][kTileBytes];      // dkv: Q; dq: K (held from the scores to the accumulation)
   uint8_t ring_b[2][kTileBytes];             // dkv: dO; dq: V
-  float lse2[2][kRows], delta[2][kRows];     // dkv: of the Q stage's rows, negated
-  uint64_t own_full, a_full[2], a_empty[2], b_full[2], b_empty[2];
+  float lse2[2][kRows], delta[2][kRows];     // dkv: of the query tile's rows, negated
+  uint64_t own_full, a_full[kStagesA], a_empty[kStagesA], b_full[2], b_empty[2], rows_full[2];
   uint64_t s_full[2], s_done[2], dp_full[2], ds_done[2];   // dkv: per half of the query columns; dq: [0]
   uint64_t acc[2], drain[2];
   uint32_t tmem_base;
@@ -126,6 +129,7 @@ __device__ __forceinline__ bool bounded_wait(Smem& sm, uint64_t& bar, uint32_t p
   return ok;
 }
 __device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&bar), parity))) return true;
   return __all_sync(0xffffffffu, bounded_wait(sm, bar, parity, err));
 }
 
@@ -188,10 +192,13 @@ template <class Init>
 __device__ __forceinline__ uint32_t set_up(Smem& sm, int warps, Init init) {
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sm.own_full), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStagesA; ++i) {
       mbar_init(smem_u32(&sm.a_full[i]), 1);
       mbar_init(smem_u32(&sm.a_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.b_full[i]), 1);
+      mbar_init(smem_u32(&sm.rows_full[i]), 1);
       mbar_init(smem_u32(&sm.acc[i]), 1);
       mbar_init(smem_u32(&sm.drain[i]), 1);
     }
@@ -316,33 +323,42 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       mbar_arrive_expect_tx(smem_u32(&sm.own_full), 2 * kTileBytes);
       load_tile(sm.own[0], &map_k, k0, a.o1_h ? hk : 0, a.o1_b ? b : 0, sm.own_full);
       load_tile(sm.own[1], &map_v, k0, a.o2_h ? hk : 0, a.o2_b ? b : 0, sm.own_full);
-      int j = 0;
-      for (; ok && j < n; ++j) {
-        const int st = j & 1, g = j / len, idx = j - g * len, h = hk * p.group + g;
+      int j = 0, h = hk * p.group, idx = 0;
+      size_t last = 0;                                     // rows of the tile before
+      for (; j <= n; ++j, ++idx) {
+        if (idx == len) idx = 0, ++h;
+        const int sa = j % kStagesA, sb = j & 1;
+        if (j >= kStagesA && !(ok = bounded_wait(sm, sm.a_empty[sa], (j / kStagesA - 1) & 1, a.err))) break;
+        if (j > 0) {
+          // lse and D of tile j - 1 over those of j - 3: that step has ended (its Q stage is free)
+          const uint32_t bar = smem_u32(&sm.rows_full[sb ^ 1]);
+          mbar_arrive_expect_tx(bar, 2 * kRows * 4);
+          bulk_load(smem_u32(sm.lse2[sb ^ 1]), a.lse2 + last, kRows * 4, bar);
+          bulk_load(smem_u32(sm.delta[sb ^ 1]), a.delta + last, kRows * 4, bar);
+        }
+        if (j == n) break;
         const int qt = (list ? list[idx] : first + idx) & kTileMask;
         const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
-        if (j >= 2 && !(ok = bounded_wait(sm, sm.a_empty[st], (j / 2 - 1) & 1, a.err))) break;
+        last = (static_cast<size_t>(b) * p.Hq + h) * a.padded + qt * kRows;
         const bool bad_q = a.clean_a.bad && any(a.clean_a.bad[tile]);
-        mbar_arrive_expect_tx(smem_u32(&sm.a_full[st]), kTileBytes + 2 * kRows * 4);
-        load_tile(sm.ring_a[st], bad_q ? &map_qc : &map_q, qt * kRows, bad_q || a.a_h ? h : 0, bad_q || a.a_b ? b : 0,
-                  sm.a_full[st]);
-        const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + qt * kRows;
-        bulk_load(smem_u32(sm.lse2[st]), a.lse2 + at, kRows * 4, smem_u32(&sm.a_full[st]));
-        bulk_load(smem_u32(sm.delta[st]), a.delta + at, kRows * 4, smem_u32(&sm.a_full[st]));
-        if (j >= 2 && !(ok = bounded_wait(sm, sm.b_empty[st], (j / 2 - 1) & 1, a.err))) {
+        mbar_arrive_expect_tx(smem_u32(&sm.a_full[sa]), kTileBytes);
+        load_tile(sm.ring_a[sa], bad_q ? &map_qc : &map_q, qt * kRows, bad_q || a.a_h ? h : 0, bad_q || a.a_b ? b : 0,
+                  sm.a_full[sa]);
+        if (j >= 2 && !(ok = bounded_wait(sm, sm.b_empty[sb], (j / 2 - 1) & 1, a.err))) {
           ++j;                                             // its Q is in flight; its dO is not
           break;
         }
         const bool bad_o = a.clean_b.bad && any(a.clean_b.bad[tile]);
-        mbar_arrive_expect_tx(smem_u32(&sm.b_full[st]), kTileBytes);
-        load_tile(sm.ring_b[st], bad_o ? &map_oc : &map_o, qt * kRows, bad_o || a.b_h ? h : 0, bad_o || a.b_b ? b : 0,
-                  sm.b_full[st]);
+        mbar_arrive_expect_tx(smem_u32(&sm.b_full[sb]), kTileBytes);
+        load_tile(sm.ring_b[sb], bad_o ? &map_oc : &map_o, qt * kRows, bad_o || a.b_h ? h : 0, bad_o || a.b_b ? b : 0,
+                  sm.b_full[sb]);
       }
       if (!ok || n == 0) {                                 // every issued copy lands before the block exits
         mbar_wait(smem_u32(&sm.own_full), 0, nullptr, kDrainNs);
-        for (int i = max(0, j - 3); i < j; ++i) {
-          mbar_wait(smem_u32(&sm.a_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+        for (int i = max(0, j - 4); i < j; ++i) {
+          mbar_wait(smem_u32(&sm.a_full[i % kStagesA]), (i / kStagesA) & 1, nullptr, kDrainNs);
           mbar_wait(smem_u32(&sm.b_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+          mbar_wait(smem_u32(&sm.rows_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
         }
       }
     }
@@ -356,32 +372,34 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     const bool x = warp == kWarpX;
     if (n > 0) {
       bool ok = warp_wait(sm, sm.own_full, 0, a.err);
-      uint64_t* src_full = x ? sm.a_full : sm.b_full;
-      uint64_t* other_full = x ? sm.b_full : sm.a_full;
+      auto q_stage = [&](int j) { return sm.ring_a[j % kStagesA]; };
+      auto o_stage = [&](int j) { return sm.ring_b[j & 1]; };
+      auto landed = [&](bool q, int j) {
+        return q ? warp_wait(sm, sm.a_full[j % kStagesA], (j / kStagesA) & 1, a.err)
+                 : warp_wait(sm, sm.b_full[j & 1], (j / 2) & 1, a.err);
+      };
       const uint32_t ts = tmem + (x ? kColS : kColDp), to = tmem + (x ? kColDv : kColDk);
       auto scores = [&](int j, int half) {
-        const int st = j & 1;
-        if (half == 0 && !warp_wait(sm, src_full[st], (j / 2) & 1, a.err)) return false;
+        if (half == 0 && !landed(x, j)) return false;
         tc_fence_after();
         if (elect_one()) {
-          product_kk(ts, sm.own[x ? 0 : 1], x ? sm.ring_a[st] : sm.ring_b[st], half);
+          product_kk(ts, sm.own[x ? 0 : 1], x ? q_stage(j) : o_stage(j), half);
           umma_commit(smem_u32(x ? &sm.s_full[half] : &sm.dp_full[half]));
-          if (!x && half == 1) umma_commit(smem_u32(&sm.b_empty[st]));
+          if (!x && half == 1) umma_commit(smem_u32(&sm.b_empty[j & 1]));
         }
         __syncwarp();
         return true;
       };
       if (ok) ok = scores(0, 0) && scores(0, 1);
       for (int j = 0; ok && j < n; ++j) {
-        const int st = j & 1;
-        if (!(ok = warp_wait(sm, other_full[st], (j / 2) & 1, a.err))) break;
+        if (!(ok = landed(!x, j))) break;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           if (!(ok = warp_wait(sm, x ? sm.s_done[half] : sm.ds_done[half], j & 1, a.err))) break;
           tc_fence_after();
           if (elect_one()) {
-            product_km(to, ts + 64 * half, x ? sm.ring_b[st] : sm.ring_a[st], half, j > 0 || half > 0);
-            if (half == 1) umma_commit(smem_u32(x ? &sm.b_empty[st] : &sm.a_empty[st]));
+            product_km(to, ts + 64 * half, x ? o_stage(j) : q_stage(j), half, j > 0 || half > 0);
+            if (half == 1) umma_commit(smem_u32(x ? &sm.b_empty[j & 1] : &sm.a_empty[j % kStagesA]));
             if (half == 1 && j + 1 == n) umma_commit(smem_u32(&sm.acc[x ? 0 : 1]));
           }
           __syncwarp();
@@ -413,14 +431,14 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       const int qt = rec & kTileMask, q0 = qt * kRows;
       const bool part_doc = rec & kPartial0;
       const bool partial = part_doc || (p.causal && prefix < k0 + kRows && q0 + p.off < k0 + kRows - 1);
-      const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
       uint4 bm = make_uint4(0, 0, 0, 0);
       if (a.clean_a.bad) {
+        const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
         const uint4 m1 = a.clean_a.bad[tile], m2 = a.clean_b.bad[tile];
         bm = make_uint4(m1.x | m2.x, m1.y | m2.y, m1.z | m2.z, m1.w | m2.w);
       }
       const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
-      if (!(ok = warp_wait(sm, sm.a_full[st], (j / 2) & 1, a.err))) break;     // lse and D
+      if (!(ok = warp_wait(sm, sm.rows_full[st], (j / 2) & 1, a.err))) break;
       if (!(ok = warp_wait(sm, sm.s_full[half], j & 1, a.err))) break;
       tc_fence_after();
       // visible columns of chunk q2 as a bit mask; only where some pair is hidden
@@ -546,23 +564,23 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
       load_tile(sm.own[1], &map_o, q0, a.o2_h ? h : 0, a.o2_b ? b : 0, sm.own_full);
       int j = 0;
       for (; ok && j < n; ++j) {
-        const int st = j & 1, kt = (list ? list[j] : j) & kTileMask;
+        const int st = j & 1, sa = j % kStagesA, kt = (list ? list[j] : j) & kTileMask;
         if (j >= 2 && !(ok = bounded_wait(sm, sm.b_empty[st], (j / 2 - 1) & 1, a.err))) break;
         mbar_arrive_expect_tx(smem_u32(&sm.b_full[st]), kTileBytes);
         load_tile(sm.ring_b[st], &map_v, kt * kRows, a.b_h ? hk : 0, a.b_b ? b : 0, sm.b_full[st]);
-        if (j >= 2 && !(ok = bounded_wait(sm, sm.a_empty[st], (j / 2 - 1) & 1, a.err))) {
+        if (j >= kStagesA && !(ok = bounded_wait(sm, sm.a_empty[sa], (j / kStagesA - 1) & 1, a.err))) {
           ++j;
           break;
         }
         const bool bad_k = bad && any(bad[kt]);
-        mbar_arrive_expect_tx(smem_u32(&sm.a_full[st]), kTileBytes);
-        load_tile(sm.ring_a[st], bad_k ? &map_kc : &map_k, kt * kRows, bad_k || a.a_h ? hk : 0,
-                  bad_k || a.a_b ? b : 0, sm.a_full[st]);
+        mbar_arrive_expect_tx(smem_u32(&sm.a_full[sa]), kTileBytes);
+        load_tile(sm.ring_a[sa], bad_k ? &map_kc : &map_k, kt * kRows, bad_k || a.a_h ? hk : 0,
+                  bad_k || a.a_b ? b : 0, sm.a_full[sa]);
       }
       if (!ok || n == 0) {
         mbar_wait(smem_u32(&sm.own_full), 0, nullptr, kDrainNs);
-        for (int i = max(0, j - 3); i < j; ++i) {
-          mbar_wait(smem_u32(&sm.a_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
+        for (int i = max(0, j - 4); i < j; ++i) {
+          mbar_wait(smem_u32(&sm.a_full[i % kStagesA]), (i / kStagesA) & 1, nullptr, kDrainNs);
           mbar_wait(smem_u32(&sm.b_full[i & 1]), (i / 2) & 1, nullptr, kDrainNs);
         }
       }
@@ -572,11 +590,11 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     if (n > 0) {
       bool ok = warp_wait(sm, sm.own_full, 0, a.err);
       for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = warp_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        if (!(ok = warp_wait(sm, sm.a_full[j % kStagesA], (j / kStagesA) & 1, a.err))) break;
         if (j > 0 && !(ok = warp_wait(sm, sm.s_done[0], (j - 1) & 1, a.err))) break;    // S(j - 1) was read
         tc_fence_after();
         if (elect_one()) {
-          product_kk(tmem + kColS, sm.own[0], sm.ring_a[j & 1], -1);
+          product_kk(tmem + kColS, sm.own[0], sm.ring_a[j % kStagesA], -1);
           umma_commit(smem_u32(&sm.s_full[0]));
         }
         __syncwarp();
@@ -608,12 +626,12 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
         if (!(ok = warp_wait(sm, sm.ds_done[0], j & 1, a.err))) break;
         tc_fence_after();
         if (j + 1 < n && !(ok = dp(j + 1))) break;
-        if (!(ok = warp_wait(sm, sm.a_full[j & 1], (j / 2) & 1, a.err))) break;
+        if (!(ok = warp_wait(sm, sm.a_full[j % kStagesA], (j / kStagesA) & 1, a.err))) break;
         if (elect_one()) {
           const uint32_t ds = tmem + kColDs + 64 * (j & 1);
-          product_km(tmem + kColDq, ds, sm.ring_a[j & 1], 0, j > 0);
-          product_km(tmem + kColDq, ds + 32, sm.ring_a[j & 1], 1, true);
-          umma_commit(smem_u32(&sm.a_empty[j & 1]));
+          product_km(tmem + kColDq, ds, sm.ring_a[j % kStagesA], 0, j > 0);
+          product_km(tmem + kColDq, ds + 32, sm.ring_a[j % kStagesA], 1, true);
+          umma_commit(smem_u32(&sm.a_empty[j % kStagesA]));
           if (j + 1 == n) umma_commit(smem_u32(&sm.acc[0]));
         }
         __syncwarp();
