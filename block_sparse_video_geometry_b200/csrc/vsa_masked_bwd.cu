@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
 }
 
 // ------------------------------------------------------------------- shared
-constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpX = 9, kWarpY = 10;     // warps 0-7: elementwise work
+constexpr int kThreads = 608;
+constexpr int kEw = 16;                      // elementwise warps: four per lane quadrant, 32 columns each
+constexpr int kWarpLoad = kEw, kWarpX = kEw + 1, kWarpY = kEw + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescKK = idesc_bf16_f32(128, 128, 0, 0);   // A and B K-major
 constexpr uint32_t kIdescKK64 = idesc_bf16_f32(128, 64, 0, 0);  // 64 rows of B
@@ -148,11 +149,11 @@ __device__ __forceinline__ void product_kk(uint32_t d, const uint8_t* x, const u
 
 // D += A B over 64 rows of B from row 64 half (MN-major: 16 rows = 2 KB per K step, d
 // halves 16 KB apart); A in TMEM as bf16 pairs, 8 columns per K step.
-__device__ __forceinline__ void product_km(uint32_t d, uint32_t x, const uint8_t* y, int half, bool add) {
+__device__ __forceinline__ void product_km(uint32_t d, uint32_t x, int second, const uint8_t* y, int half, bool add) {
   const uint64_t yd = smem_desc_sw128(smem_u32(y) + 8192 * half, 16384, 1024);
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
-    umma_ts(d, x + kk * 8, yd + kk * (2048 >> 4), kIdescKM, add || kk > 0 ? 1u : 0u);
+    umma_ts(d, x + (kk >> 1) * second + (kk & 1) * 8, yd + kk * (2048 >> 4), kIdescKM, add || kk > 0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int row, int h, int b, uint64_t& bar) {
@@ -163,28 +164,23 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 
 __device__ __forceinline__ bool any(uint4 m) { return m.x | m.y | m.z | m.w; }
 
-// 64 columns of 32-bit sums times `f` as bf16 into a row (or zeros).
-__device__ __forceinline__ void write_half_row(uint32_t taddr, bool have, float f, bool live, uint16_t* row) {
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    float o[32];
-    __syncwarp();
-    if (have) {
-      tmem_ld32x32f(taddr + 32 * c, o);
-      tmem_wait_ld32(o);
-    } else {
+// 32 columns of 32-bit sums times `f` as bf16 into a row (or zeros).
+__device__ __forceinline__ void write_columns(uint32_t taddr, bool have, float f, bool live, uint16_t* row) {
+  float o[32];
+  __syncwarp();
+  if (have) {
+    tmem_ld32x32f(taddr, o);
+    tmem_wait_ld32(o);
+  } else {
 #pragma unroll
-      for (int u = 0; u < 32; ++u) o[u] = 0.0f;
-    }
-    if (live) {
-      uint4* dst = reinterpret_cast<uint4*>(row + 32 * c);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        dst[u] = make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
-                            pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f),
-                            pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
-    }
+    for (int u = 0; u < 32; ++u) o[u] = 0.0f;
   }
+  if (!live) return;
+  uint4* dst = reinterpret_cast<uint4*>(row);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    dst[u] = make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
+                        pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f), pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
 }
 
 // Barriers and TMEM; `warps` elementwise warps arrive per score buffer.
@@ -298,7 +294,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
   const int per = p.Hk * p.B, kt = blockIdx.x / per;       // early key tiles, the longest under a causal mask, first
   const int hk = blockIdx.x % per % p.Hk, b = blockIdx.x % per / p.Hk;
   const int k0 = kt * kRows;
-  const uint32_t tmem = set_up(sm, 4, [&] {
+  const uint32_t tmem = set_up(sm, kEw / 2, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 2);                // dO is read by dP^T and by dV
     mbar_init(smem_u32(&sm.b_empty[1]), 2);
   });
@@ -398,7 +394,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
           if (!(ok = warp_wait(sm, x ? sm.s_done[half] : sm.ds_done[half], j & 1, a.err))) break;
           tc_fence_after();
           if (elect_one()) {
-            product_km(to, ts + 64 * half, x ? o_stage(j) : q_stage(j), half, j > 0 || half > 0);
+            product_km(to, ts + 64 * half, 32, x ? o_stage(j) : q_stage(j), half, j > 0 || half > 0);
             if (half == 1) umma_commit(smem_u32(x ? &sm.b_empty[j & 1] : &sm.a_empty[j % kStagesA]));
             if (half == 1 && j + 1 == n) umma_commit(smem_u32(&sm.acc[x ? 0 : 1]));
           }
@@ -412,11 +408,11 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    const int quad = warp & 3, half = warp >> 2;           // 64 query columns per warp
+  } else if (warp < kEw) {
+    const int quad = warp & 3, part = warp >> 2, half = part >> 1;   // query columns [32 part, + 32)
     const int key = k0 + quad * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t ts = lane_addr + kColS + 64 * half, tp = lane_addr + kColDp + 64 * half;
+    const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
     const float c = p.scale * kLog2e;
     // first query that sees this key by order
     const int i_min = !p.causal || key < prefix ? INT32_MIN : key - p.off;
@@ -428,85 +424,69 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       if (idx == len) idx = 0, ++h;
       const int st = j & 1;
       const int rec = list ? list[idx] : first + idx;
-      const int qt = rec & kTileMask, q0 = qt * kRows;
+      const int qt = rec & kTileMask, q0 = qt * kRows, i0 = q0 + 32 * part;
       const bool part_doc = rec & kPartial0;
       const bool partial = part_doc || (p.causal && prefix < k0 + kRows && q0 + p.off < k0 + kRows - 1);
-      uint4 bm = make_uint4(0, 0, 0, 0);
+      uint32_t bad = 0;                                    // columns whose q or dout holds an infinity or NaN
       if (a.clean_a.bad) {
         const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
-        const uint4 m1 = a.clean_a.bad[tile], m2 = a.clean_b.bad[tile];
-        bm = make_uint4(m1.x | m2.x, m1.y | m2.y, m1.z | m2.z, m1.w | m2.w);
+        bad = reinterpret_cast<const uint32_t*>(a.clean_a.bad + tile)[part] |
+              reinterpret_cast<const uint32_t*>(a.clean_b.bad + tile)[part];
       }
       const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+      // visible columns as a bit mask; only where some pair is hidden
+      uint32_t see = 0xffffffffu;
+      if (partial) {
+        see = 0;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) see |= (i0 + u >= i_min ? 1u : 0u) << u;
+        if (part_doc) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const int d = __ldg(dq + min(i0 + u, p.Sq - 1));
+            if (!(d == doc && d >= 0)) see &= ~(1u << u);
+          }
+        }
+      }
       if (!(ok = warp_wait(sm, sm.rows_full[st], (j / 2) & 1, a.err))) break;
       if (!(ok = warp_wait(sm, sm.s_full[half], j & 1, a.err))) break;
       tc_fence_after();
-      // visible columns of chunk q2 as a bit mask; only where some pair is hidden
-      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      float x[32], w[32];
+      uint32_t pw[16];
+      tmem_ld32x32f(ts, x);
+      tmem_wait_ld32(x);
+      const float* lse = sm.lse2[st] + 32 * part;
+      probabilities<kCap, kBias>(x, w, p, c, slope, static_cast<float>(i0 + p.off - key), 1.0f,
+                                 [&](int u) { return *reinterpret_cast<const uint64_t*>(lse + u); });
       if (partial) {
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) {
-          const int i0 = q0 + 64 * half + 32 * q2;
-          uint32_t m = 0;
-#pragma unroll
-          for (int u = 0; u < 32; ++u) m |= (i0 + u >= i_min ? 1u : 0u) << u;
-          if (part_doc) {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int d = __ldg(dq + min(i0 + u, p.Sq - 1));
-              if (!(d == doc && d >= 0)) m &= ~(1u << u);
-            }
-          }
-          see[q2] = m;
-        }
+        for (int u = 0; u < 32; ++u) x[u] = (see >> u) & 1u ? x[u] : 0.0f;
       }
-      const uint32_t bad[2] = {half ? bm.z : bm.x, half ? bm.w : bm.y};
-      float w[2][32];
+      if (bad) {
 #pragma unroll
-      for (int q2 = 0; q2 < 2; ++q2) {
-        float x[32];
-        tmem_ld32x32f(ts + 32 * q2, x);
-        tmem_wait_ld32(x);
-        const float* lse = sm.lse2[st] + 64 * half + 32 * q2;
-        const float d0 = static_cast<float>(q0 + p.off + 64 * half + 32 * q2 - key);
-        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, 1.0f, [&](int u) { return *reinterpret_cast<const uint64_t*>(lse + u); });
-        if (partial) {
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
-        }
-        if (bad[q2]) {
-#pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if ((bad[q2] & see[q2]) >> u & 1u) x[u] = w[q2][u] = NAN;
-        }
-        uint32_t pw[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
-        // queries 64 half + [32 q2, + 32): 16 columns of pairs, in this warp's own half of the scores
-        tmem_st32x16(ts + 16 * q2, pw);
+        for (int u = 0; u < 32; ++u)
+          if ((bad & see) >> u & 1u) x[u] = w[u] = NAN;
       }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+      tmem_st32x16(ts, pw);                                // over this warp's own columns
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[half]));
       if (!(ok = warp_wait(sm, sm.dp_full[half], j & 1, a.err))) break;
       tc_fence_after();
+      tmem_ld32x32f(tp, x);
+      tmem_wait_ld32(x);
+      const float* dl = sm.delta[st] + 32 * part;
+      score_gradients(x, w, [&](int u) { return *reinterpret_cast<const uint64_t*>(dl + u); });
+      if (partial) {
 #pragma unroll
-      for (int q2 = 0; q2 < 2; ++q2) {
-        float x[32];
-        tmem_ld32x32f(tp + 32 * q2, x);
-        tmem_wait_ld32(x);
-        const float* dl = sm.delta[st] + 64 * half + 32 * q2;
-        score_gradients(x, w[q2], [&](int u) { return *reinterpret_cast<const uint64_t*>(dl + u); });
-        if (partial) {
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
-        }
-        uint32_t pw[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
-        tmem_st32x16(tp + 16 * q2, pw);
+        for (int u = 0; u < 32; ++u) x[u] = (see >> u) & 1u ? x[u] : 0.0f;
       }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+      tmem_st32x16(tp, pw);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -519,10 +499,10 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     if (ok) {
       const bool live = key < p.Sk;
       const int64_t kk = live ? key : 0;
-      write_half_row(lane_addr + kColDk + 64 * half, n > 0, p.scale, live,
-                     a.out1 + b * a.so1.b + kk * a.so1.s + hk * a.so1.h + 64 * half);
-      write_half_row(lane_addr + kColDv + 64 * half, n > 0, 1.0f, live,
-                     a.out2 + b * a.so2.b + kk * a.so2.s + hk * a.so2.h + 64 * half);
+      write_columns(lane_addr + kColDk + 32 * part, n > 0, p.scale, live,
+                    a.out1 + b * a.so1.b + kk * a.so1.s + hk * a.so1.h + 32 * part);
+      write_columns(lane_addr + kColDv + 32 * part, n > 0, 1.0f, live,
+                    a.out2 + b * a.so2.b + kk * a.so2.s + hk * a.so2.h + 32 * part);
     }
   }
   finish(tmem);
@@ -545,7 +525,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
   const int per = p.Hq * p.B, qt = a.nqt - 1 - blockIdx.x / per;   // late query tiles first
   const int h = blockIdx.x % per % p.Hq, b = blockIdx.x % per / p.Hq, hk = h / p.group;
   const int q0 = qt * kRows;
-  const uint32_t tmem = set_up(sm, 8, [&] {
+  const uint32_t tmem = set_up(sm, kEw, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 1);
     mbar_init(smem_u32(&sm.b_empty[1]), 1);
   });
@@ -629,8 +609,8 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
         if (!(ok = warp_wait(sm, sm.a_full[j % kStagesA], (j / kStagesA) & 1, a.err))) break;
         if (elect_one()) {
           const uint32_t ds = tmem + kColDs + 64 * (j & 1);
-          product_km(tmem + kColDq, ds, sm.ring_a[j % kStagesA], 0, j > 0);
-          product_km(tmem + kColDq, ds + 32, sm.ring_a[j % kStagesA], 1, true);
+          product_km(tmem + kColDq, ds, 16, sm.ring_a[j % kStagesA], 0, j > 0);
+          product_km(tmem + kColDq, ds + 32, 16, sm.ring_a[j % kStagesA], 1, true);
           umma_commit(smem_u32(&sm.a_empty[j % kStagesA]));
           if (j + 1 == n) umma_commit(smem_u32(&sm.acc[0]));
         }
@@ -642,12 +622,12 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    const int quad = warp & 3, half = warp >> 2;           // 64 key columns per warp
+  } else if (warp < kEw) {
+    const int quad = warp & 3, part = warp >> 2;           // key columns [32 part, + 32)
     const int i_q = min(q0 + quad * 32 + lane, p.Sq - 1);
     const bool live = q0 + quad * 32 + lane < p.Sq;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t ts = lane_addr + kColS + 64 * half, tp = lane_addr + kColDp + 64 * half;
+    const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
     const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + q0 + quad * 32 + lane;
     const uint64_t lse2 = pack_f32x2(a.lse2[at], a.lse2[at]), minus_delta = pack_f32x2(a.delta[at], a.delta[at]);
     const float c = p.scale * kLog2e, slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
@@ -657,68 +637,52 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int rec = list ? list[j] : j;
-      const int kt = rec & kTileMask, k0 = kt * kRows;
+      const int kt = rec & kTileMask, k0 = kt * kRows, col = k0 + 32 * part;
       const bool part_doc = rec & kPartial0;
       const bool partial = part_doc || k0 + kRows - 1 > lim0;
-      uint4 bm = make_uint4(0, 0, 0, 0);
-      if (bad) bm = bad[kt];
-      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      uint32_t bad_k = 0;                                  // columns whose k holds an infinity or NaN
+      if (bad) bad_k = reinterpret_cast<const uint32_t*>(bad + kt)[part];
+      uint32_t see = 0xffffffffu;
       if (partial) {
+        see = 0;
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) {
-          const int col = k0 + 64 * half + 32 * q2;
-          uint32_t m = 0;
+        for (int u = 0; u < 32; ++u) see |= (col + u <= lim ? 1u : 0u) << u;
+        if (part_doc) {
 #pragma unroll
-          for (int u = 0; u < 32; ++u) m |= (col + u <= lim ? 1u : 0u) << u;
-          if (part_doc) {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int d = __ldg(dk + min(col + u, p.Sk - 1));
-              if (!(d == doc && d >= 0)) m &= ~(1u << u);
-            }
+          for (int u = 0; u < 32; ++u) {
+            const int d = __ldg(dk + min(col + u, p.Sk - 1));
+            if (!(d == doc && d >= 0)) see &= ~(1u << u);
           }
-          see[q2] = m;
         }
       }
-      const uint32_t bb[2] = {half ? bm.z : bm.x, half ? bm.w : bm.y};
       if (!(ok = warp_wait(sm, sm.s_full[0], j & 1, a.err))) break;
       tc_fence_after();
-      float w[2][32];
-#pragma unroll
-      for (int q2 = 0; q2 < 2; ++q2) {
-        float x[32];
-        tmem_ld32x32f(ts + 32 * q2, x);
-        tmem_wait_ld32(x);
-        if (q2 == 1) {                                     // S(j) is in registers: S(j + 1) may replace it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
-        }
-        const float d0 = static_cast<float>(i_q + p.off - k0 - 64 * half - 32 * q2);
-        probabilities<kCap, kBias>(x, w[q2], p, c, slope, d0, -1.0f, [&](int) { return lse2; });
-      }
+      float x[32], w[32];
+      uint32_t pw[16];
+      tmem_ld32x32f(ts, x);
+      tmem_wait_ld32(x);
+      tc_fence_before();                                   // S(j) is in registers: S(j + 1) may replace it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
+      probabilities<kCap, kBias>(x, w, p, c, slope, static_cast<float>(i_q + p.off - col), -1.0f,
+                                 [&](int) { return lse2; });
       if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
       tc_fence_after();
+      tmem_ld32x32f(tp, x);
+      tmem_wait_ld32(x);
+      score_gradients(x, w, [&](int) { return minus_delta; });
+      if (partial) {
 #pragma unroll
-      for (int q2 = 0; q2 < 2; ++q2) {
-        float x[32];
-        tmem_ld32x32f(tp + 32 * q2, x);
-        tmem_wait_ld32(x);
-        score_gradients(x, w[q2], [&](int) { return minus_delta; });
-        if (partial) {
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = (see[q2] >> u) & 1u ? x[u] : 0.0f;
-        }
-        if (bb[q2]) {                                      // a visible key with an infinity or NaN in its k
-#pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if ((bb[q2] & see[q2]) >> u & 1u) x[u] = NAN;
-        }
-        uint32_t pw[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
-        tmem_st32x16(lane_addr + kColDs + 64 * (j & 1) + 32 * half + 16 * q2, pw);
+        for (int u = 0; u < 32; ++u) x[u] = (see >> u) & 1u ? x[u] : 0.0f;
       }
+      if (bad_k) {
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+          if ((bad_k & see) >> u & 1u) x[u] = NAN;
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) pw[u] = pack_bf16x2(x[2 * u], x[2 * u + 1]);
+      tmem_st32x16(lane_addr + kColDs + 64 * (j & 1) + 16 * part, pw);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -729,8 +693,8 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
       tc_fence_after();
     }
     if (ok)
-      write_half_row(lane_addr + kColDq + 64 * half, n > 0, p.scale, live,
-                     a.out1 + b * a.so1.b + i_q * a.so1.s + h * a.so1.h + 64 * half);
+      write_columns(lane_addr + kColDq + 32 * part, n > 0, p.scale, live,
+                    a.out1 + b * a.so1.b + i_q * a.so1.s + h * a.so1.h + 32 * part);
   }
   finish(tmem);
 }

@@ -60,7 +60,7 @@ struct FwdArgs {
   const void *w, *b;
   float *mean, *rstd;
   Strides sx, sy;
-  int width, w_f32;
+  int width, w_f32, w_wide;
   float eps, inv_n;
 };
 
@@ -71,19 +71,34 @@ struct BwdArgs {
   void* dx;
   Strides sdy, sx, sdx;
   float* part;                       // [blocks][2][width] partial dw, db, or null
-  int width, w_f32, dx_f32;
+  int width, w_f32, w_wide, dx_f32;
   float inv_n;
 };
 
-// Weight or bias values of VEC columns from c; `w_f32`: stored as float.
+// Weight or bias values of VEC columns from c, stored as float or T; with
+// `w_wide` in one access (16-byte aligned vectors).
 template <class T, int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int w_f32, int c, float (&v)[VEC]) {
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int w_wide, int c, float (&v)[VEC]) {
   if (w_f32 || sizeof(T) == 4) {
+    const float* p = static_cast<const float*>(w) + c;
+    if (w_wide) {
+      Pack<float, VEC> k;
+      k.load(p);
+      k.get(v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = __ldg(static_cast<const float*>(w) + c + i);
+      for (int i = 0; i < VEC; ++i) v[i] = __ldg(p + i);
+    }
   } else {
+    const T* p = static_cast<const T*>(w) + c;
+    if (w_wide) {
+      Pack<T, VEC> k;
+      k.load(p);
+      k.get(v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = to_f32(static_cast<const T*>(w)[c + i]);
+      for (int i = 0; i < VEC; ++i) v[i] = to_f32(p[i]);
+    }
   }
 }
 
@@ -92,8 +107,8 @@ template <class T, int VEC>
 __device__ __forceinline__ void weights(const FwdArgs& a, int c, int nv, float (&w)[VEC], float (&b)[VEC]) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) w[j] = 1.0f, b[j] = 0.0f;
-  if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, c * VEC, w);
-  if (a.b && c < nv) load_weight<T, VEC>(a.b, a.w_f32, c * VEC, b);
+  if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, a.w_wide, c * VEC, w);
+  if (a.b && c < nv) load_weight<T, VEC>(a.b, a.w_f32, a.w_wide, c * VEC, b);
 }
 
 template <int LANES>
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
 #pragma unroll
     for (int j = 0; j < VEC; ++j) w[i][j] = 1.0f, dw[i][j] = 0.0f, db[i][j] = 0.0f;
     const int c = i * tpr + t;
-    if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, c * VEC, w[i]);
+    if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, a.w_wide, c * VEC, w[i]);
   }
   Pack<T, VEC> kx[U][E];
   Pack<G, VEC> kg[U][E];
@@ -360,26 +375,26 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
   }
 }
 
-// dweight and dbias from the blocks' partial rows: 32 columns per block, eight
-// rows of threads each adding every eighth partial, then a tree over the eight.
-constexpr int kSumCols = 32, kSumRows = 8;
+// dweight and dbias from the blocks' partial rows: 32 columns per block, 32 rows
+// of threads each adding every 32nd partial, then a tree over the 32.
+constexpr int kSumCols = 32, kSumRows = 32;
 __global__ void __launch_bounds__(kSumCols * kSumRows)
 norm_sum_kernel(const float* __restrict__ part, int n_part, int width, float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float acc[kSumRows][kSumCols];
-  const int c = blockIdx.x * kSumCols + threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+  __shared__ float acc[kSumRows][kSumCols + 1];
+  const int cc = threadIdx.x % kSumCols, c = blockIdx.x * kSumCols + cc, r = threadIdx.x / kSumCols;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;                                 // the whole block
   float s = 0.0f;
-  if (c < width)
-    for (int i = r; i < n_part; i += kSumRows) s += part[(static_cast<int64_t>(i) * 2 + blockIdx.y) * width + c];
-  acc[r][threadIdx.x % kSumCols] = s;
-  __syncthreads();
-  if (r == 0 && c < width) {
-    float x = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kSumRows; ++i) x += acc[i][threadIdx.x];
-    out[c] = x;
+  if (c < width) {
+    const float* p = part + static_cast<int64_t>(blockIdx.y) * width + c;
+#pragma unroll 4
+    for (int i = r; i < n_part; i += kSumRows) s += p[static_cast<int64_t>(i) * 2 * width];
   }
+  acc[r][cc] = s;
+  __syncthreads();
+  const float x = lane_sum<32>(acc[cc][r]);         // row r now sums column r
+  const int col = blockIdx.x * kSumCols + r;
+  if (cc == 0 && col < width) out[col] = x;
 }
 
 // ------------------------------------------------------------------ launches
@@ -431,9 +446,8 @@ template <class T, int VEC>
 void fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
   const int64_t groups = (a.R.n + s.rows_per_block - 1) / s.rows_per_block;
   const int blocks = static_cast<int>(std::min<int64_t>(groups, 1 << 20));
-  const int waves = static_cast<int>(std::min<int64_t>(groups, sm_count() * 8));
-  if (s.lanes == 16) norm_fwd_kernel<T, VEC, 1, 16, kFwdU, kWarpBlock><<<waves, s.threads, 0, stream>>>(a);
-  else if (s.lanes == 32) norm_fwd_kernel<T, VEC, 1, 32, kFwdU, kWarpBlock><<<waves, s.threads, 0, stream>>>(a);
+  if (s.lanes == 16) norm_fwd_kernel<T, VEC, 1, 16, kFwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
+  else if (s.lanes == 32) norm_fwd_kernel<T, VEC, 1, 32, kFwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
   else if (s.ept == 32) norm_fwd_kernel<T, VEC, 32 / VEC, 64, 1, 512><<<blocks, s.threads, 0, stream>>>(a);
   else if (s.ept == 16) norm_fwd_kernel<T, VEC, 16 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
   else norm_fwd_kernel<T, VEC, 8 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
@@ -515,6 +529,7 @@ vsa_status vsa_layer_norm_fwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.w = weight;
   a.b = bias;
   a.w_f32 = weight_dtype == VSA_F32;
+  a.w_wide = aligned(weight, 16) && aligned(bias, 16);
   a.mean = mean;
   a.rstd = rstd;
   a.sx = view_strides(x, B, S);
@@ -578,6 +593,7 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.x = x->data;
   a.w = weight;
   a.w_f32 = weight_dtype == VSA_F32;
+  a.w_wide = aligned(weight, 16);
   a.mean = mean;
   a.rstd = rstd;
   a.dx = dx->data;

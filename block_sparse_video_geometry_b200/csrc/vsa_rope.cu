@@ -14,7 +14,7 @@
 // the heads' rows in chunks of 8 channels, four chunks in flight per thread.
 // A chunk holds whole pairs when pairs are adjacent; with halves the partner
 // channels sit in other chunks of the row at offsets that need not be multiples
-// of 8 (a width block of 42 channels), so the 16 lanes of a row exchange it
+// of 8 (a width block of 42 channels), so the 16 lanes of a row exchange them
 // through shared memory.
 
 #include <cmath>
@@ -30,17 +30,18 @@ constexpr int kPairs = kHeadDim / 2;
 constexpr int kChunk = 8;                        // channels per thread and step
 constexpr int kLanes = kHeadDim / kChunk;        // lanes per row
 constexpr int kRopeUnroll = 4;                   // rows in flight per thread
-constexpr int kRopeTokens = 4;                   // most tokens per block
-constexpr int kRopeMaxHeads = 8192;              // of q and of k: row numbers of a block times heads fit 32 bits
+constexpr int kRopeTokens = 16;                  // most tokens per block
+constexpr int kRopeMaxHeads = 4096;              // of q and of k: row numbers of a block times heads fit 32 bits
 
 struct RopeTable {
   double rate[kPairs];         // turns per position
+  int32_t rotated;             // channels before the pass-through ones
   uint8_t axis[kPairs];
-  // channel -> pair (bits 0-7), partner channel (8-15), kPass (16: not rotated),
-  // and the sign bit where the channel is its pair's first (y_a = x_a cos - x_b sin)
+  uint8_t a[kPairs], b[kPairs];   // the pair's channels: y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin
+  // channel -> its partner's place in a shared-memory row (bits 0-7), kPass where it is not rotated
   uint32_t channel[kHeadDim];
 };
-constexpr uint32_t kPass = 1u << 16, kFirst = 1u << 31;
+constexpr uint32_t kPass = 1u << 16;
 
 struct RopeArgs {
   const void* in[2];
@@ -54,42 +55,52 @@ struct RopeArgs {
   float sign;                  // +1 forward, -1 backward
 };
 
+// Shared memory holds a row of 128 channels as [i][lane] for channel 8 lane + i,
+// padded so that neither the writes nor the partner's reads of a warp's two rows
+// meet in a bank (in channel order they met eight at a time: 195 us for the fp32
+// gradient of 17,408 x 32 heads).
+constexpr int kRowPitch = kLanes + 1, kRowWords = 144;
+__host__ __device__ __forceinline__ int row_word(int channel) { return channel % kChunk * kRowPitch + channel / kChunk; }
+
 template <class I, class O, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, int tokens_per_block) {
-  extern __shared__ float2 turn[];               // [token][pair]: cos, signed sin
+  extern __shared__ float2 turn[];               // [token][row_word(channel)] or [token][pair]: cos, signed sin
   __shared__ int64_t base[kRopeTokens][4];       // element offset of each token in q, k and their outputs
-  __shared__ float rows[kHalves ? kRopeThreads / kLanes * kHeadDim : 1];
+  __shared__ float rows[kHalves ? kRopeThreads / kLanes * kRowWords : 1];
+  constexpr int kTurns = kHalves ? kRowWords : kPairs;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_block), a.n_tokens - t0));
-  for (int i = threadIdx.x; i < nt * kPairs; i += kRopeThreads) {
-    const int64_t tok = t0 + i / kPairs;
-    const int p = i % kPairs;
-    const int64_t b = tok / a.S, s = tok - b * a.S;
-    if (p < 4) {
-      const Strides st = p == 0 ? a.si[0] : p == 1 ? a.si[1] : p == 2 ? a.so[0] : a.so[1];
-      base[i / kPairs][p] = b * st.b + s * st.s;
-    }
-    const double t = static_cast<double>(a.pos[b * a.pos_sb + 3 * s + tab.axis[p]]) * tab.rate[p];
-    float sn, cs;
-    sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &cs);
-    turn[i] = make_float2(cs, a.sign * sn);
+  if (threadIdx.x < 4 * nt) {
+    const int p = threadIdx.x & 3;
+    const uint32_t tok = static_cast<uint32_t>(t0) + threadIdx.x / 4, S = static_cast<uint32_t>(a.S);   // < 2^31
+    const int64_t b = tok / S, s = tok - static_cast<uint32_t>(b) * S;
+    const Strides st = p == 0 ? a.si[0] : p == 1 ? a.si[1] : p == 2 ? a.so[0] : a.so[1];
+    base[threadIdx.x / 4][p] = b * st.b + s * st.s;
   }
   const int lane = threadIdx.x % kLanes, c0 = lane * kChunk;
-  uint32_t ch[kChunk];
+  // Values of the parameter block at an index that differs between lanes are read
+  // one lane after the other: each thread reads its own once per block.
+  uint32_t ch[kHalves ? kChunk : 1];
+  if constexpr (kHalves) {
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) ch[i] = tab.channel[c0 + i];
+    for (int i = 0; i < kChunk; ++i) ch[i] = tab.channel[c0 + i];
+  }
+  const int pr = threadIdx.x % kPairs;
+  const double rate = tab.rate[pr];
+  const int axis = tab.axis[pr];
+  const int ca = kHalves ? row_word(tab.a[pr]) : 0, cb = kHalves ? row_word(tab.b[pr]) : 0;
   __syncthreads();
 
   const int group = threadIdx.x / kLanes;
   constexpr int kGroups = kRopeThreads / kLanes;
   const int n_rows = nt * a.heads;
+  Pack<I, kChunk> x[kRopeUnroll];
+  O* dst[kRopeUnroll];
+  int tk[kRopeUnroll];
   // Every lane runs every step (the exchange synchronises warps); rows past the
   // end are neither read nor written.
-  for (int row0 = 0; row0 < n_rows; row0 += kGroups * kRopeUnroll) {
-    Pack<I, kChunk> x[kRopeUnroll];
-    O* dst[kRopeUnroll];
-    int tk[kRopeUnroll];
+  auto fetch = [&](int row0) {
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
       const int r = row0 + u * kGroups + group;
@@ -104,25 +115,43 @@ rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeA
       x[u].load(static_cast<const I*>(w ? a.in[1] : a.in[0]) + at[0] + h * (w ? a.si[1].h : a.si[0].h) + c0);
       dst[u] = static_cast<O*>(w ? a.out[1] : a.out[0]) + at[2] + h * (w ? a.so[1].h : a.so[0].h) + c0;
     }
+  };
+  for (int i = threadIdx.x / kPairs; i < nt; i += kRopeThreads / kPairs) {
+    const uint32_t tok = static_cast<uint32_t>(t0) + i, S = static_cast<uint32_t>(a.S);
+    const int64_t b = tok / S, s = tok - static_cast<uint32_t>(b) * S;
+    const double t = static_cast<double>(a.pos[b * a.pos_sb + 3 * s + axis]) * rate;
+    float sn, cs;
+    sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &cs);
+    sn *= a.sign;
+    float2* tt = turn + i * kTurns;
+    if constexpr (kHalves) {
+      tt[ca] = make_float2(cs, -sn);
+      tt[cb] = make_float2(cs, sn);
+    } else {
+      tt[pr] = make_float2(cs, sn);
+    }
+  }
+  __syncthreads();
+
+  for (int row0 = 0; row0 < n_rows; row0 += kGroups * kRopeUnroll) {
+    fetch(row0);
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
       float v[kChunk], y[kChunk];
-      const float2* tt = turn + tk[u] * kPairs;
+      const float2* tt = turn + tk[u] * kTurns;
       if constexpr (kHalves) {
-        float* row = rows + group * kHeadDim;
+        float* row = rows + group * kRowWords;
         if (dst[u]) {
           x[u].get(v);
 #pragma unroll
-          for (int i = 0; i < kChunk; i += 4)
-            *reinterpret_cast<float4*>(row + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < kChunk; ++i) row[i * kRowPitch + lane] = v[i];
         }
         __syncwarp();
         if (dst[u]) {
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) {
-            const float2 cs = tt[ch[i] & 0xFFu];
-            const float turned = __uint_as_float(__float_as_uint(cs.y) ^ (ch[i] & kFirst));
-            const float z = fmaf(v[i], cs.x, row[(ch[i] >> 8) & 0xFFu] * turned);
+            const float2 cs = tt[i * kRowPitch + lane];
+            const float z = fmaf(v[i], cs.x, row[ch[i] & 0xFFu] * cs.y);
             y[i] = ch[i] & kPass ? v[i] : z;
           }
         }
@@ -134,8 +163,8 @@ rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeA
           const float2 cs = tt[(c0 + i) / 2];
           const float za = fmaf(v[i], cs.x, -v[i + 1] * cs.y);
           const float zb = fmaf(v[i + 1], cs.x, v[i] * cs.y);
-          y[i] = ch[i] & kPass ? v[i] : za;
-          y[i + 1] = ch[i] & kPass ? v[i + 1] : zb;
+          y[i] = c0 + i >= tab.rotated ? v[i] : za;
+          y[i + 1] = c0 + i >= tab.rotated ? v[i + 1] : zb;
         }
       }
       if (dst[u]) {
@@ -179,6 +208,7 @@ bool rope_table(const vsa_rope* r, RopeTable* t) {
     sum += dim[ax];
   }
   if (sum > kHeadDim) return false;
+  t->rotated = static_cast<int32_t>(sum);
   constexpr double kTwoPi = 6.283185307179586476925;
   for (int p = 0; p < kPairs; ++p) {             // pass through unless set below
     t->rate[p] = 0.0;
@@ -197,9 +227,11 @@ bool rope_table(const vsa_rope* r, RopeTable* t) {
         t->axis[p] = static_cast<uint8_t>(ax);
       }
       const int ca = at + (halves ? i : 2 * i), cb = halves ? ca + d / 2 : ca + 1;
-      const uint32_t e = static_cast<uint32_t>(p) | (ax == 3 ? kPass : 0u);
-      t->channel[ca] = e | static_cast<uint32_t>(cb) << 8 | kFirst;
-      t->channel[cb] = e | static_cast<uint32_t>(ca) << 8;
+      const uint32_t pass = ax == 3 ? kPass : 0u;
+      t->a[p] = static_cast<uint8_t>(ca);
+      t->b[p] = static_cast<uint8_t>(cb);
+      t->channel[ca] = pass | static_cast<uint32_t>(row_word(cb));
+      t->channel[cb] = pass | static_cast<uint32_t>(row_word(ca));
     }
     at += d;
   }
@@ -208,7 +240,7 @@ bool rope_table(const vsa_rope* r, RopeTable* t) {
 
 template <class I, class O>
 void rope_launch(const RopeTable& tab, const RopeArgs& a, bool halves, int tpb, int blocks, cudaStream_t stream) {
-  const size_t smem = sizeof(float2) * kPairs * tpb;
+  const size_t smem = sizeof(float2) * (halves ? kRowWords : kPairs) * tpb;
   if (halves)
     rope_kernel<I, O, true><<<blocks, kRopeThreads, smem, stream>>>(tab, a, tpb);
   else
@@ -262,7 +294,7 @@ vsa_status rope_call(const char* where, const vsa_rope* rope, int32_t B, int64_t
     a.pos = pos;
     a.pos_sb = B > 1 ? pos_sb : 0;
     a.sign = sign;
-    const int tpb = a.n_tokens >= 4096 ? kRopeTokens : 1;
+    const int tpb = a.n_tokens >= 8192 ? kRopeTokens : a.n_tokens >= 2048 ? 4 : 1;
     const int blocks = static_cast<int>((a.n_tokens + tpb - 1) / tpb);
     const bool halves = rope->pairing == VSA_ROPE_HALVES;
     if (in[w]->dtype == VSA_F32) rope_launch_in<float>(out[w]->dtype, tab, a, halves, tpb, blocks, stream);

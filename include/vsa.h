@@ -529,7 +529,7 @@ vsa_status vsa_rope_positions(const vsa_layout* layout, int32_t t0, int32_t h0, 
  * any other overlap is the caller's error. q and k have their own head counts.
  * The angle is reduced to a turn in 64 bits, its sine and cosine and the
  * rotation are 32-bit, and the result is rounded once. B, S >= 0 (0: nothing
- * to do); at most 2^31 - 1 tokens and 8192 heads (UNSUPPORTED beyond). */
+ * to do); at most 2^31 - 1 tokens and 4096 heads (UNSUPPORTED beyond). */
 vsa_status vsa_rope_fwd(const vsa_rope* rope, int32_t B, int64_t S, const int32_t* pos, int64_t pos_stride_b,
                         const vsa_view* q, const vsa_view* k, const vsa_view* q_out, const vsa_view* k_out,
                         cudaStream_t stream);
