@@ -29,7 +29,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kPairs = kHeadDim / 2;
 constexpr int kChunk = 8;                        // channels per thread and step
 constexpr int kLanes = kHeadDim / kChunk;        // lanes per row
-constexpr int kRopeUnroll = 4;                   // rows in flight per thread
+constexpr int kRopeUnroll = 2;                   // rows in flight per thread
 constexpr int kRopeTokens = 16;                  // most tokens per block
 constexpr int kRopeMaxHeads = 4096;              // of q and of k: row numbers of a block times heads fit 32 bits
 
@@ -63,7 +63,7 @@ constexpr int kRowPitch = kLanes + 1, kRowWords = 144;
 __host__ __device__ __forceinline__ int row_word(int channel) { return channel % kChunk * kRowPitch + channel / kChunk; }
 
 template <class I, class O, bool kHalves>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kHalves ? 4 : 6)
 rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, int tokens_per_block) {
   extern __shared__ float2 turn[];               // [token][row_word(channel)] or [token][pair]: cos, signed sin
   __shared__ int64_t base[kRopeTokens][4];       // element offset of each token in q, k and their outputs
@@ -84,7 +84,10 @@ rope_kernel(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeA
   uint32_t ch[kHalves ? kChunk : 1];
   if constexpr (kHalves) {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) ch[i] = tab.channel[c0 + i];
+    for (int i = 0; i < kChunk; ++i) {
+      ch[i] = tab.channel[c0 + i];
+      asm volatile("" : "+r"(ch[i]));            // held: not to be read again from the parameters
+    }
   }
   const int pr = threadIdx.x % kPairs;
   const double rate = tab.rate[pr];
