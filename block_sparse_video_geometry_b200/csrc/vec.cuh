@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,52 +26,70 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float x) { return __float2bfloat1
 template <>
 __device__ __forceinline__ f16 from_f32<f16>(float x) { return __float2half_rn(x); }
 
-// N consecutive elements in as few words as they fill (N * sizeof(T) is a
-// multiple of the word: 16, 8 or 4 bytes, or one element).
+// N consecutive elements in words of the widest access that fills them (16, 8, 4
+// or 2 bytes); as large as the elements.
 template <class T, int N>
 struct Pack {
   static constexpr int kBytes = N * static_cast<int>(sizeof(T));
-  static constexpr int kWord = kBytes % 16 == 0 ? 16 : kBytes % 8 == 0 ? 8 : kBytes % 4 == 0 ? 4 : 2;
+  using Word = std::conditional_t<
+      kBytes % 16 == 0, uint4,
+      std::conditional_t<kBytes % 8 == 0, uint2, std::conditional_t<kBytes % 4 == 0, uint32_t, uint16_t>>>;
+  static constexpr int kWords = kBytes / static_cast<int>(sizeof(Word));
   union {
     T t[N];
-    uint4 u4[kBytes >= 16 ? kBytes / 16 : 1];
-    uint2 u2;
-    uint32_t u1;
-    uint16_t h;
+    Word w[kWords];
   };
   __device__ __forceinline__ Pack() {}
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kWord == 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) u4[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else if constexpr (kWord == 8) {
-      u2 = *reinterpret_cast<const uint2*>(p);
-    } else if constexpr (kWord == 4) {
-      u1 = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      h = *reinterpret_cast<const uint16_t*>(p);
-    }
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const Word*>(p)[i];
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kWord == 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(p)[i] = u4[i];
-    } else if constexpr (kWord == 8) {
-      *reinterpret_cast<uint2*>(p) = u2;
-    } else if constexpr (kWord == 4) {
-      *reinterpret_cast<uint32_t*>(p) = u1;
-    } else {
-      *reinterpret_cast<uint16_t*>(p) = h;
-    }
+    for (int i = 0; i < kWords; ++i) reinterpret_cast<Word*>(p)[i] = w[i];
   }
   __device__ __forceinline__ void get(float (&x)[N]) const {
+    if constexpr (sizeof(T) == 2 && sizeof(Word) > 2 && std::is_same_v<T, bf16>) {
+      // bf16 is the upper half of a float
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(t[i]);
+      for (int i = 0; i < N; i += 2) {
+        const uint32_t p = reinterpret_cast<const uint32_t*>(w)[i / 2];
+        x[i] = __uint_as_float(p << 16);
+        x[i + 1] = __uint_as_float(p & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = to_f32(t[i]);
+    }
   }
   __device__ __forceinline__ void set(const float (&x)[N]) {
+    if constexpr (sizeof(T) == 2 && sizeof(Word) > 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) t[i] = from_f32<T>(x[i]);
+      for (int i = 0; i < N; i += 2) {
+        if constexpr (std::is_same_v<T, bf16>)
+          reinterpret_cast<__nv_bfloat162*>(w)[i / 2] = __floats2bfloat162_rn(x[i], x[i + 1]);
+        else
+          reinterpret_cast<__half2*>(w)[i / 2] = __floats2half2_rn(x[i], x[i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) t[i] = from_f32<T>(x[i]);
+    }
   }
 };
+
+// Element-wise arithmetic on N floats, two per instruction where N is even.
+template <int N, class F2, class F1>
+__device__ __forceinline__ void each(F2 two, F1 one) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) two(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) one(i);
+  }
+}
+
+static_assert(sizeof(Pack<float, 1>) == 4 && sizeof(Pack<bf16, 1>) == 2 && sizeof(Pack<bf16, 8>) == 16);
 
 }  // namespace vsa

@@ -17,13 +17,17 @@
 #include <algorithm>
 #include <cmath>
 
+#include "sm100.cuh"
 #include "vec.cuh"
 #include "vsa_internal.h"
 
 namespace vsa {
 namespace {
 
+using namespace sm100;
+
 constexpr int kWarpBlock = 256;      // threads of a block of the short-row kernels
+constexpr int kFwdBlocks = 4;        // of them per SM in the forward pass
 
 // Rows [B, S, heads] in one index. Where the rows of every view lie at one
 // stride the host gives them as [1, n, 1], which needs no division.
@@ -130,118 +134,365 @@ __device__ __forceinline__ float block_sum(float x, float* buf) {
   return lane_sum<32>(lane < warps ? buf[lane] : 0.0f);
 }
 
+// 1 / sqrt(x) to within 2 * 2^-24 relative: the approximate value and one Newton
+// step (x = 0 and infinity as they come).
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return x > 0.0f && x < INFINITY ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
+}
+
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&x)[N]) {
+  uint64_t s2 = 0;
+  float s = 0.0f, t = 0.0f;
+  each<N>([&](int i) { s2 = add_f32x2(s2, pack_f32x2(x[i], x[i + 1])); }, [&](int i) { s += x[i]; });
+  if constexpr (N % 2 == 0) unpack_f32x2(s2, s, t);
+  return s + t;
+}
+
+// x = x - m in place; returns the sum of squares.
+template <int N>
+__device__ __forceinline__ float centre(float (&x)[N], float m) {
+  uint64_t s2 = 0;
+  float s = 0.0f, t = 0.0f;
+  const uint64_t m2 = pack_f32x2(-m, -m);
+  each<N>(
+      [&](int i) {
+        const uint64_t d = add_f32x2(pack_f32x2(x[i], x[i + 1]), m2);
+        s2 = fma_f32x2(d, d, s2);
+        unpack_f32x2(d, x[i], x[i + 1]);
+      },
+      [&](int i) {
+        x[i] -= m;
+        s = fmaf(x[i], x[i], s);
+      });
+  if constexpr (N % 2 == 0) unpack_f32x2(s2, s, t);
+  return s + t;
+}
+
+// x = x * (r w) + b in place.
+template <int N>
+__device__ __forceinline__ void scale_shift(float (&x)[N], float r, const float (&w)[N], const float (&b)[N]) {
+  const uint64_t r2 = pack_f32x2(r, r);
+  each<N>(
+      [&](int i) {
+        const uint64_t a = mul_f32x2(r2, pack_f32x2(w[i], w[i + 1]));
+        unpack_f32x2(fma_f32x2(pack_f32x2(x[i], x[i + 1]), a, pack_f32x2(b[i], b[i + 1])), x[i], x[i + 1]);
+      },
+      [&](int i) { x[i] = fmaf(x[i], r * w[i], b[i]); });
+}
+
 // ------------------------------------------------------------------ forward
-// A row is spread over TPR threads (LANES of a warp, or the block), E vectors of
-// VEC elements each: vector i of thread t is i * TPR + t. The row stays packed
-// in registers between its passes (sum, squares, output). U rows per group are
-// in flight at once.
-template <class T, int VEC, int E, int LANES, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr bool kWarp = LANES <= 32;
-  constexpr int kLanes = kWarp ? LANES : 32;
-  __shared__ float red[2][2][32];
-  const int tpr = kWarp ? LANES : blockDim.x;
-  const int t = kWarp ? threadIdx.x % LANES : threadIdx.x;
-  const int groups = kWarp ? kWarpBlock / LANES : 1;
-  const int group = kWarp ? threadIdx.x / LANES : 0;
-  const int nv = a.width / VEC;
-  // A short row's weights stay in registers; a long row's come from L1 with each row.
-  constexpr bool kKeep = E * VEC <= 8;
-  float w[kKeep ? E : 1][VEC], b[kKeep ? E : 1][VEC];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) weights<T, VEC>(a, i * tpr + t, nv, w[i], b[i]);
-  }
-  int phase = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * U;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups * U; r0 < a.R.n; r0 += step) {
-    Pack<T, VEC> k[U][E];
+// Short rows: LANES lanes of a warp per row, a vector of VEC elements each.
+// Persistent blocks keep the weights in registers and fetch the next U rows of a
+// lane group while they work on the current ones.
+template <class T, int VEC, int LANES, int U>
+__global__ void __launch_bounds__(kWarpBlock, kFwdBlocks) norm_fwd_warp_kernel(const __grid_constant__ FwdArgs a) {
+  constexpr int kGroups = kWarpBlock / LANES;
+  const int t = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const bool in = t < a.width / VEC;
+  float w[VEC], b[VEC];
+  weights<T, VEC>(a, t, a.width / VEC, w, b);
+  Pack<T, VEC> next[U];
+  auto fetch = [&](int64_t r0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t row = r0 + u * groups + group;
-      if (row >= a.R.n) continue;
-      const T* x = static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row));
+      const int64_t row = r0 + u * kGroups + group;
+      if (row < a.R.n && in) next[u].load(static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row)) + t * VEC);
+    }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups * U;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups * U;
+  fetch(r0);
+  for (; r0 < a.R.n; r0 += step) {
+    Pack<T, VEC> k[U];
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (i * tpr + t < nv) k[u][i].load(x + static_cast<int64_t>(i * tpr + t) * VEC);
+    for (int u = 0; u < U; ++u) k[u] = next[u];
+    fetch(r0 + step);                                // y may lie over x: other rows
+    float v[U][VEC], mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mean[u] = 0.0f;
+      if (r0 + u * kGroups + group < a.R.n && in) {
+        k[u].get(v[u]);
+        mean[u] = sum_of(v[u]);
+      }
     }
 #pragma unroll
+    for (int u = 0; u < U; ++u) mean[u] = lane_sum<LANES>(mean[u]) * a.inv_n;     // every lane takes part
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t row = r0 + u * groups + group;
-      const bool live = row < a.R.n;               // whole lane groups; every lane takes part in the sums
-      float sum = 0.0f, sq = 0.0f;
+      rstd[u] = 0.0f;
+      if (r0 + u * kGroups + group < a.R.n && in) rstd[u] = centre(v[u], mean[u]);
+    }
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (!live || i * tpr + t >= nv) continue;
-        float v[VEC];
-        k[u][i].get(v);
+    for (int u = 0; u < U; ++u) rstd[u] = inv_sqrt(lane_sum<LANES>(rstd[u]) * a.inv_n + a.eps);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum += v[j];
-      }
-      const float mean = (kWarp ? lane_sum<kLanes>(sum) : block_sum(sum, red[phase][0])) * a.inv_n;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (!live || i * tpr + t >= nv) continue;
-        float v[VEC];
-        k[u][i].get(v);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sq = fmaf(v[j] - mean, v[j] - mean, sq);
-      }
-      const float var = (kWarp ? lane_sum<kLanes>(sq) : block_sum(sq, red[phase][1])) * a.inv_n;
-      phase ^= 1;
-      const float rstd = 1.0f / sqrtf(var + a.eps);
-      if (!live) continue;
-      T* y = static_cast<T*>(a.y) + offset(a.sy, place(a.R, row));
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = i * tpr + t;
-        if (c >= nv) continue;
-        float v[VEC], wl[VEC], bl[VEC];
-        if constexpr (!kKeep) weights<T, VEC>(a, c, nv, wl, bl);
-        k[u][i].get(v);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          v[j] = fmaf((v[j] - mean) * rstd, kKeep ? w[kKeep ? i : 0][j] : wl[j], kKeep ? b[kKeep ? i : 0][j] : bl[j]);
-        k[u][i].set(v);
-        k[u][i].store(y + static_cast<int64_t>(c) * VEC);
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r0 + u * kGroups + group;
+      if (row >= a.R.n) continue;
+      if (in) {
+        scale_shift(v[u], rstd[u], w, b);
+        k[u].set(v[u]);
+        k[u].store(static_cast<T*>(a.y) + offset(a.sy, place(a.R, row)) + t * VEC);
       }
       if (t == 0 && a.mean) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
+        a.mean[row] = mean[u];
+        a.rstd[row] = rstd[u];
       }
     }
   }
 }
 
-// ----------------------------------------------------------------- backward
-// Same spread. A thread keeps the weights and the running dw and db of its
-// columns, and loads the next rows while it works on the current ones.
-template <class T, class G, int VEC, int E, int LANES, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr bool kWarp = LANES <= 32;
-  __shared__ float red[2][2][32];
-  const int tpr = kWarp ? LANES : blockDim.x;
-  const int t = kWarp ? threadIdx.x % LANES : threadIdx.x;
-  const int groups = kWarp ? kWarpBlock / LANES : 1;
-  const int group = kWarp ? threadIdx.x / LANES : 0;
-  const int nv = a.width / VEC;
-  float w[E][VEC], dw[E][VEC], db[E][VEC];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) w[i][j] = 1.0f, dw[i][j] = 0.0f, db[i][j] = 0.0f;
-    const int c = i * tpr + t;
-    if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, a.w_wide, c * VEC, w[i]);
+// Asynchronous copy of one vector into this thread's own place in shared memory
+// (of 4 or 16 bytes; 2-byte elements one by one are copied at once).
+template <int BYTES>
+__device__ __forceinline__ void stage_in(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  } else if constexpr (BYTES == 32) {
+    stage_in<16>(dst, src);
+    stage_in<16>(static_cast<char*>(dst) + 16, static_cast<const char*>(src) + 16);
+  } else if constexpr (BYTES == 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+  } else {
+    static_assert(BYTES == 2);
+    *static_cast<uint16_t*>(dst) = *static_cast<const uint16_t*>(src);
   }
-  Pack<T, VEC> kx[U][E];
-  Pack<G, VEC> kg[U][E];
-  float mean[U], rstd[U];
-  auto fetch = [&](int64_t r0) {
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Long rows: one block per row, E vectors of VEC elements per thread (vector i of
+// thread t is i * threads + t). A persistent block keeps up to three rows ahead on
+// their way into shared memory; a thread reads back only what it copied itself,
+// so the ring needs no barrier. Rows of the ring: four where `bytes` a thread and
+// row times `threads` allow it.
+__host__ __device__ constexpr int ring_rows(int bytes, int threads) {
+  const int n = (200 << 10) / (bytes * threads);
+  return n < 1 ? 1 : n > 4 ? 4 : n;
+}
+template <class T, int VEC, int E, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kRing = ring_rows(sizeof(T) * VEC * E, MAXT);
+  __shared__ float red[2][2][32];
+  using P = Pack<T, VEC>;
+  P* mine = reinterpret_cast<P*>(ring) + threadIdx.x;
+  const int tpr = blockDim.x, t = threadIdx.x, nv = a.width / VEC;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.R.n) {
+      const T* x = static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row));
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = r0 + u * groups + group;
-      mean[u] = rstd[u] = 0.0f;
-      if (row >= a.R.n) continue;
+      for (int i = 0; i < E; ++i)
+        if (i * tpr + t < nv) stage_in<sizeof(P)>(mine + (st * E + i) * tpr, x + static_cast<int64_t>(i * tpr + t) * VEC);
+    }
+    stage_commit();
+  };
+  float w[E][VEC], b[E][VEC];
+#pragma unroll
+  for (int i = 0; i < E; ++i) weights<T, VEC>(a, i * tpr + t, nv, w[i], b[i]);
+  int st = 0, phase = 0;
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+  for (int64_t row = blockIdx.x; row < a.R.n; row += gridDim.x) {
+    if constexpr (kRing == 1) fetch(row, 0);
+    stage_wait<(kRing > 2 ? kRing - 2 : 0)>();
+    float v[E][VEC], sum = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (i * tpr + t >= nv) continue;
+      mine[(st * E + i) * tpr].get(v[i]);
+      sum += sum_of(v[i]);
+    }
+    if constexpr (kRing > 1) fetch(row + static_cast<int64_t>(kRing - 1) * gridDim.x, st == 0 ? kRing - 1 : st - 1);
+    if (++st == kRing) st = 0;
+    const float mean = block_sum(sum, red[phase][0]) * a.inv_n;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (i * tpr + t < nv) sq += centre(v[i], mean);
+    }
+    const float rstd = inv_sqrt(block_sum(sq, red[phase][1]) * a.inv_n + a.eps);
+    phase ^= 1;
+    T* y = static_cast<T*>(a.y) + offset(a.sy, place(a.R, row));
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * tpr + t;
+      if (c >= nv) continue;
+      scale_shift(v[i], rstd, w[i], b[i]);
+      P k;
+      k.set(v[i]);
+      k.store(y + static_cast<int64_t>(c) * VEC);
+    }
+    if (t == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+  }
+  stage_wait<0>();
+}
+
+// ----------------------------------------------------------------- backward
+// A thread's vector of columns: the sums dw and db of the rows it passed. The row
+// itself is unpacked again for the second pass: unpacked it would not fit.
+template <class T, class G, int VEC>
+struct Columns {
+  float w[VEC], dw[VEC], db[VEC];
+  __device__ __forceinline__ void start(const BwdArgs& a, int c, int nv) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] = 1.0f, dw[j] = db[j] = 0.0f;
+    if (a.w && c < nv) load_weight<T, VEC>(a.w, a.w_f32, a.w_wide, c * VEC, w);
+  }
+  // adds a row's share of dw and db, and of the two sums over the row
+  __device__ __forceinline__ void add(const Pack<T, VEC>& kx, const Pack<G, VEC>& kg,
+                                      float mean, float rstd, float& s1, float& s2) {
+    float x[VEC], g[VEC];
+    kx.get(x);
+    kg.get(g);
+    const uint64_t m2 = pack_f32x2(-mean, -mean), r2 = pack_f32x2(rstd, rstd);
+    uint64_t a1 = 0, a2 = 0;
+    float b1 = 0.0f, b2 = 0.0f, t1 = 0.0f, t2 = 0.0f;
+    each<VEC>(
+        [&](int i) {
+          const uint64_t xh = mul_f32x2(add_f32x2(pack_f32x2(x[i], x[i + 1]), m2), r2);
+          const uint64_t d = pack_f32x2(g[i], g[i + 1]), y = mul_f32x2(d, pack_f32x2(w[i], w[i + 1]));
+          unpack_f32x2(fma_f32x2(d, xh, pack_f32x2(dw[i], dw[i + 1])), dw[i], dw[i + 1]);
+          unpack_f32x2(add_f32x2(d, pack_f32x2(db[i], db[i + 1])), db[i], db[i + 1]);
+          a1 = add_f32x2(a1, y);
+          a2 = fma_f32x2(y, xh, a2);
+        },
+        [&](int i) {
+          const float xh = (x[i] - mean) * rstd, y = g[i] * w[i];
+          dw[i] = fmaf(g[i], xh, dw[i]);
+          db[i] += g[i];
+          b1 += y;
+          b2 = fmaf(y, xh, b2);
+        });
+    if constexpr (VEC % 2 == 0) {
+      unpack_f32x2(a1, b1, t1);
+      unpack_f32x2(a2, b2, t2);
+    }
+    s1 += b1 + t1;
+    s2 += b2 + t2;
+  }
+  // rstd (g - c1 - xh c2)
+  __device__ __forceinline__ void write(const BwdArgs& a, const Pack<T, VEC>& kx, const Pack<G, VEC>& kg,
+                                               float mean, float rstd, float c1, float c2, int64_t at) {
+    float x[VEC], g[VEC];
+    kx.get(x);
+    kg.get(g);
+    const uint64_t m2 = pack_f32x2(-mean, -mean), r2 = pack_f32x2(rstd, rstd);
+    const uint64_t n1 = pack_f32x2(-c1, -c1), n2 = pack_f32x2(-c2, -c2);
+    each<VEC>(
+        [&](int i) {
+          const uint64_t xh = mul_f32x2(add_f32x2(pack_f32x2(x[i], x[i + 1]), m2), r2);
+          const uint64_t y = fma_f32x2(pack_f32x2(g[i], g[i + 1]), pack_f32x2(w[i], w[i + 1]), fma_f32x2(xh, n2, n1));
+          unpack_f32x2(mul_f32x2(r2, y), g[i], g[i + 1]);
+        },
+        [&](int i) { g[i] = rstd * fmaf(g[i], w[i], -fmaf((x[i] - mean) * rstd, c2, c1)); });
+    if (a.dx_f32) {
+      Pack<float, VEC> k;
+      k.set(g);
+      k.store(static_cast<float*>(a.dx) + at);
+    } else {
+      Pack<T, VEC> k;
+      k.set(g);
+      k.store(static_cast<T*>(a.dx) + at);
+    }
+  }
+};
+
+// Short rows, as in the forward kernel; the next row is fetched into registers
+// while the current one is worked on.
+template <class T, class G, int VEC, int E, int LANES>
+__global__ void __launch_bounds__(kWarpBlock) norm_bwd_warp_kernel(const __grid_constant__ BwdArgs a) {
+  constexpr int kGroups = kWarpBlock / LANES;
+  const int t = threadIdx.x % LANES, group = threadIdx.x / LANES, nv = a.width / VEC;
+  Columns<T, G, VEC> col[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) col[i].start(a, i * LANES + t, nv);
+  Pack<T, VEC> kx[E];
+  Pack<G, VEC> kg[E];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= a.R.n) return;
+    const Place p = place(a.R, row);
+    const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
+    const G* dy = static_cast<const G*>(a.dy) + offset(a.sdy, p);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (i * LANES + t >= nv) continue;
+      kx[i].load(x + (i * LANES + t) * VEC);
+      kg[i].load(dy + (i * LANES + t) * VEC);
+    }
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups;
+  fetch(r0 + group);
+  for (; r0 < a.R.n; r0 += step) {
+    const int64_t row = r0 + group;
+    const bool live = row < a.R.n;                   // every lane takes part in the sums
+    const float m = mean, r = rstd;
+    float s1 = 0.0f, s2 = 0.0f;
+    Pack<T, VEC> cx[E];
+    Pack<G, VEC> cg[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      cx[i] = kx[i];
+      cg[i] = kg[i];
+      if (live && i * LANES + t < nv) col[i].add(cx[i], cg[i], m, r, s1, s2);
+    }
+    // dx may lie over dy: a row is fetched and written by the same lanes, in that order
+    fetch(row + step);
+    s1 = lane_sum<LANES>(s1) * a.inv_n;
+    s2 = lane_sum<LANES>(s2) * a.inv_n;
+    if (!live) continue;
+    const int64_t od = offset(a.sdx, place(a.R, row));
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i * LANES + t < nv) col[i].write(a, cx[i], cg[i], m, r, s1, s2, od + (i * LANES + t) * VEC);
+  }
+  if (!a.part) return;
+  // the block's row groups first, in group order
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
+  __shared__ float acc[2][LANES * E * VEC];
+  for (int i = threadIdx.x; i < 2 * LANES * E * VEC; i += kWarpBlock) (&acc[0][0])[i] = 0.0f;
+  for (int gidx = 0; gidx < kGroups; ++gidx) {
+    __syncthreads();
+    if (group != gidx) continue;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        acc[0][(i * LANES + t) * VEC + j] += col[i].dw[j];
+        acc[1][(i * LANES + t) * VEC + j] += col[i].db[j];
+      }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.width; c += kWarpBlock) {
+    part[c] = acc[0][c];
+    part[a.width + c] = acc[1][c];
+  }
+}
+
+// Long rows: one persistent block per row, its next rows on their way into shared
+// memory as in the forward kernel.
+template <class T, class G, int VEC, int E, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kRing = ring_rows((sizeof(T) + sizeof(G)) * VEC * E, MAXT);
+  __shared__ float red[2][2][32];
+  using PX = Pack<T, VEC>;
+  using PG = Pack<G, VEC>;
+  const int tpr = blockDim.x, t = threadIdx.x, nv = a.width / VEC;
+  PX* my_x = reinterpret_cast<PX*>(ring) + t;
+  PG* my_g = reinterpret_cast<PG*>(ring + sizeof(PX) * kRing * E * tpr) + t;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.R.n) {
       const Place p = place(a.R, row);
       const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
       const G* dy = static_cast<const G*>(a.dy) + offset(a.sdy, p);
@@ -249,128 +500,73 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
       for (int i = 0; i < E; ++i) {
         const int64_t c = i * tpr + t;
         if (c >= nv) continue;
-        kx[u][i].load(x + c * VEC);
-        kg[u][i].load(dy + c * VEC);
+        stage_in<sizeof(PX)>(my_x + (st * E + i) * tpr, x + c * VEC);
+        stage_in<sizeof(PG)>(my_g + (st * E + i) * tpr, dy + c * VEC);
       }
-      mean[u] = a.mean[row];
-      rstd[u] = a.rstd[row];
     }
+    stage_commit();
   };
-  int phase = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups * U;
-  int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups * U;
-  if (r0 < a.R.n) fetch(r0);
-  for (; r0 < a.R.n; r0 += step) {
-    // the rows stay packed between the two passes: unpacked they would not fit
-    Pack<T, VEC> cx[U][E];
-    Pack<G, VEC> cg[U][E];
-    float s1[U], s2[U], mu[U], rs[U];
+  Columns<T, G, VEC> col[E];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool live = r0 + u * groups + group < a.R.n;
-      s1[u] = s2[u] = 0.0f;
-      mu[u] = mean[u];
-      rs[u] = rstd[u];
+  for (int i = 0; i < E; ++i) col[i].start(a, i * tpr + t, nv);
+  int st = 0, phase = 0;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (!live || i * tpr + t >= nv) continue;
-        cx[u][i] = kx[u][i];
-        cg[u][i] = kg[u][i];
-        float xh[VEC], g[VEC];
-        cx[u][i].get(xh);
-        cg[u][i].get(g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          xh[j] = (xh[j] - mu[u]) * rs[u];
-          dw[i][j] = fmaf(g[j], xh[j], dw[i][j]);
-          db[i][j] += g[j];
-          g[j] *= w[i][j];
-          s1[u] += g[j];
-          s2[u] = fmaf(g[j], xh[j], s2[u]);
-        }
-      }
-    }
-    // dx may lie over dy: a row is fetched and written by the same block, in that order
-    if (r0 + step < a.R.n) fetch(r0 + step);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      s1[u] = lane_sum<kWarp ? LANES : 32>(s1[u]);
-      s2[u] = lane_sum<kWarp ? LANES : 32>(s2[u]);
-    }
-    if constexpr (!kWarp) {
-      static_assert(U == 1, "one row per block");
-      const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-      if (warps > 1) {
-        if (lane == 0) {
-          red[phase][0][threadIdx.x >> 5] = s1[0];
-          red[phase][1][threadIdx.x >> 5] = s2[0];
-        }
-        __syncthreads();
-        s1[0] = lane_sum<32>(lane < warps ? red[phase][0][lane] : 0.0f);
-        s2[0] = lane_sum<32>(lane < warps ? red[phase][1][lane] : 0.0f);
-        phase ^= 1;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = r0 + u * groups + group;
-      if (row >= a.R.n) continue;
-      const float c1 = s1[u] * a.inv_n, c2 = s2[u] * a.inv_n;
-      const int64_t od = offset(a.sdx, place(a.R, row));
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = i * tpr + t;
-        if (c >= nv) continue;
-        float o[VEC], g[VEC];
-        cx[u][i].get(o);
-        cg[u][i].get(g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = rs[u] * (g[j] * w[i][j] - fmaf((o[j] - mu[u]) * rs[u], c2, c1));
-        const int64_t at = od + static_cast<int64_t>(c) * VEC;
-        if (a.dx_f32) {
-          Pack<float, VEC> k;
-          k.set(o);
-          k.store(static_cast<float*>(a.dx) + at);
-        } else {
-          Pack<T, VEC> k;
-          k.set(o);
-          k.store(static_cast<T*>(a.dx) + at);
-        }
-      }
-    }
+  for (int i = 0; i < kRing - 1; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+  float mean = 0.0f, rstd = 0.0f;
+  if (blockIdx.x < a.R.n) {
+    mean = a.mean[blockIdx.x];
+    rstd = a.rstd[blockIdx.x];
   }
-  if (!a.part) return;
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
-  if constexpr (kWarp) {
-    // the block's row groups first, in group order
-    __shared__ float acc[2][LANES * E * VEC];
-    for (int i = threadIdx.x; i < 2 * LANES * E * VEC; i += kWarpBlock) (&acc[0][0])[i] = 0.0f;
-    for (int gidx = 0; gidx < kWarpBlock / LANES; ++gidx) {
+  for (int64_t row = blockIdx.x; row < a.R.n; row += gridDim.x) {
+    const int64_t next = row + gridDim.x;
+    const float next_mean = next < a.R.n ? a.mean[next] : 0.0f, next_rstd = next < a.R.n ? a.rstd[next] : 0.0f;
+    if constexpr (kRing == 1) fetch(row, 0);
+    stage_wait<(kRing > 2 ? kRing - 2 : 0)>();
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i * tpr + t < nv)
+        col[i].add(my_x[(st * E + i) * tpr], my_g[(st * E + i) * tpr], mean, rstd, s1, s2);
+    // dx may lie over dy: a row is fetched and written by the same block, in that order
+    if constexpr (kRing > 1) fetch(row + static_cast<int64_t>(kRing - 1) * gridDim.x, st == 0 ? kRing - 1 : st - 1);
+    s1 = lane_sum<32>(s1);
+    s2 = lane_sum<32>(s2);
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (warps > 1) {
+      if (lane == 0) {
+        red[phase][0][threadIdx.x >> 5] = s1;
+        red[phase][1][threadIdx.x >> 5] = s2;
+      }
       __syncthreads();
-      if (group != gidx) continue;
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          acc[0][(i * LANES + t) * VEC + j] += dw[i][j];
-          acc[1][(i * LANES + t) * VEC + j] += db[i][j];
-        }
+      s1 = lane_sum<32>(lane < warps ? red[phase][0][lane] : 0.0f);
+      s2 = lane_sum<32>(lane < warps ? red[phase][1][lane] : 0.0f);
+      phase ^= 1;
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.width; c += kWarpBlock) {
-      part[c] = acc[0][c];
-      part[a.width + c] = acc[1][c];
-    }
-  } else {
+    s1 *= a.inv_n;
+    s2 *= a.inv_n;
+    const int64_t od = offset(a.sdx, place(a.R, row));
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = i * tpr + t;
-      if (c >= nv) continue;
+      const int64_t c = i * tpr + t;
+      if (c < nv)
+        col[i].write(a, my_x[(st * E + i) * tpr], my_g[(st * E + i) * tpr], mean, rstd, s1, s2,
+                     od + c * VEC);
+    }
+    if (++st == kRing) st = 0;
+    mean = next_mean;
+    rstd = next_rstd;
+  }
+  stage_wait<0>();
+  if (!a.part) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        part[c * VEC + j] = dw[i][j];
-        part[a.width + c * VEC + j] = db[i][j];
-      }
+  for (int i = 0; i < E; ++i) {
+    const int c = i * tpr + t;
+    if (c >= nv) continue;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      part[c * VEC + j] = col[i].dw[j];
+      part[a.width + c * VEC + j] = col[i].db[j];
     }
   }
 }
@@ -387,7 +583,7 @@ norm_sum_kernel(const float* __restrict__ part, int n_part, int width, float* __
   float s = 0.0f;
   if (c < width) {
     const float* p = part + static_cast<int64_t>(blockIdx.y) * width + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = r; i < n_part; i += kSumRows) s += p[static_cast<int64_t>(i) * 2 * width];
   }
   acc[r][cc] = s;
@@ -399,33 +595,26 @@ norm_sum_kernel(const float* __restrict__ part, int n_part, int width, float* __
 
 // ------------------------------------------------------------------ launches
 // Few vectors of the widest aligned access: lanes of one warp per row. Else one
-// block per row with `ept` elements per thread.
+// block per row with `ept` elements per thread: 16 from a width of 2048 on where
+// rows fill the GPU (17,408 x 5120 forward and backward: 209 us; 8: 318 us, the
+// row's fixed work of sums and addresses; 32: 250 us, too few threads beside their
+// registers), 8 for narrower or few rows, 32 above 8192.
 struct Shape {
   int vec, lanes;         // lanes 64: one block per row
   int ept;
   int threads, rows_per_block;
 };
-constexpr int kFwdU = 4, kBwdU = 2;   // rows in flight per lane group of the short-row kernels
+constexpr int kFwdU = 2;   // rows in flight per lane group of the short-row forward kernel
 
-Shape shape_of(int width, int vec, int ept, int u) {
+Shape shape_of(int width, int vec, int64_t rows, int u) {
   const int nv = width / vec;
   if (nv <= 32) {
     const int lanes = nv <= 16 ? 16 : 32;
     return Shape{vec, lanes, vec, kWarpBlock, kWarpBlock / lanes * u};
   }
-  const int e = ept / vec;
+  const int ept = width > 8192 ? 32 : width >= 2048 && rows >= 512 ? 16 : 8, e = ept / vec;
   return Shape{vec, 64, ept, ((nv + e - 1) / e + 31) / 32 * 32, 1};
 }
-
-// Forward: 32 elements per thread (four 16-byte loads of bf16 in flight) once
-// the rows fill the GPU; few rows are spread over more threads.
-int fwd_ept(int width, int64_t rows) {
-  if (width > 8192) return rows >= 512 ? 32 : 16;
-  return rows >= 512 && width >= 2048 ? 32 : 8;
-}
-// Backward: 16 elements per thread, so that weights, dw, db, two rows and the
-// next rows' packed data fit its registers; 8 for narrow rows.
-int bwd_ept(int width) { return width > 1024 ? 16 : 8; }
 
 int sm_count() {
   int dev = 0, n = 0;
@@ -435,31 +624,56 @@ int sm_count() {
 }
 
 constexpr int kMaxSms = 160;                        // the workspace is sized for this many
-// Blocks of the backward kernel: a partial row each, so no more than fill the GPU.
-int bwd_blocks(int64_t rows, const Shape& s) {
-  const int per_sm = std::max(1, std::min(8, 640 / s.threads));
+// Persistent blocks: as many per SM as make about `threads` threads, at most 8.
+int persistent(int64_t rows, const Shape& s, int threads) {
+  const int per_sm = std::max(1, std::min(8, threads / s.threads));
   const int64_t most = static_cast<int64_t>(std::min(sm_count(), kMaxSms)) * per_sm;
   return static_cast<int>(std::min<int64_t>((rows + s.rows_per_block - 1) / s.rows_per_block, most));
 }
 
-template <class T, int VEC>
-void fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
-  const int64_t groups = (a.R.n + s.rows_per_block - 1) / s.rows_per_block;
-  const int blocks = static_cast<int>(std::min<int64_t>(groups, 1 << 20));
-  if (s.lanes == 16) norm_fwd_kernel<T, VEC, 1, 16, kFwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.lanes == 32) norm_fwd_kernel<T, VEC, 1, 32, kFwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.ept == 32) norm_fwd_kernel<T, VEC, 32 / VEC, 64, 1, 512><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.ept == 16) norm_fwd_kernel<T, VEC, 16 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
-  else norm_fwd_kernel<T, VEC, 8 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
+template <class K, class A>
+vsa_status start(const char* where, K kernel, int blocks, int threads, size_t smem, const A& a, cudaStream_t stream) {
+  if (smem > (48u << 10)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(where, e);
+  }
+  kernel<<<blocks, threads, smem, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK : cuda_fail(where, e);
 }
 
+template <class T, int VEC>
+vsa_status fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
+  const char* where = "vsa_layer_norm_fwd";
+  const int n = persistent(a.R.n, s, s.lanes <= 32 ? kFwdBlocks * kWarpBlock : 960);
+  if (s.lanes == 16) return start(where, norm_fwd_warp_kernel<T, VEC, 16, kFwdU>, n, s.threads, 0, a, stream);
+  if (s.lanes == 32) return start(where, norm_fwd_warp_kernel<T, VEC, 32, kFwdU>, n, s.threads, 0, a, stream);
+  const int row = static_cast<int>(sizeof(T)) * s.ept;
+  auto smem = [&](int most) { return static_cast<size_t>(row) * s.threads * ring_rows(row, most); };
+  if (s.ept == 8) return start(where, norm_fwd_kernel<T, VEC, 8 / VEC, 1024>, n, s.threads, smem(1024), a, stream);
+  if (s.ept == 16) return start(where, norm_fwd_kernel<T, VEC, 16 / VEC, 512>, n, s.threads, smem(512), a, stream);
+  if (s.threads <= 256) return start(where, norm_fwd_kernel<T, VEC, 32 / VEC, 256>, n, s.threads, smem(256), a, stream);
+  return start(where, norm_fwd_kernel<T, VEC, 32 / VEC, 512>, n, s.threads, smem(512), a, stream);
+}
+
+// Blocks of the backward kernel: a partial row each.
+int bwd_blocks(int64_t rows, const Shape& s) { return persistent(rows, s, s.lanes <= 32 ? 4 * kWarpBlock : 640); }
+
 template <class T, class G, int VEC>
-void bwd_launch(const Shape& s, const BwdArgs& a, int blocks, cudaStream_t stream) {
-  if (s.lanes == 16) norm_bwd_kernel<T, G, VEC, 1, 16, kBwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.lanes == 32) norm_bwd_kernel<T, G, VEC, 1, 32, kBwdU, kWarpBlock><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.ept == 8) norm_bwd_kernel<T, G, VEC, 8 / VEC, 64, 1, 640><<<blocks, s.threads, 0, stream>>>(a);
-  else if (s.threads <= 640) norm_bwd_kernel<T, G, VEC, 16 / VEC, 64, 1, 640><<<blocks, s.threads, 0, stream>>>(a);
-  else norm_bwd_kernel<T, G, VEC, 16 / VEC, 64, 1, 1024><<<blocks, s.threads, 0, stream>>>(a);
+vsa_status bwd_launch(const Shape& s, const BwdArgs& a, int blocks, cudaStream_t stream) {
+  const char* where = "vsa_layer_norm_bwd";
+  if (s.lanes == 16) return start(where, norm_bwd_warp_kernel<T, G, VEC, 1, 16>, blocks, s.threads, 0, a, stream);
+  if (s.lanes == 32) return start(where, norm_bwd_warp_kernel<T, G, VEC, 1, 32>, blocks, s.threads, 0, a, stream);
+  const int row = static_cast<int>(sizeof(T) + sizeof(G)) * s.ept;
+  auto smem = [&](int most) { return static_cast<size_t>(row) * s.threads * ring_rows(row, most); };
+  if (s.ept == 8)
+    return start(where, norm_bwd_kernel<T, G, VEC, 8 / VEC, 1024>, blocks, s.threads, smem(1024), a, stream);
+  if (s.ept == 16)
+    return start(where, norm_bwd_kernel<T, G, VEC, 16 / VEC, 512>, blocks, s.threads, smem(512), a, stream);
+  if (s.threads <= 256)
+    return start(where, norm_bwd_kernel<T, G, VEC, 32 / VEC, 256>, blocks, s.threads, smem(256), a, stream);
+  return start(where, norm_bwd_kernel<T, G, VEC, 32 / VEC, 512>, blocks, s.threads, smem(512), a, stream);
 }
 
 // Rows at one stride in all views: [1, n, 1].
@@ -540,12 +754,10 @@ vsa_status vsa_layer_norm_fwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.inv_n = 1.0f / static_cast<float>(width);
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(y, a.sy, vec, width);
-  const Shape s = shape_of(width, wide ? vec : 1, fwd_ept(width, a.R.n), kFwdU);
-  if (x->dtype == VSA_F32) wide ? fwd_launch<float, 4>(s, a, stream) : fwd_launch<float, 1>(s, a, stream);
-  else if (x->dtype == VSA_BF16) wide ? fwd_launch<bf16, 8>(s, a, stream) : fwd_launch<bf16, 1>(s, a, stream);
-  else wide ? fwd_launch<f16, 8>(s, a, stream) : fwd_launch<f16, 1>(s, a, stream);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_layer_norm_fwd", e);
+  const Shape s = shape_of(width, wide ? vec : 1, a.R.n, kFwdU);
+  if (x->dtype == VSA_F32) return wide ? fwd_launch<float, 4>(s, a, stream) : fwd_launch<float, 1>(s, a, stream);
+  if (x->dtype == VSA_BF16) return wide ? fwd_launch<bf16, 8>(s, a, stream) : fwd_launch<bf16, 1>(s, a, stream);
+  return wide ? fwd_launch<f16, 8>(s, a, stream) : fwd_launch<f16, 1>(s, a, stream);
 }
 
 vsa_status vsa_layer_norm_bwd_workspace_size(int32_t B, int64_t S, int32_t heads, int32_t width, size_t* bytes) {
@@ -607,24 +819,24 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   a.inv_n = 1.0f / static_cast<float>(width);
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(dy, a.sdy, vec, width) && vec_ok(dx, a.sdx, vec, width);
-  const Shape s = shape_of(width, wide ? vec : 1, bwd_ept(width), kBwdU);
-  const int blocks = bwd_blocks(a.R.n, s);
+  const Shape s = shape_of(width, wide ? vec : 1, a.R.n, 1);
+  const int n = bwd_blocks(a.R.n, s);
   const bool g32 = dy->dtype == VSA_F32;
-  if (x->dtype == VSA_F32) {
-    wide ? bwd_launch<float, float, 4>(s, a, blocks, stream) : bwd_launch<float, float, 1>(s, a, blocks, stream);
-  } else if (x->dtype == VSA_BF16) {
-    if (g32) wide ? bwd_launch<bf16, float, 8>(s, a, blocks, stream) : bwd_launch<bf16, float, 1>(s, a, blocks, stream);
-    else wide ? bwd_launch<bf16, bf16, 8>(s, a, blocks, stream) : bwd_launch<bf16, bf16, 1>(s, a, blocks, stream);
-  } else {
-    if (g32) wide ? bwd_launch<f16, float, 8>(s, a, blocks, stream) : bwd_launch<f16, float, 1>(s, a, blocks, stream);
-    else wide ? bwd_launch<f16, f16, 8>(s, a, blocks, stream) : bwd_launch<f16, f16, 1>(s, a, blocks, stream);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail("vsa_layer_norm_bwd", e);
+  if (x->dtype == VSA_F32)
+    st = wide ? bwd_launch<float, float, 4>(s, a, n, stream) : bwd_launch<float, float, 1>(s, a, n, stream);
+  else if (x->dtype == VSA_BF16 && g32)
+    st = wide ? bwd_launch<bf16, float, 8>(s, a, n, stream) : bwd_launch<bf16, float, 1>(s, a, n, stream);
+  else if (x->dtype == VSA_BF16)
+    st = wide ? bwd_launch<bf16, bf16, 8>(s, a, n, stream) : bwd_launch<bf16, bf16, 1>(s, a, n, stream);
+  else if (g32)
+    st = wide ? bwd_launch<f16, float, 8>(s, a, n, stream) : bwd_launch<f16, float, 1>(s, a, n, stream);
+  else
+    st = wide ? bwd_launch<f16, f16, 8>(s, a, n, stream) : bwd_launch<f16, f16, 1>(s, a, n, stream);
+  if (st != VSA_OK) return st;
   if (!a.part) return VSA_OK;
   const dim3 grid((width + kSumCols - 1) / kSumCols, 2);
-  norm_sum_kernel<<<grid, kSumCols * kSumRows, 0, stream>>>(a.part, blocks, width, dweight, dbias);
-  e = cudaGetLastError();
+  norm_sum_kernel<<<grid, kSumCols * kSumRows, 0, stream>>>(a.part, n, width, dweight, dbias);
+  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_layer_norm_bwd: sums", e);
 }
 
