@@ -28,8 +28,8 @@
 #include <cmath>
 #include <cstdint>
 
+#include "masked_scores.cuh"
 #include "sm100.cuh"
-#include "vec.cuh"
 #include "vsa_masked.h"
 
 namespace vsa {
@@ -541,10 +541,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int lim0 = p.limit(b, a.packed ? 0 : min(tile_row0, p.Sq - 1));
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
-    constexpr float kLog2e = 1.4426950408889634f;
     const float c = p.scale * kLog2e;                      // raw score -> log2 units
-    const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
-    const float cap2 = kCap ? p.cap * kLog2e : 0.0f, in2 = kCap ? 2.0f * c / p.cap : 0.0f;
+    const ScoreTerms terms{c, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f, kBias ? p.slopes[h] * kLog2e : 0.0f};
     const float c_exp = kCap || kBias ? 1.0f : c;          // factor still to apply inside the exponential
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
@@ -565,17 +563,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         // scores of key columns [32 q4, 32 q4 + 32) in place: cap, bias, mask
         auto finish = [&](int q4, float (&x)[32]) {
           const int col = 32 * q4;
-          if constexpr (kCap) {
-            // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-#pragma unroll
-            for (int u = 0; u < 32; ++u) x[u] = fmaf(rcp_approx(1.0f + ex2_approx(x[u] * in2)), -2.0f * cap2, cap2);
-          }
-          if constexpr (kBias) {
-            const float d0 = static_cast<float>(i_q + p.off - k0 - col);
-#pragma unroll
-            for (int u = 0; u < 32; ++u)
-              x[u] = fmaf(-slope, fabsf(d0 - static_cast<float>(u)), kCap ? x[u] : x[u] * c);
-          }
+          float tanhs[32];
+          score_terms<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f);
           if (partial) {
             const int lc = lim - k0 - col;
 #pragma unroll

@@ -30,17 +30,14 @@
 #include <cmath>
 #include <cstdint>
 
+#include "masked_scores.cuh"
 #include "sm100.cuh"
-#include "vec.cuh"
 #include "vsa_masked.h"
 
 namespace vsa {
 namespace masked {
 namespace {
 
-using namespace sm100;
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ prepare
 // Minus D and minus lse2 of every row, [B][Hq][nqt * 128]; rows past Sq, and rows
@@ -231,38 +228,29 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 // of columns at a time), and into `w` P times the cap's derivative. A quarter of
 // the exponentials go to the FMA pipe.
 template <bool kCap, bool kBias, class Ref>
-__device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const Problem& p, float c, float slope,
-                                              float d0, float dir, Ref ref) {
-  const float cap2 = kCap ? p.cap * kLog2e : 0.0f, in2 = kCap ? 2.0f * c / p.cap : 0.0f;
-  const uint64_t c2 = kCap || kBias ? pack_f32x2(1.0f, 1.0f) : pack_f32x2(c, c);
+__device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const ScoreTerms& s, float d0, float dir,
+                                              Ref ref) {
+  score_terms<kCap, kBias>(x, w, s, d0, dir);              // w: tanh
+  const uint64_t c2 = kCap || kBias ? pack_f32x2(1.0f, 1.0f) : pack_f32x2(s.c, s.c);
+  const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
-    float t[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float s = x[u + i];
-      if constexpr (kCap) {
-        t[i] = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(s * in2)), 1.0f);
-        s = cap2 * t[i];
-      } else if constexpr (kBias) {
-        s *= c;
-      }
-      if constexpr (kBias) s = fmaf(-slope, fabsf(fmaf(dir, static_cast<float>(u + i), d0)), s);
-      x[u + i] = s;
-    }
     const uint64_t arg = fma_f32x2(pack_f32x2(x[u], x[u + 1]), c2, ref(u));
-    float e0, e1;
     if (u % 8 == 4) {
-      ex2_poly_f32x2(arg, e0, e1);
+      ex2_poly_f32x2(arg, x[u], x[u + 1]);
     } else {
+      float e0, e1;
       unpack_f32x2(arg, e0, e1);
-      e0 = ex2_approx(e0);
-      e1 = ex2_approx(e1);
+      x[u] = ex2_approx(e0);
+      x[u + 1] = ex2_approx(e1);
     }
-    x[u] = e0;
-    x[u + 1] = e1;
-    w[u] = kCap ? e0 * fmaf(-t[0], t[0], 1.0f) : e0;
-    w[u + 1] = kCap ? e1 * fmaf(-t[1], t[1], 1.0f) : e1;
+    if constexpr (kCap) {
+      const uint64_t t = pack_f32x2(w[u], w[u + 1]);
+      unpack_f32x2(mul_f32x2(pack_f32x2(x[u], x[u + 1]), fma_f32x2(mul_f32x2(t, neg), t, one)), w[u], w[u + 1]);
+    } else {
+      w[u] = x[u];
+      w[u + 1] = x[u + 1];
+    }
   }
 }
 
@@ -413,7 +401,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     const int key = k0 + quad * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
-    const float c = p.scale * kLog2e;
+    ScoreTerms terms{p.scale * kLog2e, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f, 0.0f};
     // first query that sees this key by order
     const int i_min = !p.causal || key < prefix ? INT32_MIN : key - p.off;
     const int doc = p.documents && key < p.Sk ? p.doc_k[b * p.doc_k_sb + key] : -1;
@@ -433,7 +421,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
         bad = reinterpret_cast<const uint32_t*>(a.clean_a.bad + tile)[part] |
               reinterpret_cast<const uint32_t*>(a.clean_b.bad + tile)[part];
       }
-      const float slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+      if constexpr (kBias) terms.slope = p.slopes[h] * kLog2e;
       // visible columns as a bit mask; only where some pair is hidden
       uint32_t see = 0xffffffffu;
       if (partial) {
@@ -456,7 +444,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       const float* lse = sm.lse2[st] + 32 * part;
-      probabilities<kCap, kBias>(x, w, p, c, slope, static_cast<float>(i0 + p.off - key), 1.0f,
+      probabilities<kCap, kBias>(x, w, terms, static_cast<float>(i0 + p.off - key), 1.0f,
                                  [&](int u) { return *reinterpret_cast<const uint64_t*>(lse + u); });
       if (partial) {
 #pragma unroll
@@ -630,7 +618,8 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
     const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + q0 + quad * 32 + lane;
     const uint64_t lse2 = pack_f32x2(a.lse2[at], a.lse2[at]), minus_delta = pack_f32x2(a.delta[at], a.delta[at]);
-    const float c = p.scale * kLog2e, slope = kBias ? p.slopes[h] * kLog2e : 0.0f;
+    const ScoreTerms terms{p.scale * kLog2e, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f,
+                           kBias ? p.slopes[h] * kLog2e : 0.0f};
     const int lim = p.limit(b, i_q), lim0 = p.limit(b, q0);
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
@@ -664,7 +653,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
       tc_fence_before();                                   // S(j) is in registers: S(j + 1) may replace it
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
-      probabilities<kCap, kBias>(x, w, p, c, slope, static_cast<float>(i_q + p.off - col), -1.0f,
+      probabilities<kCap, kBias>(x, w, terms, static_cast<float>(i_q + p.off - col), -1.0f,
                                  [&](int) { return lse2; });
       if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
       tc_fence_after();

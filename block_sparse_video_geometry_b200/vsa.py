@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -57,11 +58,6 @@ class LayoutInfo(ctypes.Structure):
                 ("video_start", ctypes.c_int64), ("device_bytes", ctypes.c_size_t)]
 
 
-class View(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
-                ("stride_h", ctypes.c_int64), ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
-
-
 class Rope(ctypes.Structure):
     _fields_ = [("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
                 ("pairing", ctypes.c_int32), ("theta", ctypes.c_double), ("scale_t", ctypes.c_double),
@@ -81,7 +77,7 @@ class MaskTerms(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-_V = ctypes.POINTER(View)
+_V = ctypes.c_void_p      # a vsa_view, passed as the bytes of the struct
 
 _SIGNATURES = {
     "vsa_layout_build": (_I32, [ctypes.POINTER(Segment), _I32, _I64, _P, _SZ, _P, ctypes.POINTER(_P)]),
@@ -416,44 +412,46 @@ def _dtype(t) -> int:
     return code
 
 
-def _view(t):
-    """The vsa_view of a [..., width] tensor of 2 ([S, width]), 3 ([B, S, width]) or 4 dimensions, as a
-    reference that ctypes passes by address."""
+_VIEW = struct.Struct("@Pqqqii")      # vsa_view: data, stride_b, stride_s, stride_h, heads, dtype
+
+
+def view_bytes(data: int, stride_b: int, stride_s: int, stride_h: int, heads: int, dtype: int) -> bytes:
+    """A vsa_view as bytes, which ctypes passes by address."""
+    return _VIEW.pack(data, stride_b, stride_s, stride_h, heads, dtype)
+
+
+def _view(t) -> bytes:
+    """The vsa_view of a [..., width] tensor of 2 ([S, width]), 3 ([B, S, width]) or 4 dimensions."""
     shape, st = t.shape, t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("the last dimension must be contiguous")
-    if len(shape) == 4:
-        v = View(t.data_ptr(), st[0], st[1], st[2], shape[2], _dtype(t))
-    elif len(shape) == 3:
-        v = View(t.data_ptr(), st[0], st[1], 0, 1, _dtype(t))
-    elif len(shape) == 2:
-        v = View(t.data_ptr(), 0, st[0], 0, 1, _dtype(t))
+    n = len(st)
+    if n == 4:
+        return _VIEW.pack(t.data_ptr(), st[0], st[1], st[2], shape[2], _dtype(t))
+    if n == 3:
+        return _VIEW.pack(t.data_ptr(), st[0], st[1], 0, 1, _dtype(t))
+    if n == 2:
+        return _VIEW.pack(t.data_ptr(), 0, st[0], 0, 1, _dtype(t))
+    raise ValueError("tensors must have 2, 3 or 4 dimensions")
+
+
+def _run(name, tensors, *args) -> None:
+    """Calls a library function with the tensors' device current; they must share one CUDA device."""
+    import torch
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, got %s" % device)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors must be on one device, got %s and %s" % (device, t.device))
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args)
     else:
-        raise ValueError("tensors must have 2, 3 or 4 dimensions")
-    return ctypes.byref(v)
-
-
-class _On:
-    """Makes the tensors' device current for a call; they must share one CUDA device."""
-
-    def __init__(self, first, *others):
-        self.device = first.device
-        if self.device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device, got %s" % self.device)
-        for t in others:
-            if t is not None and t.device != self.device:
-                raise ValueError("tensors must be on one device, got %s and %s" % (self.device, t.device))
-        self.guard = None
-
-    def __enter__(self):
-        import torch
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != OK:
+        raise VSAError(status, name)
 
 
 def make_rope(dims=(44, 42, 42), theta: float = 10000.0, scale=(1.0, 1.0, 1.0),
@@ -469,9 +467,7 @@ def rope_positions(layout: Layout, pos, origin=(0, 0, 0), stream=None) -> None:
     import torch
     if pos.dtype != torch.int32 or tuple(pos.shape) != (layout.info.seq_len, 3) or not pos.is_contiguous():
         raise ValueError("pos must be a contiguous int32 [seq_len, 3] tensor")
-    with _On(pos):
-        _check(lib().vsa_rope_positions(layout.handle, *origin, pos.data_ptr(), _stream_handle(stream)),
-               "vsa_rope_positions")
+    _run("vsa_rope_positions", (pos,), layout.handle, *origin, pos.data_ptr(), _stream_handle(stream))
 
 
 def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
@@ -487,10 +483,9 @@ def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
     if pos.dtype != torch.int32 or tuple(pos.shape) not in ((S, 3), (B, S, 3)) \
             or (S > 1 and pos.stride()[-2:] != (3, 1)):
         raise ValueError("pos must be int32 [S, 3] or [B, S, 3], contiguous in its last two dimensions")
-    with _On(q, pos, k, q_out, k_out):
-        _check(getattr(lib(), name)(ctypes.byref(rope), B, S, pos.data_ptr(), pos.stride(0) if pos.dim() == 3 else 0,
-                                    _view(q), None if k is None else _view(k), _view(q_out),
-                                    None if k is None else _view(k_out), _stream_handle(stream)), name)
+    _run(name, (q, pos, k, q_out, k_out), ctypes.byref(rope), B, S, pos.data_ptr(),
+         pos.stride(0) if pos.dim() == 3 else 0, _view(q), None if k is None else _view(k), _view(q_out),
+         None if k is None else _view(k_out), _stream_handle(stream))
 
 
 def rope_fwd(rope: Rope, pos, q, k, q_out, k_out, stream=None) -> None:
@@ -516,7 +511,7 @@ def _vector(t, n, what, dtypes):
     """Address of a contiguous [n] tensor of one of the types, or None."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_contiguous() or t.dtype not in dtypes:
+    if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d elements of %s" % (what, n, " or ".join(map(str, dtypes))))
     return t.data_ptr()
 
@@ -532,12 +527,10 @@ def layer_norm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=
     types = (x.dtype, torch.float32)
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have one type")
-    with _On(x, weight, bias, y, mean, rstd):
-        _check(lib().vsa_layer_norm_fwd(B, S, N, _view(x), _vector(weight, N, "weight", types),
-                                        _vector(bias, N, "bias", types), 0 if wt is None else _dtype(wt), eps, _view(y),
-                                        _vector(mean, B * S * H, "mean", (torch.float32,)),
-                                        _vector(rstd, B * S * H, "rstd", (torch.float32,)), _stream_handle(stream)),
-               "vsa_layer_norm_fwd")
+    f32 = (torch.float32,)
+    _run("vsa_layer_norm_fwd", (x, weight, bias, y, mean, rstd), B, S, N, _view(x), _vector(weight, N, "weight", types),
+         _vector(bias, N, "bias", types), 0 if wt is None else _dtype(wt), eps, _view(y),
+         _vector(mean, B * S * H, "mean", f32), _vector(rstd, B * S * H, "rstd", f32), _stream_handle(stream))
 
 
 def layer_norm_bwd_workspace_size(x) -> int:
@@ -556,14 +549,11 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, str
     if dy.shape != x.shape or dx.shape != x.shape:
         raise ValueError("dy and dx must have x's shape")
     f32 = (torch.float32,)
-    with _On(x, dy, weight, mean, rstd, dx, dweight, dbias, workspace):
-        _check(lib().vsa_layer_norm_bwd(B, S, N, _view(dy), _view(x),
-                                        _vector(weight, N, "weight", (x.dtype, torch.float32)),
-                                        0 if weight is None else _dtype(weight), _vector(mean, B * S * H, "mean", f32),
-                                        _vector(rstd, B * S * H, "rstd", f32), _view(dx),
-                                        _vector(dweight, N, "dweight", f32), _vector(dbias, N, "dbias", f32),
-                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                        _stream_handle(stream)), "vsa_layer_norm_bwd")
+    _run("vsa_layer_norm_bwd", (x, dy, weight, mean, rstd, dx, dweight, dbias, workspace), B, S, N, _view(dy), _view(x),
+         _vector(weight, N, "weight", (x.dtype, torch.float32)), 0 if weight is None else _dtype(weight),
+         _vector(mean, B * S * H, "mean", f32), _vector(rstd, B * S * H, "rstd", f32), _view(dx),
+         _vector(dweight, N, "dweight", f32), _vector(dbias, N, "dbias", f32), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), _stream_handle(stream))
 
 
 def make_mask(causal: bool = False, softcap: float = 0.0, scale: float = 0.0, documents: bool = False) -> Mask:
@@ -611,11 +601,10 @@ def masked_attn_fwd(mask: Mask, q, k, v, out, lse, workspace, doc_q=None, doc_k=
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
-    with _On(q, k, v, out, lse, workspace, doc_q, doc_k, prefix, slopes):
-        _check(lib().vsa_masked_attn_fwd(ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v),
-                                         _view(out), _vector(lse, B * Hq * Sq, "lse", (torch.float32,)),
-                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                         _stream_handle(stream)), "vsa_masked_attn_fwd")
+    _run("vsa_masked_attn_fwd", (q, k, v, out, lse, workspace, doc_q, doc_k, prefix, slopes), ctypes.byref(mask),
+         ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
+         _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), _stream_handle(stream))
 
 
 def masked_attn_bwd_workspace_size(mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int) -> int:
@@ -636,12 +625,10 @@ def masked_attn_bwd(mask: Mask, q, k, v, out, lse, dout, dq, dk, dv, workspace, 
     if dk.shape != k.shape or dv.shape != k.shape:
         raise ValueError("dk and dv must have k's shape")
     terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
-    with _On(q, k, v, out, lse, dout, dq, dk, dv, workspace, doc_q, doc_k, prefix, slopes):
-        _check(lib().vsa_masked_attn_bwd(ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v),
-                                         _view(out), _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), _view(dout),
-                                         _view(dq), _view(dk), _view(dv), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), _stream_handle(stream)),
-               "vsa_masked_attn_bwd")
+    _run("vsa_masked_attn_bwd", (q, k, v, out, lse, dout, dq, dk, dv, workspace, doc_q, doc_k, prefix, slopes),
+         ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
+         _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), _view(dout), _view(dq), _view(dk), _view(dv),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
 
 
 def masked_attn_status(workspace, stream=None) -> int:
