@@ -11,74 +11,108 @@ using namespace sm100;
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Per-row constants: `c` turns raw scores into log2 units, cap2 = cap log2(e),
-// in = scale / cap, slope in log2 units.
+// Constants of a row or a call: `c` turns raw scores into log2 units, cap2 = cap
+// log2(e), in = scale / cap; slope of the bias in log2 units.
 struct ScoreTerms {
   float c, cap2, in, slope;
+  float poly[4];               // see score_args
+  float limit;                 // largest |raw score| of the polynomial
+  __device__ __forceinline__ ScoreTerms(float scale, float cap, float slope_) {
+    c = scale * kLog2e;
+    cap2 = cap * kLog2e;
+    in = cap > 0.0f ? scale / cap : 0.0f;
+    slope = slope_ * kLog2e;
+    // c tanh(y) / y = c (1 + a1 z + a2 z^2 + a3 z^3 + a4 z^4), z = y^2 = (in x)^2, with
+    // in^2 and c multiplied into the coefficients
+    const float in2 = in * in;
+    float f = c * in2;
+    poly[0] = -0.333325982f * f;
+    poly[1] = 0.133131161f * (f *= in2);
+    poly[2] = -0.0522118137f * (f *= in2);
+    poly[3] = 0.0156126432f * (f *= in2);
+    limit = in > 0.0f && in < 1000.0f ? 0.6f / in : -1.0f;   // beyond that the coefficients could overflow
+  }
 };
 
-// Raw scores x (sums of products) -> log2 units, except that without cap and bias
-// they stay raw (the caller's exponential applies c). With a cap t receives
+// Raw scores x (sums of products) -> their log2 values minus a reference (`ref`
+// gives minus the reference for a pair of columns). With a cap t receives
 // tanh(score / cap). Distance of column u: |d0 + dir u|, dir = 1 or -1.
 //
 // tanh: 1 - 2 / (1 + e^(2y)) takes two operations of the exponential unit per
 // score, which then bounds the kernels. Where all of a warp's 32 x 32 scores have
-// |y| <= 0.6 (a cap well above the scores, as caps are) it is y (1 + z p(z)),
-// z = y^2, on the FMA pipe: p of degree 4, least squares with weights driven to
-// equal extrema, relative error below 2^-23.
-// Bias: where the columns lie on one side of every row of the warp, it is linear in
-// the column: two operations for a pair of scores.
-// Both together: 362 -> STREAMUS us for 2 x 1,111 queries over 5,003 keys, 24 heads.
-template <bool kCap, bool kBias>
-__device__ __forceinline__ void score_terms(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir) {
-  uint64_t mul = pack_f32x2(s.c, s.c);          // what the bias step still multiplies by
+// |y| <= 0.6 (a cap well above the scores, as caps are), tanh(y) / y is a polynomial
+// in y^2 on the FMA pipe: degree 4, least squares with weights driven to equal
+// extrema, relative error below 2^-23; five operations a score.
+// Bias: where the columns lie on one side of every row of the warp it is linear in
+// the column, one operation a score.
+// A call of 2 x 1,111 queries over 5,003 keys, 24 heads, cap and bias: a half tile's
+// softmax 2950 cycles with both general forms in the exponential unit, NEWCYC so.
+template <bool kCap, bool kBias, class Ref>
+__device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
+                                           Ref ref) {
+  bool poly = true;
   if constexpr (kCap) {
     float top = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 32; ++u) top = fmaxf(top, fabsf(x[u]));
-    const uint64_t in2 = pack_f32x2(s.in, s.in);
-    if (__all_sync(0xffffffffu, top * s.in <= 0.6f)) {
-      const uint64_t one = pack_f32x2(1.0f, 1.0f);
-#pragma unroll
-      for (int u = 0; u < 32; u += 2) {
-        const uint64_t y = mul_f32x2(pack_f32x2(x[u], x[u + 1]), in2), z = mul_f32x2(y, y);
-        uint64_t p = pack_f32x2(-0.00589513499f, -0.00589513499f);
-        p = fma_f32x2(p, z, pack_f32x2(0.0207959544f, 0.0207959544f));
-        p = fma_f32x2(p, z, pack_f32x2(-0.0537838265f, -0.0537838265f));
-        p = fma_f32x2(p, z, pack_f32x2(0.133319244f, 0.133319244f));
-        p = fma_f32x2(p, z, pack_f32x2(-0.333332986f, -0.333332986f));
-        unpack_f32x2(mul_f32x2(y, fma_f32x2(p, z, one)), t[u], t[u + 1]);
-      }
-    } else {
-      const float in_e = 2.0f * kLog2e * s.in;
-#pragma unroll
-      for (int u = 0; u < 32; ++u) t[u] = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(x[u] * in_e)), 1.0f);
-    }
-    mul = pack_f32x2(s.cap2, s.cap2);
+    for (int u = 0; u < 32; u += 2) top = fmaxf(fmaxf(top, fabsf(x[u])), fabsf(x[u + 1]));
+    poly = __all_sync(0xffffffffu, top <= s.limit);
   }
-  float(&y)[32] = kCap ? t : x;
+  float k = 0.0f;               // bias of column u: k (d0 + dir u)
+  bool linear = true;
   if constexpr (kBias) {
     const float d31 = fmaf(dir, 31.0f, d0);
     const bool right = __all_sync(0xffffffffu, d0 >= 0.0f && d31 >= 0.0f);
-    const bool left = __all_sync(0xffffffffu, d0 <= 0.0f && d31 <= 0.0f);
-    if (right || left) {
-      const float k = right ? -s.slope : s.slope, step = k * dir;
-      const uint64_t base = pack_f32x2(k * d0, k * d0), step2 = pack_f32x2(step, step);
+    linear = right || __all_sync(0xffffffffu, d0 <= 0.0f && d31 <= 0.0f);
+    k = right ? -s.slope : s.slope;
+  }
+  if (poly && linear) {
+    const uint64_t c2 = pack_f32x2(s.c, s.c), base = pack_f32x2(k * d0, k * d0), step = pack_f32x2(k * dir, k * dir);
+    const uint64_t p0 = pack_f32x2(s.poly[0], s.poly[0]), p1 = pack_f32x2(s.poly[1], s.poly[1]);
+    const uint64_t p2 = pack_f32x2(s.poly[2], s.poly[2]), p3 = pack_f32x2(s.poly[3], s.poly[3]);
 #pragma unroll
-      for (int u = 0; u < 32; u += 2) {
-        const uint64_t b = fma_f32x2(step2, pack_f32x2(static_cast<float>(u), static_cast<float>(u + 1)), base);
-        unpack_f32x2(fma_f32x2(pack_f32x2(y[u], y[u + 1]), mul, b), x[u], x[u + 1]);
+    for (int u = 0; u < 32; u += 2) {
+      const uint64_t v = pack_f32x2(x[u], x[u + 1]);
+      uint64_t q = c2, add = ref(u);
+      if constexpr (kCap) {
+        const uint64_t z = mul_f32x2(v, v);
+        q = fma_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(p3, z, p2), z, p1), z, p0), z, c2);
       }
-    } else {
-      const float m = kCap ? s.cap2 : s.c;
-#pragma unroll
-      for (int u = 0; u < 32; ++u)
-        x[u] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), y[u] * m);
+      if constexpr (kBias)
+        add = add_f32x2(add, fma_f32x2(step, pack_f32x2(static_cast<float>(u), static_cast<float>(u + 1)), base));
+      unpack_f32x2(fma_f32x2(v, q, add), x[u], x[u + 1]);
+      if constexpr (kCap) unpack_f32x2(mul_f32x2(v, q), t[u], t[u + 1]);   // times 1 / cap2 below
     }
-  } else if constexpr (kCap) {
+    if constexpr (kCap) {
+      const float inv = 1.0f / s.cap2;
 #pragma unroll
-    for (int u = 0; u < 32; u += 2)
-      unpack_f32x2(mul_f32x2(pack_f32x2(y[u], y[u + 1]), mul), x[u], x[u + 1]);
+      for (int u = 0; u < 32; ++u) t[u] *= inv;
+    }
+    return;
+  }
+  const float in_e = 2.0f * kLog2e * s.in;
+#pragma unroll
+  for (int u = 0; u < 32; u += 2) {
+#pragma unroll
+    for (int i = u; i < u + 2; ++i) {
+      if constexpr (kCap) {
+        t[i] = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(x[i] * in_e)), 1.0f);
+        x[i] = t[i] * s.cap2;
+      } else {
+        x[i] *= s.c;
+      }
+      if constexpr (kBias) x[i] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(i), d0)), x[i]);
+    }
+    unpack_f32x2(add_f32x2(pack_f32x2(x[u], x[u + 1]), ref(u)), x[u], x[u + 1]);
+  }
+}
+
+// 2^x of a pair of columns: with `fma_pipe` on the FMA pipe, else the exponential unit.
+__device__ __forceinline__ void ex2_pair(float& a, float& b, bool fma_pipe) {
+  if (fma_pipe) {
+    ex2_poly_f32x2(pack_f32x2(a, b), a, b);
+  } else {
+    a = ex2_approx(a);
+    b = ex2_approx(b);
   }
 }
 

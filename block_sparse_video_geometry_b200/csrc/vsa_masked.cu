@@ -541,9 +541,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int lim0 = p.limit(b, a.packed ? 0 : min(tile_row0, p.Sq - 1));
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
-    const float c = p.scale * kLog2e;                      // raw score -> log2 units
-    const ScoreTerms terms{c, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f, kBias ? p.slopes[h] * kLog2e : 0.0f};
-    const float c_exp = kCap || kBias ? 1.0f : c;          // factor still to apply inside the exponential
+    const ScoreTerms terms(p.scale, p.cap, kBias ? p.slopes[h] : 0.0f);
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     const int step = one ? 2 : 1;
@@ -560,11 +558,13 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         const uint32_t tb = ts + 64 * hb;                    // this half's scores
         if (!(ok = warp_wait(sm, sm.s_full[t][hb], i & 1, a.err))) break;
         tc_fence_after();
-        // scores of key columns [32 q4, 32 q4 + 32) in place: cap, bias, mask
-        auto finish = [&](int q4, float (&x)[32]) {
+        // scores of key columns [32 q4, 32 q4 + 32) in place -> log2 units minus a
+        // reference: cap, bias, mask
+        auto finish = [&](int q4, float (&x)[32], float minus_ref) {
           const int col = 32 * q4;
           float tanhs[32];
-          score_terms<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f);
+          score_args<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
+                                  [&](int) { return pack_f32x2(minus_ref, minus_ref); });
           if (partial) {
             const int lc = lim - k0 - col;
 #pragma unroll
@@ -590,7 +590,6 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         uint32_t w[2][16];
         auto exponentials = [&]() {
           const float ms = m == -INFINITY ? 0.0f : m;
-          const uint64_t c2 = pack_f32x2(c_exp, c_exp), ms2 = pack_f32x2(-ms, -ms);
           uint64_t ls[2] = {0, 0};
           float x[2][32];
           tmem_ld32x32f(tb, x[0]);
@@ -600,20 +599,13 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           for (int q2 = 0; q2 < 2; ++q2) {
             float(&y)[32] = x[q2];
             if (q2) tmem_wait_ld32(y);
-            finish(2 * hb + q2, y);
+            finish(2 * hb + q2, y, -ms);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
               // a quarter of the exponentials on the FMA pipe: 868 -> 834 us for 8192 x 24
-              // heads (an eighth 848, three eighths 862)
-              float p0, p1;
-              const uint64_t arg = fma_f32x2(pack_f32x2(y[2 * u], y[2 * u + 1]), c2, ms2);
-              if (u % 4 == 2) {
-                ex2_poly_f32x2(arg, p0, p1);
-              } else {
-                unpack_f32x2(arg, p0, p1);
-                p0 = ex2_approx(p0);
-                p1 = ex2_approx(p1);
-              }
+              // heads (an eighth 848, three eighths 862); none where the cap fills it
+              float p0 = y[2 * u], p1 = y[2 * u + 1];
+              ex2_pair(p0, p1, !kCap && u % 4 == 2);
               ls[u & 1] = add_f32x2(ls[u & 1], pack_f32x2(p0, p1));
               w[q2][u] = pack_bf16x2(p0, p1);
             }
@@ -637,11 +629,10 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             float x[32];
             tmem_ld32x32f(tb + 32 * q2, x);
             tmem_wait_ld32(x);
-            finish(2 * hb + q2, x);
+            finish(2 * hb + q2, x, 0.0f);
 #pragma unroll
             for (int u = 0; u < 32; ++u) top = fmaxf(top, x[u]);
           }
-          top *= c_exp;
           const bool grow = top > m;
           const float f = grow ? ex2_approx(m - top) : 1.0f;   // m = -inf: 0, and l and O are 0
           if (grow) m = top;

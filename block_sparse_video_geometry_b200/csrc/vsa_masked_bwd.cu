@@ -225,25 +225,16 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 }
 
 // Scores of 32 columns in place -> P against `ref` (minus lse in log2 units, a pair
-// of columns at a time), and into `w` P times the cap's derivative. A quarter of
-// the exponentials go to the FMA pipe.
+// of columns at a time), and into `w` P times the cap's derivative. Without a
+// cap a quarter of the exponentials go to the FMA pipe.
 template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const ScoreTerms& s, float d0, float dir,
                                               Ref ref) {
-  score_terms<kCap, kBias>(x, w, s, d0, dir);              // w: tanh
-  const uint64_t c2 = kCap || kBias ? pack_f32x2(1.0f, 1.0f) : pack_f32x2(s.c, s.c);
+  score_args<kCap, kBias>(x, w, s, d0, dir, ref);          // w: tanh
   const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
-    const uint64_t arg = fma_f32x2(pack_f32x2(x[u], x[u + 1]), c2, ref(u));
-    if (u % 8 == 4) {
-      ex2_poly_f32x2(arg, x[u], x[u + 1]);
-    } else {
-      float e0, e1;
-      unpack_f32x2(arg, e0, e1);
-      x[u] = ex2_approx(e0);
-      x[u + 1] = ex2_approx(e1);
-    }
+    ex2_pair(x[u], x[u + 1], !kCap && u % 8 == 4);
     if constexpr (kCap) {
       const uint64_t t = pack_f32x2(w[u], w[u + 1]);
       unpack_f32x2(mul_f32x2(pack_f32x2(x[u], x[u + 1]), fma_f32x2(mul_f32x2(t, neg), t, one)), w[u], w[u + 1]);
@@ -401,7 +392,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     const int key = k0 + quad * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
-    ScoreTerms terms{p.scale * kLog2e, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f, 0.0f};
+    ScoreTerms terms(p.scale, p.cap, 0.0f);
     // first query that sees this key by order
     const int i_min = !p.causal || key < prefix ? INT32_MIN : key - p.off;
     const int doc = p.documents && key < p.Sk ? p.doc_k[b * p.doc_k_sb + key] : -1;
@@ -618,8 +609,7 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     const uint32_t ts = lane_addr + kColS + 32 * part, tp = lane_addr + kColDp + 32 * part;
     const size_t at = (static_cast<size_t>(b) * p.Hq + h) * a.padded + q0 + quad * 32 + lane;
     const uint64_t lse2 = pack_f32x2(a.lse2[at], a.lse2[at]), minus_delta = pack_f32x2(a.delta[at], a.delta[at]);
-    const ScoreTerms terms{p.scale * kLog2e, p.cap * kLog2e, kCap ? p.scale / p.cap : 0.0f,
-                           kBias ? p.slopes[h] * kLog2e : 0.0f};
+    const ScoreTerms terms(p.scale, p.cap, kBias ? p.slopes[h] : 0.0f);
     const int lim = p.limit(b, i_q), lim0 = p.limit(b, q0);
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
