@@ -9,17 +9,17 @@
 // (one per pair; two more operations of that unit with a cap); one query over a
 // long cache: HBM (k and v read once).
 //
-// Design. A block owns 256 rows of one head as two M = 128 tiles and walks the
+// Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks the
 // key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
 // 32 KB stages; one warp issues the products, the two tiles in turn; two groups of
 // four warps run the softmax, a thread per row. Scores come in two buffers of 64
 // keys per query tile; P (bf16, the A operand of O += P V) overwrites its scores
 // in TMEM, and the next scores follow behind that product. The softmax's reference is raised, and O rescaled in TMEM,
 // only when a row's sum of P in a tile passes 2^32.
-// Few rows (a new token over a cache): the heads that share a key head are
-// packed into one tile, the two slots take the key tiles in turn with the same
-// queries, and the key axis is split over blocks; a second kernel joins the
-// parts.
+// Few rows: blocks of 128 rows, whose two slots take the key tiles in turn with the
+// same queries and join their results in shared memory. Few queries (a new token
+// over a cache): the heads that share a key head are packed into one tile, and the
+// key axis is split over blocks; a second kernel joins the parts.
 // Tiles that no row of the block sees are skipped: by arithmetic for causal
 // masks, by a list that plan_kernel makes from the tiles' document ranges.
 // Every wait is bounded (see vsa_masked_attn_status).
@@ -148,43 +148,19 @@ vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, 
 // ------------------------------------------------------------- small kernels
 namespace {
 
-// One block per (tile, head, batch entry): rows with an infinity or NaN, and the
-// tile's copy without them if there is one. HBM bound: x read once.
-__global__ void __launch_bounds__(256)
-scan_kernel(const uint16_t* __restrict__ x, Strides st, int S, Clean c) {
-  const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+// Rows of v with an infinity or NaN, and the tiles' copies without them. One block
+// per (head, tile, batch entry), heads first: neighbours read neighbouring memory.
+// HBM bound: v read once.
+__global__ void __launch_bounds__(kTileThreads) scan_kernel(const uint16_t* __restrict__ x, Strides st, int S, Clean c) {
+  const int h = blockIdx.x, tile = blockIdx.y, b = blockIdx.z;
   __shared__ uint32_t bad[4];
   if (threadIdx.x < 4) bad[threadIdx.x] = 0;
+  uint4 w[kPieces];
+  load_pieces(w, x + b * st.b + h * st.h + static_cast<int64_t>(tile) * kRows * st.s, st.s, min(kRows, S - tile * kRows));
   __syncthreads();
-  const int n = min(kRows, S - tile * kRows);
-  const uint16_t* base = x + b * st.b + h * st.h + static_cast<int64_t>(tile) * kRows * st.s;
-  uint4 w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = i * 256 + threadIdx.x, r = e >> 4;
-    w[i] = make_uint4(0, 0, 0, 0);
-    if (r < n) w[i] = *reinterpret_cast<const uint4*>(base + r * st.s + (e & 15) * 8);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = (i * 256 + threadIdx.x) >> 4;
-    bool any = false;
-    for (uint32_t v : {w[i].x, w[i].y, w[i].z, w[i].w})
-      any |= (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
-    if (any) atomicOr(&bad[r >> 5], 1u << (r & 31));
-  }
+  find_bad(w, bad);
   __syncthreads();
-  const uint4 m = make_uint4(bad[0], bad[1], bad[2], bad[3]);
-  if (threadIdx.x == 0) c.bad[(static_cast<size_t>(b) * gridDim.y + h) * gridDim.x + tile] = m;
-  if (!(m.x | m.y | m.z | m.w)) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = i * 256 + threadIdx.x, r = e >> 4;
-    if (r >= n) continue;
-    if ((bad[r >> 5] >> (r & 31)) & 1u) w[i] = make_uint4(0, 0, 0, 0);
-    const size_t row = (static_cast<size_t>(b) * S + tile * kRows + r) * gridDim.y + h;
-    *reinterpret_cast<uint4*>(c.copy + row * kHeadDim + (e & 15) * 8) = w[i];
-  }
+  write_clean(c, w, bad, b, h, gridDim.x, tile, gridDim.y, S);
 }
 
 // Smallest and largest document of positions [i0, i0 + n) of a row of ids
@@ -311,6 +287,8 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes];
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], drain[2];   // [slot][score buffer]
+  uint64_t first_done, second_out;   // one tile: slot 0 needs Q no longer; slot 1's result is in shared memory
+  float m1[kRows], l1[kRows];        // its maximum and sum; its O lies over Q, [channel][row]
   uint32_t tmem_base;
   int abort;
 };
@@ -327,11 +305,11 @@ struct Args {
   const int32_t* count;              // plan of visible tiles, or null
   const int32_t* list;
   int32_t packed;                    // rows = (head of the group, query), unit = key head; else unit = query head
-  int32_t units, rows, n_blocks;     // rows of a unit, blocks of 256 of them
-  int32_t one_tile;                  // rows <= 128: both slots hold the same rows and take turns over the key tiles
-  int32_t splits, parts;             // parts = splits, times 2 with one_tile
-  float* part_o;                     // [part][B][Hq][Sq][128], or null (parts == 1)
-  float* part_lse;                   // [part][B][Hq][Sq], log2
+  int32_t units, rows, n_blocks;     // rows of a unit, blocks of them
+  int32_t one_tile;                  // blocks of 128 rows, which both slots hold, taking turns over the key tiles; else 256
+  int32_t splits;                    // parts of the key axis
+  float* part_o;                     // [split][B][Hq][Sq][128], or null (splits == 1)
+  float* part_lse;                   // [split][B][Hq][Sq], log2
   int* err;
 };
 
@@ -379,6 +357,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one slot, or by both
     }
     mbar_init(smem_u32(&sm.q_full), 8);
+    mbar_init(smem_u32(&sm.first_done), 4);
+    mbar_init(smem_u32(&sm.second_out), 4);
     for (int t = 0; t < 2; ++t) {
       for (int hb = 0; hb < 2; ++hb) {
         mbar_init(smem_u32(&sm.s_full[t][hb]), 1);
@@ -405,7 +385,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if (a.count) {
     n_all = a.count[plan_row];
   } else {
-    const int last = a.packed ? p.Sq - 1 : min(qb * 256 + 255, p.Sq - 1);
+    const int last = a.packed ? p.Sq - 1 : min((qb + 1) * (one ? kRows : 2 * kRows), p.Sq) - 1;
     n_all = max(0, p.limit(b, last) + kRows) / kRows;     // tiles up to the last row's limit (none: below 0)
   }
   const int32_t* list = a.count ? a.list + plan_row * p.nkt : nullptr;
@@ -512,7 +492,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int r = threadIdx.x & 127;                       // row of the tile = TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ts = lane_addr + kColS + 128 * t, to = lane_addr + kColO + 128 * t;
-    const int tile_row0 = qb * 256 + (one ? 0 : t * 128);
+    const int tile_row0 = one ? qb * kRows : (2 * qb + t) * kRows;
     // rows of Q into shared memory, 16 lanes per row (rows past the end: zero)
     if (!one || t == 0) {
       for (int it = 0; it < 16; ++it) {
@@ -670,14 +650,46 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       ok = warp_wait(sm, sm.pv_done[t], 0, a.err) && warp_wait(sm, sm.pv_done[t], 1, a.err);
       tc_fence_after();
     }
-    if (ok && !(one && t == 1 && a.parts == 1)) {
+    float* o1 = reinterpret_cast<float*>(sm.q[0]);          // 64 KB over both Q tiles
+    float f0 = 1.0f, f1 = 0.0f;
+    if (one && ok) {
+      if (t == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.first_done));
+        ok = warp_wait(sm, sm.second_out, 0, a.err);
+        if (ok) {
+          const float m1 = sm.m1[r], l1 = sm.l1[r], top = fmaxf(m, m1), ref = top == -INFINITY ? 0.0f : top;
+          f0 = ex2_approx(m - ref);
+          f1 = ex2_approx(m1 - ref);
+          l = fmaf(l, f0, l1 * f1);
+          m = top;
+        }
+      } else {
+        ok = warp_wait(sm, sm.first_done, 0, a.err);
+        if (ok) {
+          sm.m1[r] = m;
+          sm.l1[r] = l;
+#pragma unroll 1
+          for (int q4 = 0; i > 0 && q4 < 4; ++q4) {
+            float o[32];
+            tmem_ld32x32f(to + 32 * q4, o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o1[(32 * q4 + u) * kRows + r] = o[u];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.second_out));
+        }
+      }
+    }
+    if (ok && !(one && t == 1)) {
+      const bool second = one && n > 1;                      // slot 1 had a key tile
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
       const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.Sq + i_q;
-      const int part = one ? split * 2 + t : split;
       const size_t all = static_cast<size_t>(p.B) * p.Hq * p.Sq;
       if (live) {
-        if (a.part_o) a.part_lse[part * all + at] = lse2;
+        if (a.part_o) a.part_lse[split * all + at] = lse2;
         else a.lse[at] = lse2 * 0.6931471805599453f;
       }
 #pragma unroll 1
@@ -691,19 +703,24 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0.0f;
         }
-        if (!live) continue;
+        if (live) {
+          if (second) {
 #pragma unroll
-        for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
-        if (a.part_o) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + (part * all + at) * kHeadDim + 32 * q4);
+            for (int u = 0; u < 32; ++u) o[u] = fmaf(o1[(32 * q4 + u) * kRows + r], f1, o[u] * f0);
+          }
 #pragma unroll
-          for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + 32 * q4);
+          for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
+          if (a.part_o) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (split * all + at) * kHeadDim + 32 * q4);
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                                pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+            for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + 32 * q4);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                                  pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+          }
         }
       }
     }
@@ -726,7 +743,7 @@ join_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31;
   float top = -INFINITY;
   bool nan = false;
-  for (int s = lane; s < a.parts; s += 32) {
+  for (int s = lane; s < a.splits; s += 32) {
     const float x = a.part_lse[s * all + at];
     top = fmaxf(top, x);
     nan |= isnan(x);
@@ -737,7 +754,7 @@ join_kernel(const __grid_constant__ Args a) {
   const float ref = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int s = 0; s < a.parts; ++s) {
+  for (int s = 0; s < a.splits; ++s) {
     const float w = exp2f(a.part_lse[s * all + at] - ref);
     const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * all + at) * kHeadDim + lane * 4);
     sum += w;
@@ -772,35 +789,51 @@ __global__ void __launch_bounds__(256) empty_kernel(const __grid_constant__ Args
 
 // How the rows are laid over blocks, and how often the key axis is split.
 struct Layout {
-  int32_t packed, units, rows, n_blocks, one_tile, splits, parts;
+  int32_t packed, units, rows, n_blocks, one_tile, splits;
 };
 
-// The heads of a group share a tile when all their queries fit one block. The
-// key axis is split where blocks are too few: the count that leaves the last
-// block finished first, a block costing its key tiles and about four more
-// (start, epilogue), a split also the joining pass.
+// The heads of a group share a tile when all their queries fit 128 rows. Blocks
+// of 256 rows read each key tile once for two query tiles; blocks of 128 rows
+// leave less of the GPU idle where blocks are few or of different length (2 x
+// 1,111 queries over 5,003 keys, 24 heads: 240 or 432 blocks on 148 SMs). The key
+// axis is split where there are fewer blocks than SMs. The choice is the least of an
+// estimate in quarters of a 256-row block's key tile: for equal blocks the rounds
+// they take, under a causal mask the work spread over all SMs and a third of the
+// longest block; a block adds its start and end, splitting the joining pass.
 Layout layout_of(const Problem& p) {
-  Layout L{};
-  L.packed = p.group > 1 && static_cast<int64_t>(p.group) * p.Sq <= 256;
-  L.units = L.packed ? p.Hk : p.Hq;
-  L.rows = L.packed ? p.group * p.Sq : p.Sq;
-  L.n_blocks = (L.rows + 255) / 256;
-  L.one_tile = L.rows <= kRows;
-  const int64_t ctas = static_cast<int64_t>(L.n_blocks) * L.units * p.B, sms = sm_count();
-  const int per_tile = L.one_tile ? 2 : 4;               // cost of a key tile: one slot's work, or both
-  double best = 1e300;
-  L.splits = 1;
-  for (int s = 1; s <= 64 && s <= std::max(1, p.nkt / 2); ++s) {
-    const double waves = static_cast<double>((ctas * s + sms - 1) / sms);
-    const double t = waves * (per_tile * ((p.nkt + s - 1) / s) + 16.0) + (s > 1 ? 16.0 : 0.0);
-    if (t < best * 0.97) {
-      best = t;
-      L.splits = s;
+  Layout best{};
+  best.packed = p.group > 1 && static_cast<int64_t>(p.group) * p.Sq <= kRows;
+  best.units = best.packed ? p.Hk : p.Hq;
+  best.rows = best.packed ? p.group * p.Sq : p.Sq;
+  const double sms = sm_count(), pairs = static_cast<double>(best.units) * p.B;
+  double least = 1e300;
+  for (int one = best.rows <= kRows ? 1 : 0; one < 2; ++one) {
+    const int per = one ? kRows : 2 * kRows, n_blocks = (best.rows + per - 1) / per;
+    // one tile reads the key tile for half the rows; where no other block reads it, HBM bounds it
+    const double tile = !one ? 4.0 : n_blocks > 1 ? 2.2 : 3.3, fixed = one && n_blocks == 1 ? 16.0 : 6.0;
+    // key tiles of the blocks together, and of the longest
+    double total = static_cast<double>(n_blocks) * p.nkt;
+    const bool unequal = p.causal && !best.packed && n_blocks > 1;
+    if (unequal) {
+      total = 0.0;
+      for (int qb = 0; qb < n_blocks; ++qb)
+        total += std::max(0, std::min(p.nkt, (std::min((qb + 1) * per, p.Sq) + p.off + kRows - 1) / kRows));
+    }
+    for (int s = 1; s <= 64 && s <= std::max(1, p.nkt / 2); ++s) {
+      const double longest = tile * ((p.nkt + s - 1) / s) + fixed, blocks = n_blocks * pairs * s;
+      const double work = pairs * (tile * total + fixed * n_blocks * s) / sms;
+      double t = unequal ? std::max(longest, work + longest / 3.0) : std::ceil(blocks / sms) * longest;
+      // a split writes and reads its rows in 32 bits (0.45 us a unit, 6.5 TB/s) behind one more launch
+      if (s > 1) t += 12.0 + pairs * best.rows * s * 1024.0 / 6.5e12 / 0.45e-6;
+      if (t < least * 0.97) {
+        least = t;
+        best.n_blocks = n_blocks;
+        best.one_tile = one;
+        best.splits = s;
+      }
     }
   }
-  L.parts = L.splits * (L.one_tile ? 2 : 1);
-  if (L.one_tile && p.nkt == 1) L.parts = 1;             // one key tile: the second slot has no work
-  return L;
+  return best;
 }
 
 struct Workspace {
@@ -825,8 +858,8 @@ Workspace workspace_of(const Problem& p, const Layout& L) {
     w.bad = take(b * p.Hk * nkt * sizeof(uint4));
     w.copy = take(b * p.Sk * p.Hk * kHeadDim * 2);
   }
-  if (L.parts > 1) {
-    const size_t rows = b * p.Hq * p.Sq * static_cast<size_t>(L.parts);
+  if (L.splits > 1) {
+    const size_t rows = b * p.Hq * p.Sq * static_cast<size_t>(L.splits);
     w.part_o = take(rows * kHeadDim * sizeof(float));
     w.part_lse = take(rows * sizeof(float));
   }
@@ -856,13 +889,6 @@ void plan_keys(const Problem& p, const int4* range, int4* range_q, int32_t* coun
   const int nqt = tiles(p.Sq);
   range_kernel<<<dim3((nqt + 3) / 4, p.B), 128, 0, stream>>>(p.doc_q, p.doc_q_sb, p.Sq, nqt, range_q);
   plan_keys_kernel<<<dim3(p.nkt, p.B), 256, 0, stream>>>(p, range, range_q, nqt, count, list);
-}
-
-vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream) {
-  const dim3 grid(tiles(S), x->heads, B);
-  scan_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x->data), view_strides(x, B, S), S, c);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn: scan", e);
 }
 
 }  // namespace masked
@@ -937,9 +963,8 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
   a.n_blocks = L.n_blocks;
   a.one_tile = L.one_tile;
   a.splits = L.splits;
-  a.parts = L.parts;
   a.err = reinterpret_cast<int*>(ws);
-  if (L.parts > 1) {
+  if (L.splits > 1) {
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   }
@@ -947,20 +972,21 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
     int4* range = reinterpret_cast<int4*>(ws + w.range);
     a.count = reinterpret_cast<int32_t*>(ws + w.count);
     a.list = reinterpret_cast<int32_t*>(ws + w.list);
-    plan(a.p, L.packed || L.one_tile ? kPlanAll : kPlanPairs, L.n_blocks, range,
+    plan(a.p, L.packed ? kPlanAll : L.one_tile ? kPlanSingle : kPlanPairs, L.n_blocks, range,
          reinterpret_cast<int32_t*>(ws + w.count), reinterpret_cast<int32_t*>(ws + w.list), stream);
   }
   if (a.p.masked) {
     a.clean_v = Clean{reinterpret_cast<uint4*>(ws + w.bad), reinterpret_cast<uint16_t*>(ws + w.copy)};
     st = make_map(&mvc, a.clean_v.copy, B, Sk, k->heads);
-    if (st == VSA_OK) st = scan(v, B, Sk, a.clean_v, stream);
     if (st != VSA_OK) return st;
+    scan_kernel<<<dim3(k->heads, a.p.nkt, B), kTileThreads, 0, stream>>>(static_cast<const uint16_t*>(v->data), sv, Sk,
+                                                                         a.clean_v);
   }
   const bool cap = a.p.cap > 0.0f, bias = a.p.slopes != nullptr;
   st = cap ? (bias ? launch<true, true>(a, mk, mv, mvc, stream) : launch<true, false>(a, mk, mv, mvc, stream))
            : (bias ? launch<false, true>(a, mk, mv, mvc, stream) : launch<false, false>(a, mk, mv, mvc, stream));
   if (st != VSA_OK) return st;
-  if (L.parts > 1) join_kernel<<<row_blocks, 256, 0, stream>>>(a);
+  if (L.splits > 1) join_kernel<<<row_blocks, 256, 0, stream>>>(a);
   e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_fwd", e);
 }

@@ -49,6 +49,49 @@ struct Clean {
 
 inline int tiles(int n) { return (n + kRows - 1) / kRows; }
 
+#ifdef __CUDACC__
+constexpr int kTileThreads = 256;           // threads that hold a tile: 8 pieces of 16 bytes each
+constexpr int kPieces = 8;
+
+// Piece i of thread t is row (256 i + t) / 16, channels 8 ((256 i + t) % 16) ..+7; rows past n: zero.
+__device__ __forceinline__ void load_pieces(uint4 (&w)[kPieces], const uint16_t* base, int64_t row_stride, int n) {
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = i * kTileThreads + threadIdx.x, r = e >> 4;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (r < n) w[i] = *reinterpret_cast<const uint4*>(base + r * row_stride + (e & 15) * 8);
+  }
+}
+
+// Marks the rows of the block's tile that hold an infinity or NaN (bad[4], cleared).
+__device__ __forceinline__ void find_bad(const uint4 (&w)[kPieces], uint32_t* bad) {
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int r = (i * kTileThreads + threadIdx.x) >> 4;
+    bool any = false;
+    for (uint32_t v : {w[i].x, w[i].y, w[i].z, w[i].w})
+      any |= (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+    if (any) atomicOr(&bad[r >> 5], 1u << (r & 31));
+  }
+}
+
+// Behind a barrier: the tile's marks, and its copy without such rows if there are any.
+__device__ __forceinline__ void write_clean(const Clean& c, uint4 (&w)[kPieces], const uint32_t* bad, int b, int h,
+                                            int heads, int tile, int n_tiles, int S) {
+  const uint4 m = make_uint4(bad[0], bad[1], bad[2], bad[3]);
+  if (threadIdx.x == 0) c.bad[(static_cast<size_t>(b) * heads + h) * n_tiles + tile] = m;
+  if (!(m.x | m.y | m.z | m.w)) return;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = i * kTileThreads + threadIdx.x, r = e >> 4;
+    if (tile * kRows + r >= S) continue;
+    if ((bad[r >> 5] >> (r & 31)) & 1u) w[i] = make_uint4(0, 0, 0, 0);
+    const size_t row = (static_cast<size_t>(b) * S + tile * kRows + r) * heads + h;
+    *reinterpret_cast<uint4*>(c.copy + row * kHeadDim + (e & 15) * 8) = w[i];
+  }
+}
+#endif
+
 // cuTensorMapEncodeTiled over a view: boxes of 64 channels x 128 rows of one
 // head and batch entry, 128-byte swizzled, rows past S read as zero.
 vsa_status make_map(CUtensorMap* map, const vsa_view* v, int32_t B, int32_t S);
@@ -58,9 +101,6 @@ vsa_status make_map(CUtensorMap* map, const uint16_t* copy, int32_t B, int32_t S
 vsa_status check(const vsa_mask* mask, const vsa_mask_terms* t, int32_t B, int32_t Sq, int32_t Sk, int32_t Hq,
                  int32_t Hk, Problem* p);
 vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, bool output);
-
-// Scans x for rows with infinities or NaN (see Clean).
-vsa_status scan(const vsa_view* x, int32_t B, int32_t S, const Clean& c, cudaStream_t stream);
 
 // Records of a list of visible tiles: the tile, and where documents hide part of
 // it from query tile 0 or 1 of the block.

@@ -41,14 +41,17 @@ namespace {
 
 // ------------------------------------------------------------------ prepare
 // Minus D and minus lse2 of every row, [B][Hq][nqt * 128]; rows past Sq, and rows
-// without visible keys: 0 and -inf, so that P = 0.
-// 16 lanes per row. HBM bound: out and dout read once.
+// without visible keys: 0 and -inf, so that P = 0. Where the call masks anything,
+// also the rows of dout, q and k with an infinity or NaN (see Clean). One block per
+// (head of q, then of k; tile; batch entry), heads first: neighbours read
+// neighbouring memory. HBM bound: out and dout (and q, k) read once.
 struct PrepArgs {
-  const uint16_t *out, *dout;
-  Strides so, sd;
+  const uint16_t *out, *dout, *q, *k;
+  Strides so, sd, sq, sk;
   const float* lse;
-  int32_t B, Hq, Sq, padded;
+  int32_t Hq, Hk, Sq, Sk, nqt, nkt, masked;
   float *lse2, *delta;
+  Clean clean_q, clean_o, clean_k;
 };
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
@@ -62,24 +65,49 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   return s;
 }
 
-__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepArgs a) {
-  const int i = blockIdx.x * 16 + (threadIdx.x >> 4), h = blockIdx.y, c = threadIdx.x & 15;
-  const int64_t b = blockIdx.z;
-  float d = 0.0f, l = -INFINITY;
-  if (i < a.Sq) {
-    const uint4 o = *reinterpret_cast<const uint4*>(a.out + b * a.so.b + i * a.so.s + h * a.so.h + c * 8);
-    const uint4 g = *reinterpret_cast<const uint4*>(a.dout + b * a.sd.b + i * a.sd.s + h * a.sd.h + c * 8);
-    d = dot8(o, g);
-    l = a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Sq + i] * -kLog2e;
-    if (l == INFINITY) l = -INFINITY;
+__global__ void __launch_bounds__(kTileThreads) prepare_kernel(const __grid_constant__ PrepArgs a) {
+  const int tile = blockIdx.y, b = blockIdx.z;
+  const bool key = static_cast<int>(blockIdx.x) >= a.Hq;
+  const int h = key ? blockIdx.x - a.Hq : blockIdx.x;
+  if (tile >= (key ? a.nkt : a.nqt)) return;               // the whole block
+  __shared__ uint32_t bad[2][4];
+  if (threadIdx.x < 8) (&bad[0][0])[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t r0 = static_cast<int64_t>(tile) * kRows;
+  uint4 w[kPieces];
+  if (key) {
+    load_pieces(w, a.k + b * a.sk.b + r0 * a.sk.s + h * a.sk.h, a.sk.s, min(kRows, a.Sk - tile * kRows));
+    find_bad(w, bad[0]);
+    __syncthreads();
+    write_clean(a.clean_k, w, bad[0], b, h, a.Hk, tile, a.nkt, a.Sk);
+    return;
   }
+  const int n = min(kRows, a.Sq - tile * kRows);
+  load_pieces(w, a.dout + b * a.sd.b + r0 * a.sd.s + h * a.sd.h, a.sd.s, n);
+  const size_t row0 = (static_cast<size_t>(b) * a.Hq + h) * a.nqt * kRows + r0;
+  const float* lse = a.lse + (static_cast<size_t>(b) * a.Hq + h) * a.Sq + r0;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (c == 0 && i < a.padded) {
-    const size_t at = (static_cast<size_t>(b) * a.Hq + h) * a.padded + i;
-    a.delta[at] = -d;
-    a.lse2[at] = l;
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = i * kTileThreads + threadIdx.x, r = e >> 4;
+    float d = 0.0f;
+    if (r < n) d = dot8(w[i], *reinterpret_cast<const uint4*>(a.out + b * a.so.b + (r0 + r) * a.so.s + h * a.so.h + (e & 15) * 8));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((e & 15) == 0) {
+      float l = -INFINITY;
+      if (r < n) l = lse[r] * -kLog2e;
+      a.delta[row0 + r] = -d;
+      a.lse2[row0 + r] = l == INFINITY ? -INFINITY : l;
+    }
   }
+  if (!a.masked) return;
+  find_bad(w, bad[0]);
+  __syncthreads();
+  write_clean(a.clean_o, w, bad[0], b, h, a.Hq, tile, a.nqt, a.Sq);
+  load_pieces(w, a.q + b * a.sq.b + r0 * a.sq.s + h * a.sq.h, a.sq.s, n);
+  find_bad(w, bad[1]);
+  __syncthreads();
+  write_clean(a.clean_q, w, bad[1], b, h, a.Hq, tile, a.nqt, a.Sq);
 }
 
 // ------------------------------------------------------------------- shared
@@ -812,25 +840,42 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
   PrepArgs pa{};
   pa.out = static_cast<const uint16_t*>(out->data);
   pa.dout = static_cast<const uint16_t*>(dout->data);
+  pa.q = static_cast<const uint16_t*>(q->data);
+  pa.k = static_cast<const uint16_t*>(k->data);
   pa.so = view_strides(out, B, Sq);
   pa.sd = view_strides(dout, B, Sq);
+  pa.sq = view_strides(q, B, Sq);
+  pa.sk = view_strides(k, B, Sk);
   pa.lse = lse;
-  pa.B = B;
   pa.Hq = p.Hq;
+  pa.Hk = p.Hk;
   pa.Sq = Sq;
-  pa.padded = nqt * kRows;
+  pa.Sk = Sk;
+  pa.nqt = nqt;
+  pa.nkt = p.nkt;
+  pa.masked = p.masked;
   pa.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   pa.delta = reinterpret_cast<float*>(ws + w.delta);
-  prepare_kernel<<<dim3(nqt * kRows / 16, p.Hq, B), 256, 0, stream>>>(pa);
+  if (p.masked) {
+    pa.clean_q = Clean{reinterpret_cast<uint4*>(ws + w.bad_q), reinterpret_cast<uint16_t*>(ws + w.copy_q)};
+    pa.clean_o = Clean{reinterpret_cast<uint4*>(ws + w.bad_o), reinterpret_cast<uint16_t*>(ws + w.copy_o)};
+    pa.clean_k = Clean{reinterpret_cast<uint4*>(ws + w.bad_k), reinterpret_cast<uint16_t*>(ws + w.copy_k)};
+    if ((st = make_map(&m.qc, pa.clean_q.copy, B, Sq, p.Hq)) != VSA_OK ||
+        (st = make_map(&m.oc, pa.clean_o.copy, B, Sq, p.Hq)) != VSA_OK ||
+        (st = make_map(&m.kc, pa.clean_k.copy, B, Sk, p.Hk)) != VSA_OK)
+      return st;
+  }
+  prepare_kernel<<<dim3(p.Hq + (p.masked ? p.Hk : 0), p.masked ? std::max(nqt, p.nkt) : nqt, B), kTileThreads, 0,
+                   stream>>>(pa);
 
   Args g{};
   g.p = p;
   g.lse2 = pa.lse2;
   g.delta = pa.delta;
-  g.padded = pa.padded;
+  g.padded = nqt * kRows;
   g.nqt = nqt;
   g.err = reinterpret_cast<int*>(ws);
-  const Strides sq = view_strides(q, B, Sq), sd = pa.sd, sk = view_strides(k, B, Sk), sv = view_strides(v, B, Sk);
+  const Strides sq = pa.sq, sd = pa.sd, sk = pa.sk, sv = view_strides(v, B, Sk);
   Args kv = g, qq = g;
   kv.a_h = qq.o1_h = sq.h != 0;
   kv.a_b = qq.o1_b = sq.b != 0;
@@ -857,18 +902,9 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
     kv.count = ck;
     kv.list = lk;
   }
-  if (p.masked) {
-    kv.clean_a = Clean{reinterpret_cast<uint4*>(ws + w.bad_q), reinterpret_cast<uint16_t*>(ws + w.copy_q)};
-    kv.clean_b = Clean{reinterpret_cast<uint4*>(ws + w.bad_o), reinterpret_cast<uint16_t*>(ws + w.copy_o)};
-    qq.clean_a = Clean{reinterpret_cast<uint4*>(ws + w.bad_k), reinterpret_cast<uint16_t*>(ws + w.copy_k)};
-    if ((st = make_map(&m.qc, kv.clean_a.copy, B, Sq, p.Hq)) != VSA_OK ||
-        (st = make_map(&m.oc, kv.clean_b.copy, B, Sq, p.Hq)) != VSA_OK ||
-        (st = make_map(&m.kc, qq.clean_a.copy, B, Sk, p.Hk)) != VSA_OK)
-      return st;
-    if ((st = scan(q, B, Sq, kv.clean_a, stream)) != VSA_OK || (st = scan(dout, B, Sq, kv.clean_b, stream)) != VSA_OK ||
-        (st = scan(k, B, Sk, qq.clean_a, stream)) != VSA_OK)
-      return st;
-  }
+  kv.clean_a = pa.clean_q;
+  kv.clean_b = pa.clean_o;
+  qq.clean_a = pa.clean_k;
   const bool cap = p.cap > 0.0f, bias = p.slopes != nullptr;
   if (cap) return bias ? launch<true, true>(kv, qq, m, stream) : launch<true, false>(kv, qq, m, stream);
   return bias ? launch<false, true>(kv, qq, m, stream) : launch<false, false>(kv, qq, m, stream);
