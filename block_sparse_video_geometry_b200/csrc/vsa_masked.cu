@@ -195,7 +195,8 @@ range_kernel(const int32_t* __restrict__ ids, int64_t sb, int S, int n_tiles, in
 }
 
 __device__ __forceinline__ bool meet(int4 a, int4 b) { return a.x <= b.y && b.x <= a.y; }
-__device__ __forceinline__ bool same(int4 a, int4 b) { return a.x == a.y && b.x == b.y && a.x == b.x && !a.z && !b.z; }
+__device__ __forceinline__ bool one_doc(int4 a) { return a.x == a.y && !a.z; }
+__device__ __forceinline__ bool same(int4 a, int4 b) { return one_doc(a) && one_doc(b) && a.x == b.x; }
 
 // Appends the records (>= 0) of a block's 256 threads to `out` from `total`, in
 // thread order; returns the new total.
@@ -242,7 +243,7 @@ plan_kernel(const __grid_constant__ Problem p, const int4* __restrict__ range, P
         any |= meet(k, q[t]) && kt * kRows <= q[t].w;
         if (!same(k, q[t])) flags |= t ? kPartial1 : kPartial0;
       }
-      if (any) rec = kt | flags;
+      if (any) rec = kt | flags | (one_doc(k) ? kOneDoc : 0);
     }
     total = append(rec, total, out, n_warp);
   }
@@ -265,7 +266,7 @@ plan_keys_kernel(const __grid_constant__ Problem p, const int4* __restrict__ ran
     if (qt < nqt) {
       const int4 q = range_q[static_cast<size_t>(b) * nqt + qt];
       if (meet(k, q) && kt * kRows <= p.limit(b, min((qt + 1) * kRows, p.Sq) - 1))
-        rec = qt | (same(k, q) ? 0 : kPartial0);
+        rec = qt | (same(k, q) ? 0 : kPartial0) | (one_doc(q) ? kOneDoc : 0);
     }
     total = append(rec, total, out, n_warp);
   }
@@ -529,8 +530,10 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     for (int j = one ? t : 0; j < n; j += step, ++i) {
       const int rec = list ? list[s1 - 1 - j] : s1 - 1 - j;
       const int kt = rec & kTileMask, k0 = kt * kRows;
-      const bool part_doc = rec & (t ? kPartial1 : kPartial0);
-      const bool partial = part_doc || k0 + kRows - 1 > lim0;
+      // a tile of one document is hidden from a row as a whole or not at all
+      const bool by_doc = rec & (t ? kPartial1 : kPartial0), part_doc = by_doc && !(rec & kOneDoc);
+      const bool partial = by_doc || k0 + kRows - 1 > lim0;
+      const int lim_t = by_doc && !part_doc && (doc < 0 || __ldg(dk + k0) != doc) ? -1 : lim;
       uint4 bm = make_uint4(0, 0, 0, 0);
       if (bad) bm = bad[kt];
       const bool flagged = bm.x | bm.y | bm.z | bm.w;
@@ -546,7 +549,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           score_args<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
                                   [&](int) { return pack_f32x2(minus_ref, minus_ref); });
           if (partial) {
-            const int lc = lim - k0 - col;
+            const int lc = lim_t - k0 - col;
 #pragma unroll
             for (int u = 0; u < 32; ++u) x[u] = u <= lc ? x[u] : -INFINITY;
             if (part_doc) {

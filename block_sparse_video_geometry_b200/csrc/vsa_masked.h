@@ -102,9 +102,9 @@ vsa_status check(const vsa_mask* mask, const vsa_mask_terms* t, int32_t B, int32
                  int32_t Hk, Problem* p);
 vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, bool output);
 
-// Records of a list of visible tiles: the tile, and where documents hide part of
-// it from query tile 0 or 1 of the block.
-constexpr int kPartial0 = 1 << 29, kPartial1 = 1 << 30, kTileMask = kPartial0 - 1;
+// Records of a list of visible tiles: the tile, whether it holds one document only,
+// and whether documents hide part of it from query tile 0 or 1 of the block.
+constexpr int kOneDoc = 1 << 28, kPartial0 = 1 << 29, kPartial1 = 1 << 30, kTileMask = kOneDoc - 1;
 
 // Visible key tiles of query blocks (documents only). `range`: [B][nkt] scratch;
 // count [B][n_blocks], list [B][n_blocks][nkt] out.

@@ -142,6 +142,8 @@ struct Args {
   int32_t padded, nqt;
   const int32_t *count, *list;               // visible tiles of the other side, or null
   uint16_t *out1, *out2;                     // dkv: dk, dv; dq: dq
+  int32_t splits;                            // dkv: parts of a key tile's query tiles, one block each
+  float* part;                               // [split][dk, dv][B][Hk][nkt * 128][128], or null (splits == 1)
   Strides so1, so2;
   int* err;
 };
@@ -206,6 +208,21 @@ __device__ __forceinline__ void write_columns(uint32_t taddr, bool have, float f
   for (int u = 0; u < 4; ++u)
     dst[u] = make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
                         pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f), pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
+}
+
+// 32 columns of 32-bit sums times `f` (or zeros).
+__device__ __forceinline__ void write_part(uint32_t taddr, bool have, float f, float* row) {
+  float o[32];
+  if (have) {
+    tmem_ld32x32f(taddr, o);
+    tmem_wait_ld32(o);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 32; ++u) o[u] = 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < 32; u += 4)
+    *reinterpret_cast<float4*>(row + u) = make_float4(o[u] * f, o[u + 1] * f, o[u + 2] * f, o[u + 3] * f);
 }
 
 // Barriers and TMEM; `warps` elementwise warps arrive per score buffer.
@@ -298,8 +315,9 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = p.Hk * p.B, kt = blockIdx.x / per;       // early key tiles, the longest under a causal mask, first
-  const int hk = blockIdx.x % per % p.Hk, b = blockIdx.x % per / p.Hk;
+  // early key tiles, the longest under a causal mask, first
+  const int per = p.Hk * p.B * a.splits, kt = blockIdx.x / per, split = blockIdx.x % per % a.splits;
+  const int hk = blockIdx.x % per / a.splits % p.Hk, b = blockIdx.x % per / a.splits / p.Hk;
   const int k0 = kt * kRows;
   const uint32_t tmem = set_up(sm, kEw / 2, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 2);                // dO is read by dP^T and by dV
@@ -318,7 +336,10 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     len = max(0, a.nqt - first);
   }
   const int32_t* list = a.count ? a.list + row * a.nqt : nullptr;
-  const int n = len * p.group;
+  // this block's part of them, counted over the group's heads
+  const int all = len * p.group, begin = static_cast<int>(static_cast<int64_t>(all) * split / a.splits);
+  const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / a.splits) - begin;
+  const int h_begin = hk * p.group + (len ? begin / len : 0), idx_begin = len ? begin % len : 0;
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
@@ -326,7 +347,7 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       mbar_arrive_expect_tx(smem_u32(&sm.own_full), 2 * kTileBytes);
       load_tile(sm.own[0], &map_k, k0, a.o1_h ? hk : 0, a.o1_b ? b : 0, sm.own_full);
       load_tile(sm.own[1], &map_v, k0, a.o2_h ? hk : 0, a.o2_b ? b : 0, sm.own_full);
-      int j = 0, h = hk * p.group, idx = 0;
+      int j = 0, h = h_begin, idx = idx_begin;
       size_t last = 0;                                     // rows of the tile before
       for (; j <= n; ++j, ++idx) {
         if (idx == len) idx = 0, ++h;
@@ -426,14 +447,15 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
     const int doc = p.documents && key < p.Sk ? p.doc_k[b * p.doc_k_sb + key] : -1;
     const int32_t* dq = p.documents ? p.doc_q + b * p.doc_q_sb : nullptr;
     bool ok = true;
-    int h = hk * p.group, idx = 0;
+    int h = h_begin, idx = idx_begin;
     for (int j = 0; j < n; ++j, ++idx) {
       if (idx == len) idx = 0, ++h;
       const int st = j & 1;
       const int rec = list ? list[idx] : first + idx;
       const int qt = rec & kTileMask, q0 = qt * kRows, i0 = q0 + 32 * part;
-      const bool part_doc = rec & kPartial0;
-      const bool partial = part_doc || (p.causal && prefix < k0 + kRows && q0 + p.off < k0 + kRows - 1);
+      // a tile of one document is hidden from a key as a whole or not at all
+      const bool by_doc = rec & kPartial0, part_doc = by_doc && !(rec & kOneDoc);
+      const bool partial = by_doc || (p.causal && prefix < k0 + kRows && q0 + p.off < k0 + kRows - 1);
       uint32_t bad = 0;                                    // columns whose q or dout holds an infinity or NaN
       if (a.clean_a.bad) {
         const size_t tile = (static_cast<size_t>(b) * p.Hq + h) * a.nqt + qt;
@@ -445,8 +467,9 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       uint32_t see = 0xffffffffu;
       if (partial) {
         see = 0;
+        const int from = by_doc && !part_doc && (doc < 0 || __ldg(dq + q0) != doc) ? INT32_MAX : i_min;
 #pragma unroll
-        for (int u = 0; u < 32; ++u) see |= (i0 + u >= i_min ? 1u : 0u) << u;
+        for (int u = 0; u < 32; ++u) see |= (i0 + u >= from ? 1u : 0u) << u;
         if (part_doc) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
@@ -503,7 +526,13 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
       ok = warp_wait(sm, sm.acc[0], 0, a.err) && warp_wait(sm, sm.acc[1], 0, a.err);
       tc_fence_after();
     }
-    if (ok) {
+    if (ok && a.part) {
+      const size_t rows = static_cast<size_t>(p.B) * p.Hk * p.nkt * kRows;
+      const size_t at = (static_cast<size_t>(b) * p.Hk + hk) * p.nkt * kRows + key;
+      float* dst = a.part + (2 * split * rows + at) * kHeadDim + 32 * part;
+      write_part(lane_addr + kColDk + 32 * part, n > 0, p.scale, dst);
+      write_part(lane_addr + kColDv + 32 * part, n > 0, 1.0f, dst + rows * kHeadDim);
+    } else if (ok) {
       const bool live = key < p.Sk;
       const int64_t kk = live ? key : 0;
       write_columns(lane_addr + kColDk + 32 * part, n > 0, p.scale, live,
@@ -645,15 +674,17 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
     for (int j = 0; j < n; ++j) {
       const int rec = list ? list[j] : j;
       const int kt = rec & kTileMask, k0 = kt * kRows, col = k0 + 32 * part;
-      const bool part_doc = rec & kPartial0;
-      const bool partial = part_doc || k0 + kRows - 1 > lim0;
+      // a tile of one document is hidden from a row as a whole or not at all
+      const bool by_doc = rec & kPartial0, part_doc = by_doc && !(rec & kOneDoc);
+      const bool partial = by_doc || k0 + kRows - 1 > lim0;
+      const int lim_t = by_doc && !part_doc && (doc < 0 || __ldg(dk + k0) != doc) ? -1 : lim;
       uint32_t bad_k = 0;                                  // columns whose k holds an infinity or NaN
       if (bad) bad_k = reinterpret_cast<const uint32_t*>(bad + kt)[part];
       uint32_t see = 0xffffffffu;
       if (partial) {
         see = 0;
 #pragma unroll
-        for (int u = 0; u < 32; ++u) see |= (col + u <= lim ? 1u : 0u) << u;
+        for (int u = 0; u < 32; ++u) see |= (col + u <= lim_t ? 1u : 0u) << u;
         if (part_doc) {
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
@@ -706,6 +737,24 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
   finish(tmem);
 }
 
+// dk and dv from the blocks' parts, added in order: one piece of 4 channels a thread.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  const Problem& p = a.p;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, c = e & 31, r = e >> 5;
+  if (r >= static_cast<int64_t>(p.B) * p.Sk * p.Hk) return;
+  const int64_t h = r % p.Hk, s = r / p.Hk % p.Sk, b = r / p.Hk / p.Sk;
+  const size_t rows = static_cast<size_t>(p.B) * p.Hk * p.nkt * kRows;
+  const float* src = a.part + (blockIdx.y * rows + (static_cast<size_t>(b) * p.Hk + h) * p.nkt * kRows + s) * kHeadDim + c * 4;
+  float4 x = *reinterpret_cast<const float4*>(src);
+  for (int i = 1; i < a.splits; ++i) {
+    const float4 y = *reinterpret_cast<const float4*>(src + 2 * i * rows * kHeadDim);
+    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  }
+  const Strides st = blockIdx.y ? a.so2 : a.so1;
+  *reinterpret_cast<uint2*>((blockIdx.y ? a.out2 : a.out1) + b * st.b + s * st.s + h * st.h + c * 4) =
+      make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
 // Zeros of [B, S, heads, 128] (no keys, or no queries).
 __global__ void __launch_bounds__(256) zero_kernel(uint16_t* x, Strides st, int S, int heads, int64_t n) {
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // 16-byte piece
@@ -721,12 +770,39 @@ void zero(const vsa_view* v, int32_t B, int32_t S, cudaStream_t stream) {
                                                                             view_strides(v, B, S), S, v->heads, n);
 }
 
+// Parts of a key tile's query tiles: where one block per key tile leaves SMs idle,
+// or, under a causal mask or with shared heads, where the longest block would
+// outlast the rest. Work in query tiles: the longest block against all work spread
+// over the SMs; the parts' 32-bit sums cost their traffic (3 us a query tile).
+int splits_of(const Problem& p) {
+  const double pairs = static_cast<double>(p.B) * p.Hk, sms = sm_count();
+  const int nqt = tiles(p.Sq);
+  double total = 0.0, longest = 0.0;
+  for (int kt = 0; kt < p.nkt; ++kt) {
+    const int first = p.causal ? std::min(nqt, std::max(0, kt * kRows - p.off) / kRows) : 0;
+    total += (nqt - first) * p.group;
+    longest = std::max(longest, static_cast<double>(nqt - first) * p.group);
+  }
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 8 && s <= std::max(1.0, longest / 2); ++s) {
+    const double part = std::ceil(longest / s) + 2.0;
+    double t = std::max(part, pairs * (total + 2.0 * p.nkt * s) / sms + (s == 1 && pairs * p.nkt < sms ? 0.0 : part / 3.0));
+    if (s > 1) t += 2.0 + pairs * p.nkt * kRows * s * 2048.0 / 6.5e12 / 3e-6;
+    if (t < least * 0.95) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
 struct Workspace {
-  size_t lse2, delta, range, range_q, count_q, list_q, count_k, list_k;
+  size_t part, lse2, delta, range, range_q, count_q, list_q, count_k, list_k;
   size_t bad_q, bad_o, bad_k, copy_q, copy_o, copy_k, total;
 };
 
-Workspace workspace_of(const Problem& p) {
+Workspace workspace_of(const Problem& p, int splits) {
   Workspace w{};
   size_t off = kHeader;
   auto take = [&](size_t bytes) {
@@ -735,6 +811,7 @@ Workspace workspace_of(const Problem& p) {
     return at;
   };
   const size_t b = static_cast<size_t>(p.B), nkt = static_cast<size_t>(p.nkt), nqt = static_cast<size_t>(tiles(p.Sq));
+  if (splits > 1) w.part = take(2 * static_cast<size_t>(splits) * b * p.Hk * nkt * kRows * kHeadDim * sizeof(float));
   w.lse2 = take(b * p.Hq * nqt * kRows * sizeof(float));
   w.delta = take(b * p.Hq * nqt * kRows * sizeof(float));
   if (p.documents) {
@@ -769,7 +846,11 @@ vsa_status launch(const Args& dkv, const Args& dq, const Maps& m, cudaStream_t s
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: shared memory", e);
   const Problem& p = dkv.p;
-  k1<<<p.nkt * p.Hk * p.B, kThreads, sizeof(Smem), stream>>>(dkv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+  k1<<<p.nkt * p.Hk * p.B * dkv.splits, kThreads, sizeof(Smem), stream>>>(dkv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+  if (dkv.splits > 1) {
+    const int64_t pieces = static_cast<int64_t>(p.B) * p.Sk * p.Hk * (kHeadDim / 4);
+    join_kernel<<<dim3(static_cast<unsigned>((pieces + 255) / 256), 2), 256, 0, stream>>>(dkv);
+  }
   k2<<<dq.nqt * p.Hq * p.B, kThreads, sizeof(Smem), stream>>>(dq, m.q, m.o, m.k, m.v, m.kc);
   e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_bwd", e);
@@ -794,7 +875,7 @@ vsa_status vsa_masked_attn_bwd_workspace_size(const vsa_mask* mask, int32_t B, i
   if (st != VSA_OK) return st;
   p.documents = mask->documents;
   p.masked |= mask->documents;
-  *bytes = workspace_of(p).total;
+  *bytes = workspace_of(p, splits_of(p)).total;
   return VSA_OK;
 }
 
@@ -815,7 +896,8 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
   if (st != VSA_OK) return st;
   if (reinterpret_cast<uintptr_t>(lse) % 4) return VSA_ERR_INVALID_ARG;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256) return VSA_ERR_INVALID_ARG;
-  const Workspace w = workspace_of(p);
+  const int splits = splits_of(p);
+  const Workspace w = workspace_of(p, splits);
   if (workspace_bytes < w.total) return VSA_ERR_WORKSPACE_TOO_SMALL;
   char* ws = static_cast<char*>(workspace);
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);   // this call's status word
@@ -902,6 +984,8 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
     kv.count = ck;
     kv.list = lk;
   }
+  kv.splits = splits;
+  kv.part = splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
   kv.clean_a = pa.clean_q;
   kv.clean_b = pa.clean_o;
   qq.clean_a = pa.clean_k;
