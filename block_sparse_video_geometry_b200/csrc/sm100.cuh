@@ -315,13 +315,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // 2^x of two floats on the FMA pipe: x = n + f with n the nearest whole number
 // (found by adding 1.5 * 2^23) and f in [-1/2, 1/2], 2^f by a polynomial of
 // degree 5 with relative error below 2^-22 (least squares with weights driven to
-// equal extrema, p(0) = 1), times 2^n. x is limited to -127 from below, where the
-// result is 0; NaN stays NaN. x < 127.
+// equal extrema, p(0) = 1), times 2^n. x is limited to
+// [-127, 127]: the result is 0 below and 2^127 above; NaN stays NaN.
 __device__ __forceinline__ void ex2_poly_f32x2(uint64_t x, float& a, float& b) {
   float x0, x1;
   unpack_f32x2(x, x0, x1);
-  asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(x0) : "f"(x0));
-  asm("max.NaN.f32 %0, %1, 0fC2FE0000;" : "=f"(x1) : "f"(x1));
+  asm("max.NaN.f32 %0, %1, 0fC2FE0000;\n\tmin.NaN.f32 %0, %0, 0f42FE0000;" : "=f"(x0) : "f"(x0));
+  asm("max.NaN.f32 %0, %1, 0fC2FE0000;\n\tmin.NaN.f32 %0, %0, 0f42FE0000;" : "=f"(x1) : "f"(x1));
   x = pack_f32x2(x0, x1);
   const uint64_t magic = pack_f32x2(12582912.0f, 12582912.0f), minus = pack_f32x2(-12582912.0f, -12582912.0f);
   const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);

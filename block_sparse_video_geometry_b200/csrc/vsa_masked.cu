@@ -604,8 +604,9 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         // first visible key) the exact maximum is formed, O (complete up to the
         // last half) and l are rescaled and P is formed again.
         float psum = INFINITY;
-        if (!__any_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
-        if (__any_sync(0xffffffffu, !(psum <= kSumLimit))) {
+        if (!__all_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
+        const bool raise = m == -INFINITY || !(psum <= kSumLimit);   // the others of the warp keep theirs
+        if (__any_sync(0xffffffffu, raise)) {
           float top = -INFINITY;
 #pragma unroll 1
           for (int q2 = 0; q2 < 2; ++q2) {
@@ -616,7 +617,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 #pragma unroll
             for (int u = 0; u < 32; ++u) top = fmaxf(top, x[u]);
           }
-          const bool grow = top > m;
+          const bool grow = raise && top > m;
           const float f = grow ? ex2_approx(m - top) : 1.0f;   // m = -inf: 0, and l and O are 0
           if (grow) m = top;
           l *= f;

@@ -241,3 +241,235 @@ def test_gradients_match_the_formula(cuda_ok, case):
     ref = reference(case, q, k, v, terms, dout)
     for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
         within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+def with_padding(case=(2, 300, 300, 4, 2, True, None, 0.0, False, (70, 1, 129, 60))):
+    """Documents with padding behind them, and the rows that hold padding."""
+    q, k, v, dout = tensors(*case[:5], seed=3)
+    terms = terms_of(case)
+    return case, [q, k, v, dout], terms, terms["doc_k"] < 0
+
+
+def test_infinities_and_nan_in_masked_places_change_nothing(cuda_ok):
+    """Padding rows of q, k, v and dout that hold infinities and NaN: the same bits as with zeros there, and zero
+    outputs and gradients in the padding rows themselves."""
+    import torch
+    case, clean, terms, pad = with_padding()
+    for t in clean:
+        t[pad] = 0
+    want = run(*clean[:3], causal=True, dout=clean[3], **terms)
+    dirty = [t.clone() for t in clean]
+    for n, t in enumerate(dirty):
+        rows = pad.nonzero()
+        for i, (b, s) in enumerate(rows.tolist()):
+            t[b, s, :, (i + n) % 128] = (float("inf"), float("-inf"), float("nan"))[i % 3]
+            t[b, s, :, (i * 7 + 3) % 128] = -3e38
+    got = run(*dirty[:3], causal=True, dout=dirty[3], **terms)
+    for name, a, b in zip(("out", "lse", "dq", "dk", "dv"), got, want):
+        assert torch.equal(a, b), name
+    for g in (got[0], got[2], got[3], got[4]):
+        assert not g[pad].float().any()
+    assert torch.equal(got[1].transpose(1, 2)[pad], torch.full_like(got[1].transpose(1, 2)[pad], -math.inf))
+
+
+@pytest.mark.parametrize("Sq", [1, 40, 333])
+def test_later_keys_of_a_causal_mask_may_hold_anything(cuda_ok, Sq):
+    """Keys behind the last query's position do not exist for the call; a key that only later queries see reaches
+    no earlier one, in the forward and the backward pass."""
+    import torch
+    B, Sk, H = 1, 500, 2
+    q, k, v, dout = tensors(B, Sq, Sk, H, H, seed=4)
+    want = run(q, k, v, causal=True, dout=dout)
+    j = Sk - Sq // 2 - 1                                     # its own query and later ones see it
+    k2, v2 = k.clone(), v.clone()
+    k2[:, j, :, 5] = float("nan")
+    v2[:, j, :, 9] = float("inf")
+    got = run(q, k2, v2, causal=True, dout=dout)
+    before = j - (Sk - Sq)                                   # queries that do not see it
+    assert torch.equal(got[0][:, :before], want[0][:, :before]) and torch.equal(got[1][..., :before], want[1][..., :before])
+    assert torch.equal(got[2][:, :before], want[2][:, :before])
+    assert torch.isnan(got[0][:, before:].float()).all()     # the documented answer of rows that see it
+
+
+def test_visible_infinity_in_one_row_of_many(cuda_ok):
+    import torch
+    q, k, v, _ = tensors(1, 200, 200, 2, 2, seed=5)
+    ids = documents(1, 200, (90, 110))
+    want = run(q, k, v, doc_q=ids, doc_k=ids)
+    v[0, 100, 1, 3] = float("inf")                            # document 1, head 1
+    out, lse = run(q, k, v, doc_q=ids, doc_k=ids)
+    assert torch.isnan(out[0, 90:, 1].float()).all()
+    assert torch.equal(out[0, :90], want[0][0, :90]) and torch.equal(out[0, :, 0], want[0][0, :, 0])
+
+
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+def test_large_scores(cuda_ok, cap):
+    """Scores of hundreds (one key takes nearly all of a row's weight) and, with a small cap, far into its bend."""
+    case = (1, 200, 600, 2, 1, True, None, cap, True, None)
+    q, k, v, dout = tensors(*case[:5], seed=6, size=8.0)
+    terms = terms_of(case)
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, cap=cap, dout=dout, **terms)
+    ref = reference(case, q, k, v, terms, dout)
+    within(lse, ref.lse, ref.t_lse, "lse")
+    for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+def test_growing_scores(cuda_ok):
+    """Every key tile raises the maximum of the row by far more than the reference's slack of 2^32: towards the
+    first keys, which the kernel takes last."""
+    import torch
+    q, k, v, dout = tensors(1, 130, 1000, 1, 1, seed=7)
+    q[..., 0] = 40.0
+    k[0, :, 0, 0] = torch.linspace(80, -80, 1000, device="cuda").bfloat16()
+    out, lse, dq, dk, dv = run(q, k, v, dout=dout)
+    ref = Reference(q, k, v, visible(1, 130, 1000), dout=dout)
+    within(lse, ref.lse, ref.t_lse, "lse")
+    for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+def test_strides_and_broadcast(cuda_ok):
+    """Slices of a fused projection, heads-first outputs, heads and batch entries of k and v broadcast."""
+    import torch
+    B, S, H = 2, 200, 3
+    g = torch.Generator(device="cuda").manual_seed(8)
+    qkv = torch.randn((B, S, 3, H, 128), generator=g, device="cuda").bfloat16()
+    dout = torch.randn((B, H, S, 128), generator=g, device="cuda").bfloat16().transpose(1, 2)
+    q, k, v = qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2]
+    prefix = torch.tensor([0, 77], dtype=torch.int32, device="cuda")
+    want = run(*(t.contiguous() for t in (q, k, v)), causal=True, dout=dout.contiguous(), prefix=prefix)
+    attn = vsa.MaskedAttention(vsa.make_mask(causal=True), B, S, S, H, H)
+    out = torch.empty((B, H, S, 128), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    lse = torch.empty((B, H, S), device="cuda")
+    attn.forward(q, k, v, out, lse, prefix=prefix)
+    grads = torch.zeros((B, S, 3, H, 128), dtype=torch.bfloat16, device="cuda")
+    attn.backward(q, k, v, out, lse, dout, grads[:, :, 0], grads[:, :, 1], grads[:, :, 2], prefix=prefix)
+    for a, b in zip((out, lse, grads[:, :, 0], grads[:, :, 1], grads[:, :, 2]), want):
+        assert torch.equal(a, b)
+    one_k, one_v = k[:1, :, :1].expand(B, S, H, 128), v[:1, :, :1].expand(B, S, H, 128)
+    got = run(q, one_k, one_v, causal=True, dout=dout, prefix=prefix)
+    full = run(q, one_k.contiguous(), one_v.contiguous(), causal=True, dout=dout, prefix=prefix)
+    assert all(torch.equal(a, b) for a, b in zip(got, full))
+
+
+def test_scale_and_documents_of_a_longer_cache(cuda_ok):
+    """A scale of its own, and queries that are the last of the cache's documents."""
+    import torch
+    B, Sq, Sk, H = 1, 70, 900, 2
+    q, k, v, dout = tensors(B, Sq, Sk, H, H, seed=9)
+    ids = documents(B, Sk, (300, 290, 310))
+    terms = dict(doc_q=ids[:, Sk - Sq:], doc_k=ids)
+    got = run(q, k, v, causal=True, scale=0.2, dout=dout, **terms)
+    ref = Reference(q, k, v, visible(B, Sq, Sk, True, None, **terms), scale=float(torch.tensor(0.2)), dout=dout)
+    for name, x in zip(("out", "lse", "dq", "dk", "dv"), got):
+        within(x, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+def test_unsorted_documents(cuda_ok):
+    """Documents whose tokens are interleaved (no tile holds one only), 70 of them."""
+    import torch
+    B, S, H = 1, 390, 2
+    q, k, v, dout = tensors(B, S, S, H, H, seed=10)
+    ids = ((torch.arange(S, device="cuda") * 37) % 71 - 1).to(torch.int32)[None].contiguous()
+    got = run(q, k, v, dout=dout, doc_q=ids, doc_k=ids)
+    ref = Reference(q, k, v, visible(B, S, S, False, None, ids, ids), dout=dout)
+    for name, x in zip(("out", "lse", "dq", "dk", "dv"), got):
+        within(x, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+@pytest.mark.parametrize("B,Sq,Sk", [(1, 0, 5), (1, 5, 0), (0, 5, 5), (2, 0, 0)])
+def test_nothing_to_attend(cuda_ok, B, Sq, Sk):
+    import torch
+    q, k, v, dout = tensors(B, Sq, Sk, 4, 2, seed=11)
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, dout=dout)
+    assert not out.float().any() and not dq.float().any() and not dk.float().any() and not dv.float().any()
+    assert torch.equal(lse, torch.full_like(lse, -math.inf))
+
+
+def test_differences_agree(cuda_ok):
+    """The gradients against central differences of sum(out * dout) in float64 on the formula, along a random
+    direction: with a step h the difference is off by h^2 / 6 |L'''| < 1e-6 of the sums here; the kernel's part is
+    bounded by the elementwise tolerances."""
+    import torch
+    case = (1, 90, 150, 2, 1, True, (20,), 5.0, True, None)
+    q, k, v, dout = tensors(*case[:5], seed=12)
+    terms = terms_of(case)
+    _, _, dq, dk, dv = run(q, k, v, causal=True, cap=5.0, dout=dout, **terms)
+    ref = reference(case, q, k, v, terms, dout)
+    loss = lambda q, k, v: (reference(case, q, k, v, terms).out * dout.double()).sum().item()  # noqa: E731
+    h = 1e-4
+    for i, (name, got) in enumerate((("dq", dq), ("dk", dk), ("dv", dv))):
+        at = [t.double() for t in (q, k, v)]
+        e = torch.randn(at[i].shape, device="cuda", dtype=torch.float64)
+        up, down = list(at), list(at)
+        up[i], down[i] = at[i] + h * e, at[i] - h * e
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        have = (got.double() * e).sum().item()
+        slack = (getattr(ref, "t_" + name) * e.abs()).sum().item() + 1e-6 * (got.double() * e).abs().sum().item()
+        assert abs(have - diff) <= slack, (name, have, diff, slack)
+
+
+def test_same_bits_again_and_two_streams(cuda_ok):
+    """Equal inputs give equal bits; two calls at once on streams and workspaces of their own do not meet."""
+    import torch
+    sets = [tensors(1, 700, 700, 4, 2, seed=s) for s in (13, 14)]
+    want = [run(*t[:3], causal=True, cap=20.0, dout=t[3]) for t in sets]
+    assert all(torch.equal(a, b) for a, b in zip(run(*sets[0][:3], causal=True, cap=20.0, dout=sets[0][3]), want[0]))
+    attns = [vsa.MaskedAttention(vsa.make_mask(causal=True, softcap=20.0), 1, 700, 700, 4, 2) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[torch.empty_like(x) for x in w] for w in want]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, s, t, o in zip(attns, streams, sets, outs):
+            a.forward(*t[:3], o[0], o[1], stream=s)
+            a.backward(*t[:3], o[0], o[1], t[3], o[2], o[3], o[4], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(a, b) for a, b in zip(w, o))
+
+
+def test_captured_calls_replay_on_new_inputs(cuda_ok):
+    """Forward and backward in one graph, with documents, split keys (few queries) and changed inputs and masks."""
+    import torch
+    for Sq, Sk in ((300, 300), (3, 2000)):
+        q, k, v, dout = tensors(1, Sq, Sk, 4, 2, seed=15)
+        ids = documents(1, Sk, (Sk // 3, Sk - Sk // 3))
+        attn = vsa.MaskedAttention(vsa.make_mask(), 1, Sq, Sk, 4, 2)
+        terms = dict(doc_q=ids[:, Sk - Sq:], doc_k=ids)
+        out, lse = attn.forward(q, k, v, **terms)                       # allocates the workspaces
+        grads = attn.backward(q, k, v, out, lse, dout, **terms)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            attn.forward(q, k, v, out, lse, stream=s, **terms)
+            attn.backward(q, k, v, out, lse, dout, *grads, stream=s, **terms)
+        for seed, lengths in ((16, (Sk // 2,)), (17, (Sk - 2, 2))):
+            for a, b in zip((q, k, v, dout), tensors(1, Sq, Sk, 4, 2, seed=seed)):
+                a.copy_(b)
+            ids.copy_(documents(1, Sk, lengths))
+            graph.replay()
+            torch.cuda.synchronize()
+            ref = Reference(q, k, v, visible(1, Sq, Sk, False, None, **terms), dout=dout)
+            within(lse, ref.lse, ref.t_lse, "lse")
+            for name, x in zip(("out", "dq", "dk", "dv"), (out, *grads)):
+                within(x, getattr(ref, name), getattr(ref, "t_" + name), name)
+        del graph
+
+
+def test_workspace_contents_do_not_matter(cuda_ok):
+    """Workspaces full of NaN patterns, or left by a call of another mask, give the same bits."""
+    import torch
+    q, k, v, dout = tensors(2, 150, 450, 4, 2, seed=18)
+    ids = documents(2, 450, (200, 249))
+    terms = dict(doc_q=ids[:, 300:], doc_k=ids)
+    want = run(q, k, v, dout=dout, **terms)
+    attn = vsa.MaskedAttention(vsa.make_mask(), 2, 150, 450, 4, 2)
+    for fill in (0xFF, 0x7F):
+        out, lse = attn.forward(q, k, v, **terms)
+        grads = attn.backward(q, k, v, out, lse, dout, **terms)
+        assert all(torch.equal(a, b) for a, b in zip((out, lse, *grads), want))
+        for held in (attn.ws_fwd, attn.ws_bwd):
+            for ws in held.values():
+                ws.fill_(fill)

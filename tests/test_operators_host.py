@@ -112,3 +112,80 @@ def test_binding_refuses_what_it_cannot_pass_on():
         vsa.layer_norm_fwd(x, torch.zeros(128), torch.zeros(128).half(), 1e-6, x.clone())
     with pytest.raises(ValueError, match=r"\[S, width\]"):
         vsa.layer_norm_fwd(x[0], None, None, 1e-6, x[0])
+
+
+def attn_call(name="fwd", mask=None, B=1, Sq=8, Sk=8, q=None, k=None, v=None, out=None, lse=FAKE, dout=None, dq=None,
+              dk=None, dv=None, ws=FAKE, nbytes=1 << 40, **terms):
+    t = vsa.MaskTerms(**terms)
+    mask = mask if mask is not None else vsa.make_mask()
+    q, k, v, out, dout, dq, dk, dv = (x or view() for x in (q, k, v, out, dout, dq, dk, dv))
+    L = vsa.lib()
+    if name == "fwd":
+        return L.vsa_masked_attn_fwd(ctypes.byref(mask), ctypes.byref(t), B, Sq, Sk, q, k, v, out, lse, ws, nbytes, None)
+    return L.vsa_masked_attn_bwd(ctypes.byref(mask), ctypes.byref(t), B, Sq, Sk, q, k, v, out, lse, dout, dq, dk, dv, ws,
+                                 nbytes, None)
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd"])
+def test_masked_attention_refuses_malformed_arguments(name):
+    bad, no = vsa.ERR_INVALID_ARG, vsa.ERR_UNSUPPORTED
+    call = lambda **kw: attn_call(name, **kw)  # noqa: E731
+    for m in (vsa.Mask(2, 0, 0.0, 0.0), vsa.Mask(0, 2, 0.0, 0.0), vsa.make_mask(scale=float("nan")),
+              vsa.make_mask(softcap=-1.0), vsa.make_mask(softcap=float("inf"))):
+        assert call(mask=m) == bad
+    assert call(B=-1) == bad and call(Sq=-1) == bad and call(Sk=-1) == bad
+    assert call(q=view(heads=3)) == bad and call(k=view(heads=0)) == bad       # 3 is no multiple of 2
+    assert call(v=view(heads=1)) == bad and call(out=view(heads=4)) == bad
+    for v in (view(dtype=vsa.DTYPE_F16), view(dtype=vsa.DTYPE_F32), view(data=None), view(data=FAKE + 8), view(ss=252),
+              view(ss=-256)):
+        assert call(q=v) == bad and call(k=v) == bad and call(v=v) == bad and call(out=v) == bad
+    assert call(lse=FAKE + 2) == bad and call(ws=None) == bad and call(ws=FAKE + 128) == bad
+    assert call(q=view(ss=0)) == no and call(v=view(ss=0)) == no
+    assert call(Sk=(1 << 24) + 1) == no and call(B=70000) == no
+    assert call(k=view(ss=1 << 40)) == no
+    # documents: both or neither, as the mask says; a prefix needs a causal mask
+    doc = vsa.make_mask(documents=True)
+    assert call(mask=doc) == bad and call(mask=doc, doc_q=FAKE) == bad and call(doc_q=FAKE, doc_k=FAKE) == bad
+    assert call(mask=doc, doc_q=FAKE, doc_k=FAKE + 2) == bad
+    assert call(prefix=FAKE) == bad and call(slopes=FAKE + 1) == bad
+    n = ctypes.c_size_t()
+    size = getattr(vsa.lib(), "vsa_masked_attn_%sworkspace_size" % ("bwd_" if name == "bwd" else ""))
+    causal = vsa.make_mask(causal=True)
+    assert size(ctypes.byref(causal), 1, 8, 8, 2, 2, ctypes.byref(n)) == vsa.OK and n.value > 256
+    assert call(mask=causal, nbytes=n.value - 1) == vsa.ERR_WORKSPACE_TOO_SMALL
+    assert size(None, 1, 8, 8, 2, 2, ctypes.byref(n)) == bad and size(ctypes.byref(causal), 1, 8, 8, 2, 2, None) == bad
+    assert size(ctypes.byref(causal), 1, 8, 8, 3, 2, ctypes.byref(n)) == bad
+    assert vsa.lib().vsa_masked_attn_status(None, None) == bad
+    if name == "bwd":
+        for x in (view(sb=0), view(ss=0), view(sh=64), view(heads=1)):
+            assert call(dk=x, B=2) == bad and call(dq=x, B=2) == bad and call(dv=x, B=2) == bad
+        assert call(dout=view(heads=1)) == bad
+    else:
+        assert call(out=view(ss=0)) == bad and call(out=view(sh=64)) == bad
+
+
+def test_masked_attention_binding_refusals():
+    import torch
+    mask = vsa.make_mask()
+    q = torch.zeros((1, 8, 4, 128)).bfloat16()
+    k = torch.zeros((1, 9, 2, 128)).bfloat16()
+    lse = torch.zeros((1, 4, 8))
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA device"):
+        vsa.masked_attn_fwd(mask, q, k, k, q.clone(), lse, ws)
+    with pytest.raises(ValueError, match="multiple"):
+        vsa.masked_attn_fwd(mask, q[:, :, :3], k, k, q, lse, ws)
+    with pytest.raises(ValueError, match="lse"):
+        vsa.masked_attn_fwd(mask, q, k, k, q.clone(), lse[:, :2], ws)
+    ids = torch.zeros((1, 9), dtype=torch.int32)
+    with pytest.raises(ValueError, match="come together"):
+        vsa.masked_attn_fwd(mask, q, k, k, q.clone(), lse, ws, doc_q=ids[:, :8], doc_k=ids)
+    with pytest.raises(ValueError, match="doc_q"):
+        vsa.masked_attn_fwd(vsa.make_mask(documents=True), q, k, k, q.clone(), lse, ws, doc_q=ids, doc_k=ids)
+    with pytest.raises(ValueError, match="slopes"):
+        vsa.masked_attn_fwd(mask, q, k, k, q.clone(), lse, ws, slopes=torch.zeros(3))
+    with pytest.raises(vsa.VSAError):
+        vsa.MaskedAttention(mask, 1, 8, 8, 3, 2)
+    attn = vsa.MaskedAttention(mask, 1, 8, 8, 4, 2)
+    with pytest.raises(ValueError, match="made for"):
+        attn.forward(q, k, k)
