@@ -633,7 +633,7 @@ int persistent(int64_t rows, const Shape& s, int threads) {
 
 template <class K, class A>
 vsa_status start(const char* where, K kernel, int blocks, int threads, size_t smem, const A& a, cudaStream_t stream) {
-  if (smem > (48u << 10)) {
+  if (smem > (40u << 10)) {                          // with a block's static shared memory above 48 KB
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail(where, e);

@@ -130,6 +130,8 @@ CASES = [
     ((700, 1153), "f32", "f32", "f32", "f32"),
     ((171, 5120), "bf16", "f32", "bf16", "bf16"),
     ((171, 5128), "bf16", "f32", "f32", "bf16"),             # the next kernel variant
+    ((600, 6144), "bf16", "f32", "bf16", "bf16"),            # just 48 KB of rows in flight
+    ((6, 3000), "bf16", "f32", "bf16", "bf16"),
     ((9, 8192), "f16", "f16", "f16", "f16"),
     ((9, 8193), "bf16", "bf16", "bf16", "bf16"),
     ((3, 8200), "bf16", "f32", "f32", "f32"),
