@@ -287,7 +287,7 @@ struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], drain[2];   // [slot][score buffer]
+  uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];   // [slot][score buffer]
   uint64_t first_done, second_out;   // one tile: slot 0 needs Q no longer; slot 1's result is in shared memory
   float m1[kRows], l1[kRows];        // its maximum and sum; its O lies over Q, [channel][row]
   uint32_t tmem_base;
@@ -366,6 +366,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         mbar_init(smem_u32(&sm.p_full[t][hb]), 4);
       }
       mbar_init(smem_u32(&sm.pv_done[t]), 1);
+      mbar_init(smem_u32(&sm.o_full[t]), 1);
       mbar_init(smem_u32(&sm.drain[t]), 1);
     }
     sm.abort = 0;
@@ -442,11 +443,19 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const uint32_t ts = tmem + kColS + 128 * t, to = tmem + kColO + 128 * t;
     const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
     bool ok = warp_wait(sm, sm.q_full, 0, a.err);
+    // Waits for every stage up to the e-th in loading order, the other slot's among
+    // them: a barrier's parity tells its phases apart only for one who saw the last.
+    int seen = 0;
+    auto landed = [&](int e) {
+      for (; seen <= e; ++seen)
+        if (!warp_wait(sm, sm.full[seen % kStages], (seen / kStages) & 1, a.err)) return false;
+      return true;
+    };
     // S(j, hb) = Q K^T over half hb of key tile j: 16 channels per K step, 32 B
     // inside a swizzled row of the d half kk / 4; 64 key rows = 8 KB.
     auto scores = [&](int j, int hb) {
       const int e = place_k(j), st = e % kStages;
-      if (hb == 0 && !warp_wait(sm, sm.full[st], (e / kStages) & 1, a.err)) return false;
+      if (hb == 0 && !landed(e)) return false;
       tc_fence_after();
       const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]) + 8192 * hb, 16, 1024);
       if (elect_one()) {
@@ -464,7 +473,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     if (ok && j0 < n) ok = scores(j0, 0) && scores(j0, 1);
     for (int j = j0, i = 0; ok && j < n; j += step, ++i) {
       const int e = place_v(j), st = e % kStages;
-      if (!(ok = warp_wait(sm, sm.full[st], (e / kStages) & 1, a.err))) break;
+      if (!(ok = landed(e))) break;
 #pragma unroll 1
       for (int hb = 0; hb < 2; ++hb) {
         if (!(ok = warp_wait(sm, sm.p_full[t][hb], i & 1, a.err))) break;
@@ -478,6 +487,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             umma_ts(to, ts + 64 * hb + kk * 8, vd + kk * (2048 >> 4), kIdescPV, i > 0 || hb > 0 || kk > 0 ? 1u : 0u);
           umma_commit(smem_u32(&sm.pv_done[t]));
           if (hb == 1) umma_commit(smem_u32(&sm.empty[st]));
+          if (hb == 1 && j + step >= n) umma_commit(smem_u32(&sm.o_full[t]));
         }
         __syncwarp();
         if (j + step < n && !(ok = scores(j + step, hb))) break;
@@ -649,9 +659,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       if (!ok) break;
     }
     // ---------------------------------------------------------- epilogue
-    // the last two of 2 i products (those before are complete with the last scores)
     if (ok && i > 0) {
-      ok = warp_wait(sm, sm.pv_done[t], 0, a.err) && warp_wait(sm, sm.pv_done[t], 1, a.err);
+      ok = warp_wait(sm, sm.o_full[t], 0, a.err);
       tc_fence_after();
     }
     float* o1 = reinterpret_cast<float*>(sm.q[0]);          // 64 KB over both Q tiles
