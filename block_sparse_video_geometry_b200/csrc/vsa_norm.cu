@@ -134,13 +134,6 @@ __device__ __forceinline__ float block_sum(float x, float* buf) {
   return lane_sum<32>(lane < warps ? buf[lane] : 0.0f);
 }
 
-// 1 / sqrt(x) to within 2 * 2^-24 relative: the approximate value and one Newton
-// step (x = 0 and infinity as they come).
-__device__ __forceinline__ float inv_sqrt(float x) {
-  const float r = rsqrtf(x);
-  return x > 0.0f && x < INFINITY ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
-}
-
 template <int N>
 __device__ __forceinline__ float sum_of(const float (&x)[N]) {
   uint64_t s2 = 0;
@@ -149,6 +142,10 @@ __device__ __forceinline__ float sum_of(const float (&x)[N]) {
   if constexpr (N % 2 == 0) unpack_f32x2(s2, s, t);
   return s + t;
 }
+
+// The single-element forms round every step (no fused operations): a row of one or
+// two elements has a gradient that cancels to nothing, and so it does here, as the
+// formula does step by step.
 
 // x = x - m in place; returns the sum of squares.
 template <int N>
@@ -163,8 +160,8 @@ __device__ __forceinline__ float centre(float (&x)[N], float m) {
         unpack_f32x2(d, x[i], x[i + 1]);
       },
       [&](int i) {
-        x[i] -= m;
-        s = fmaf(x[i], x[i], s);
+        x[i] = __fsub_rn(x[i], m);
+        s = __fadd_rn(s, __fmul_rn(x[i], x[i]));
       });
   if constexpr (N % 2 == 0) unpack_f32x2(s2, s, t);
   return s + t;
@@ -183,39 +180,49 @@ __device__ __forceinline__ void scale_shift(float (&x)[N], float r, const float 
 }
 
 // ------------------------------------------------------------------ forward
-// Short rows: LANES lanes of a warp per row, a vector of VEC elements each.
-// Persistent blocks keep the weights in registers and fetch the next U rows of a
-// lane group while they work on the current ones.
-template <class T, int VEC, int LANES, int U>
-__global__ void __launch_bounds__(kWarpBlock, kFwdBlocks) norm_fwd_warp_kernel(const __grid_constant__ FwdArgs a) {
+// Short rows: LANES lanes of a warp per row, E vectors of VEC elements each (vector
+// i of lane t is i * LANES + t). Persistent blocks keep the weights in registers and
+// fetch the next U rows of a lane group while they work on the current ones.
+template <class T, int VEC, int E, int LANES, int U>
+__global__ void __launch_bounds__(kWarpBlock, E == 1 ? kFwdBlocks : 2)
+norm_fwd_warp_kernel(const __grid_constant__ FwdArgs a) {
   constexpr int kGroups = kWarpBlock / LANES;
-  const int t = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const bool in = t < a.width / VEC;
-  float w[VEC], b[VEC];
-  weights<T, VEC>(a, t, a.width / VEC, w, b);
-  Pack<T, VEC> next[U];
+  const int t = threadIdx.x % LANES, group = threadIdx.x / LANES, nv = a.width / VEC;
+  float w[E][VEC], b[E][VEC];
+#pragma unroll
+  for (int i = 0; i < E; ++i) weights<T, VEC>(a, i * LANES + t, nv, w[i], b[i]);
+  Pack<T, VEC> next[U][E];
   auto fetch = [&](int64_t r0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t row = r0 + u * kGroups + group;
-      if (row < a.R.n && in) next[u].load(static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row)) + t * VEC);
+      if (row >= a.R.n) continue;
+      const T* x = static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row));
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i * LANES + t < nv) next[u][i].load(x + (i * LANES + t) * VEC);
     }
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups * U;
   int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups * U;
   fetch(r0);
   for (; r0 < a.R.n; r0 += step) {
-    Pack<T, VEC> k[U];
+    Pack<T, VEC> k[U][E];
 #pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = next[u];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < E; ++i) k[u][i] = next[u][i];
     fetch(r0 + step);                                // y may lie over x: other rows
-    float v[U][VEC], mean[U], rstd[U];
+    float v[U][E][VEC], mean[U], rstd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       mean[u] = 0.0f;
-      if (r0 + u * kGroups + group < a.R.n && in) {
-        k[u].get(v[u]);
-        mean[u] = sum_of(v[u]);
+      if (r0 + u * kGroups + group >= a.R.n) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (i * LANES + t >= nv) continue;
+        k[u][i].get(v[u][i]);
+        mean[u] += sum_of(v[u][i]);
       }
     }
 #pragma unroll
@@ -223,18 +230,24 @@ __global__ void __launch_bounds__(kWarpBlock, kFwdBlocks) norm_fwd_warp_kernel(c
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rstd[u] = 0.0f;
-      if (r0 + u * kGroups + group < a.R.n && in) rstd[u] = centre(v[u], mean[u]);
+      if (r0 + u * kGroups + group >= a.R.n) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i * LANES + t < nv) rstd[u] += centre(v[u][i], mean[u]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) rstd[u] = inv_sqrt(lane_sum<LANES>(rstd[u]) * a.inv_n + a.eps);
+    for (int u = 0; u < U; ++u) rstd[u] = rsqrtf(lane_sum<LANES>(rstd[u]) * a.inv_n + a.eps);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t row = r0 + u * kGroups + group;
       if (row >= a.R.n) continue;
-      if (in) {
-        scale_shift(v[u], rstd[u], w, b);
-        k[u].set(v[u]);
-        k[u].store(static_cast<T*>(a.y) + offset(a.sy, place(a.R, row)) + t * VEC);
+      T* y = static_cast<T*>(a.y) + offset(a.sy, place(a.R, row));
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (i * LANES + t >= nv) continue;
+        scale_shift(v[u][i], rstd[u], w[i], b[i]);
+        k[u][i].set(v[u][i]);
+        k[u][i].store(y + (i * LANES + t) * VEC);
       }
       if (t == 0 && a.mean) {
         a.mean[row] = mean[u];
@@ -265,10 +278,35 @@ __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// 2-byte rows that start anywhere (odd widths, shifted views) are staged in the
+// aligned 16-byte pieces that they cover, the elements before the first and behind
+// the last whole piece one by one, so that nothing outside the row is read. Element
+// c of a row at address p comes to lie (p % 16) / size + c elements into the stage.
+// (One element per copy instead: 1000 us for 7,825 bf16 rows of 9,009.)
+__host__ __device__ constexpr int loose_pitch(int width, int size) { return (width * size + 15) / 16 * 16 + 16; }
+template <class T>
+__device__ __forceinline__ int loose_shift(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
+}
+template <class T>
+__device__ __forceinline__ void stage_loose(uint8_t* stage, const T* p, int width) {
+  const int shift = loose_shift(p), pieces = (shift + width + 16 / static_cast<int>(sizeof(T)) - 1) * static_cast<int>(sizeof(T)) / 16;
+  const T* base = p - shift;
+  constexpr int kN = 16 / static_cast<int>(sizeof(T));
+  for (int k = threadIdx.x; k < pieces; k += blockDim.x) {
+    const int c0 = k * kN - shift;
+    if (c0 >= 0 && c0 + kN <= width) {
+      stage_in<16>(stage + 16 * k, base + k * kN);
+    } else {
+      for (int j = max(c0, 0); j < min(c0 + kN, width); ++j) reinterpret_cast<T*>(stage)[shift + j] = p[j];
+    }
+  }
+}
+
 // Long rows: one block per row, E vectors of VEC elements per thread (vector i of
 // thread t is i * threads + t). A persistent block keeps up to three rows ahead on
 // their way into shared memory; a thread reads back only what it copied itself,
-// so the ring needs no barrier. Rows of the ring: four where `bytes` a thread and
+// so the ring needs no barrier (loose rows need one). Rows of the ring: four where `bytes` a thread and
 // row times `threads` allow it.
 __host__ __device__ constexpr int ring_rows(int bytes, int threads) {
   const int n = (200 << 10) / (bytes * threads);
@@ -278,16 +316,22 @@ template <class T, int VEC, int E, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kRing = ring_rows(sizeof(T) * VEC * E, MAXT);
+  constexpr bool kLoose = VEC == 1 && sizeof(T) == 2;
   __shared__ float red[2][2][32];
   using P = Pack<T, VEC>;
   P* mine = reinterpret_cast<P*>(ring) + threadIdx.x;
   const int tpr = blockDim.x, t = threadIdx.x, nv = a.width / VEC;
+  const int pitch = loose_pitch(a.width, sizeof(T));
   auto fetch = [&](int64_t row, int st) {
     if (row < a.R.n) {
       const T* x = static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row));
+      if constexpr (kLoose) {
+        stage_loose(ring + st * pitch, x, a.width);
+      } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (i * tpr + t < nv) stage_in<sizeof(P)>(mine + (st * E + i) * tpr, x + static_cast<int64_t>(i * tpr + t) * VEC);
+        for (int i = 0; i < E; ++i)
+          if (i * tpr + t < nv) stage_in<sizeof(P)>(mine + (st * E + i) * tpr, x + static_cast<int64_t>(i * tpr + t) * VEC);
+      }
     }
     stage_commit();
   };
@@ -298,13 +342,23 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ 
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
   for (int64_t row = blockIdx.x; row < a.R.n; row += gridDim.x) {
-    if constexpr (kRing == 1) fetch(row, 0);
+    if constexpr (kRing == 1) {
+      if constexpr (kLoose) __syncthreads();               // the row before was read by all threads
+      fetch(row, 0);
+    }
     stage_wait<(kRing > 2 ? kRing - 2 : 0)>();
+    const T* loose = nullptr;
+    if constexpr (kLoose) {
+      __syncthreads();                                       // pieces of all threads
+      loose = reinterpret_cast<const T*>(ring + st * pitch) +
+              loose_shift(static_cast<const T*>(a.x) + offset(a.sx, place(a.R, row)));
+    }
     float v[E][VEC], sum = 0.0f, sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       if (i * tpr + t >= nv) continue;
-      mine[(st * E + i) * tpr].get(v[i]);
+      if constexpr (kLoose) v[i][0] = to_f32(loose[i * tpr + t]);
+      else mine[(st * E + i) * tpr].get(v[i]);
       sum += sum_of(v[i]);
     }
     if constexpr (kRing > 1) fetch(row + static_cast<int64_t>(kRing - 1) * gridDim.x, st == 0 ? kRing - 1 : st - 1);
@@ -314,7 +368,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const __grid_constant__ 
     for (int i = 0; i < E; ++i) {
       if (i * tpr + t < nv) sq += centre(v[i], mean);
     }
-    const float rstd = inv_sqrt(block_sum(sq, red[phase][1]) * a.inv_n + a.eps);
+    const float rstd = rsqrtf(block_sum(sq, red[phase][1]) * a.inv_n + a.eps);
     phase ^= 1;
     T* y = static_cast<T*>(a.y) + offset(a.sy, place(a.R, row));
 #pragma unroll
@@ -364,11 +418,11 @@ struct Columns {
           a2 = fma_f32x2(y, xh, a2);
         },
         [&](int i) {
-          const float xh = (x[i] - mean) * rstd, y = g[i] * w[i];
+          const float xh = __fmul_rn(__fsub_rn(x[i], mean), rstd), y = __fmul_rn(g[i], w[i]);
           dw[i] = fmaf(g[i], xh, dw[i]);
           db[i] += g[i];
-          b1 += y;
-          b2 = fmaf(y, xh, b2);
+          b1 = __fadd_rn(b1, y);
+          b2 = __fadd_rn(b2, __fmul_rn(y, xh));
         });
     if constexpr (VEC % 2 == 0) {
       unpack_f32x2(a1, b1, t1);
@@ -391,7 +445,10 @@ struct Columns {
           const uint64_t y = fma_f32x2(pack_f32x2(g[i], g[i + 1]), pack_f32x2(w[i], w[i + 1]), fma_f32x2(xh, n2, n1));
           unpack_f32x2(mul_f32x2(r2, y), g[i], g[i + 1]);
         },
-        [&](int i) { g[i] = rstd * fmaf(g[i], w[i], -fmaf((x[i] - mean) * rstd, c2, c1)); });
+        [&](int i) {
+          const float xh = __fmul_rn(__fsub_rn(x[i], mean), rstd);
+          g[i] = __fmul_rn(rstd, __fsub_rn(__fsub_rn(__fmul_rn(g[i], w[i]), c1), __fmul_rn(xh, c2)));
+        });
     if (a.dx_f32) {
       Pack<float, VEC> k;
       k.set(g);
@@ -485,23 +542,30 @@ template <class T, class G, int VEC, int E, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kRing = ring_rows((sizeof(T) + sizeof(G)) * VEC * E, MAXT);
+  constexpr bool kLoose = VEC == 1 && sizeof(T) == 2;
   __shared__ float red[2][2][32];
   using PX = Pack<T, VEC>;
   using PG = Pack<G, VEC>;
   const int tpr = blockDim.x, t = threadIdx.x, nv = a.width / VEC;
   PX* my_x = reinterpret_cast<PX*>(ring) + t;
   PG* my_g = reinterpret_cast<PG*>(ring + sizeof(PX) * kRing * E * tpr) + t;
+  const int pitch_x = loose_pitch(a.width, sizeof(T)), pitch = pitch_x + loose_pitch(a.width, sizeof(G));
   auto fetch = [&](int64_t row, int st) {
     if (row < a.R.n) {
       const Place p = place(a.R, row);
       const T* x = static_cast<const T*>(a.x) + offset(a.sx, p);
       const G* dy = static_cast<const G*>(a.dy) + offset(a.sdy, p);
+      if constexpr (kLoose) {
+        stage_loose(ring + st * pitch, x, a.width);
+        stage_loose(ring + st * pitch + pitch_x, dy, a.width);
+      } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int64_t c = i * tpr + t;
-        if (c >= nv) continue;
-        stage_in<sizeof(PX)>(my_x + (st * E + i) * tpr, x + c * VEC);
-        stage_in<sizeof(PG)>(my_g + (st * E + i) * tpr, dy + c * VEC);
+        for (int i = 0; i < E; ++i) {
+          const int64_t c = i * tpr + t;
+          if (c >= nv) continue;
+          stage_in<sizeof(PX)>(my_x + (st * E + i) * tpr, x + c * VEC);
+          stage_in<sizeof(PG)>(my_g + (st * E + i) * tpr, dy + c * VEC);
+        }
       }
     }
     stage_commit();
@@ -520,13 +584,43 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
   for (int64_t row = blockIdx.x; row < a.R.n; row += gridDim.x) {
     const int64_t next = row + gridDim.x;
     const float next_mean = next < a.R.n ? a.mean[next] : 0.0f, next_rstd = next < a.R.n ? a.rstd[next] : 0.0f;
-    if constexpr (kRing == 1) fetch(row, 0);
+    if constexpr (kRing == 1) {
+      if constexpr (kLoose) __syncthreads();               // the row before was read by all threads
+      fetch(row, 0);
+    }
     stage_wait<(kRing > 2 ? kRing - 2 : 0)>();
+    const T* lx = nullptr;
+    const G* lg = nullptr;
+    if constexpr (kLoose) {
+      __syncthreads();                                       // pieces of all threads
+      const Place p = place(a.R, row);
+      lx = reinterpret_cast<const T*>(ring + st * pitch) + loose_shift(static_cast<const T*>(a.x) + offset(a.sx, p));
+      lg = reinterpret_cast<const G*>(ring + st * pitch + pitch_x) +
+           loose_shift(static_cast<const G*>(a.dy) + offset(a.sdy, p));
+    }
+    auto vec_x = [&](int i) {
+      if constexpr (kLoose) {
+        PX k;
+        k.t[0] = lx[i * tpr + t];
+        return k;
+      } else {
+        return my_x[(st * E + i) * tpr];
+      }
+    };
+    auto vec_g = [&](int i) {
+      if constexpr (kLoose) {
+        PG k;
+        k.t[0] = lg[i * tpr + t];
+        return k;
+      } else {
+        return my_g[(st * E + i) * tpr];
+      }
+    };
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i)
       if (i * tpr + t < nv)
-        col[i].add(my_x[(st * E + i) * tpr], my_g[(st * E + i) * tpr], mean, rstd, s1, s2);
+        col[i].add(vec_x(i), vec_g(i), mean, rstd, s1, s2);
     // dx may lie over dy: a row is fetched and written by the same block, in that order
     if constexpr (kRing > 1) fetch(row + static_cast<int64_t>(kRing - 1) * gridDim.x, st == 0 ? kRing - 1 : st - 1);
     s1 = lane_sum<32>(s1);
@@ -549,7 +643,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const __grid_constant__ 
     for (int i = 0; i < E; ++i) {
       const int64_t c = i * tpr + t;
       if (c < nv)
-        col[i].write(a, my_x[(st * E + i) * tpr], my_g[(st * E + i) * tpr], mean, rstd, s1, s2,
+        col[i].write(a, vec_x(i), vec_g(i), mean, rstd, s1, s2,
                      od + c * VEC);
     }
     if (++st == kRing) st = 0;
@@ -608,9 +702,10 @@ constexpr int kFwdU = 2;   // rows in flight per lane group of the short-row for
 
 Shape shape_of(int width, int vec, int64_t rows, int u) {
   const int nv = width / vec;
-  if (nv <= 32) {
-    const int lanes = nv <= 16 ? 16 : 32;
-    return Shape{vec, lanes, vec, kWarpBlock, kWarpBlock / lanes * u};
+  if (nv <= 32 || (vec == 1 && width <= 512)) {
+    // vectors per lane: 1, or for single elements up to 16
+    const int lanes = nv <= 16 ? 16 : 32, e = nv <= 32 ? 1 : nv <= 128 ? 4 : 16;
+    return Shape{vec, lanes, e * vec, kWarpBlock, kWarpBlock / lanes * (e == 1 ? u : 1)};
   }
   const int ept = width > 8192 ? 32 : width >= 2048 && rows >= 512 ? 16 : 8, e = ept / vec;
   return Shape{vec, 64, ept, ((nv + e - 1) / e + 31) / 32 * 32, 1};
@@ -646,33 +741,43 @@ vsa_status start(const char* where, K kernel, int blocks, int threads, size_t sm
 template <class T, int VEC>
 vsa_status fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
   const char* where = "vsa_layer_norm_fwd";
-  const int n = persistent(a.R.n, s, s.lanes <= 32 ? kFwdBlocks * kWarpBlock : 960);
-  if (s.lanes == 16) return start(where, norm_fwd_warp_kernel<T, VEC, 16, kFwdU>, n, s.threads, 0, a, stream);
-  if (s.lanes == 32) return start(where, norm_fwd_warp_kernel<T, VEC, 32, kFwdU>, n, s.threads, 0, a, stream);
+  const bool wide = s.ept == VEC;                          // of the warp kernels: one vector per lane
+  const int n = persistent(a.R.n, s, s.lanes > 32 ? 960 : (wide ? kFwdBlocks : 2) * kWarpBlock);
+  if (s.lanes == 16) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 16, kFwdU>, n, s.threads, 0, a, stream);
+  if (s.lanes == 32 && wide) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 32, kFwdU>, n, s.threads, 0, a, stream);
+  if constexpr (VEC == 1) {
+    if (s.lanes == 32 && s.ept == 4) return start(where, norm_fwd_warp_kernel<T, 1, 4, 32, 1>, n, s.threads, 0, a, stream);
+    if (s.lanes == 32) return start(where, norm_fwd_warp_kernel<T, 1, 16, 32, 1>, n, s.threads, 0, a, stream);
+  }
   const int row = static_cast<int>(sizeof(T)) * s.ept;
-  auto smem = [&](int most) { return static_cast<size_t>(row) * s.threads * ring_rows(row, most); };
+  auto smem = [&](int most) { return (static_cast<size_t>(row) * s.threads + 32) * ring_rows(row, most); };
   if (s.ept == 8) return start(where, norm_fwd_kernel<T, VEC, 8 / VEC, 1024>, n, s.threads, smem(1024), a, stream);
   if (s.ept == 16) return start(where, norm_fwd_kernel<T, VEC, 16 / VEC, 512>, n, s.threads, smem(512), a, stream);
-  if (s.threads <= 256) return start(where, norm_fwd_kernel<T, VEC, 32 / VEC, 256>, n, s.threads, smem(256), a, stream);
   return start(where, norm_fwd_kernel<T, VEC, 32 / VEC, 512>, n, s.threads, smem(512), a, stream);
 }
 
 // Blocks of the backward kernel: a partial row each.
-int bwd_blocks(int64_t rows, const Shape& s) { return persistent(rows, s, s.lanes <= 32 ? 4 * kWarpBlock : 640); }
+int bwd_blocks(int64_t rows, const Shape& s) {
+  return persistent(rows, s, s.lanes > 32 ? 640 : (s.ept > 8 ? 2 : 4) * kWarpBlock);
+}
 
 template <class T, class G, int VEC>
 vsa_status bwd_launch(const Shape& s, const BwdArgs& a, int blocks, cudaStream_t stream) {
   const char* where = "vsa_layer_norm_bwd";
   if (s.lanes == 16) return start(where, norm_bwd_warp_kernel<T, G, VEC, 1, 16>, blocks, s.threads, 0, a, stream);
-  if (s.lanes == 32) return start(where, norm_bwd_warp_kernel<T, G, VEC, 1, 32>, blocks, s.threads, 0, a, stream);
+  if (s.lanes == 32 && s.ept == VEC)
+    return start(where, norm_bwd_warp_kernel<T, G, VEC, 1, 32>, blocks, s.threads, 0, a, stream);
+  if constexpr (VEC == 1) {
+    if (s.lanes == 32 && s.ept == 4)
+      return start(where, norm_bwd_warp_kernel<T, G, 1, 4, 32>, blocks, s.threads, 0, a, stream);
+    if (s.lanes == 32) return start(where, norm_bwd_warp_kernel<T, G, 1, 16, 32>, blocks, s.threads, 0, a, stream);
+  }
   const int row = static_cast<int>(sizeof(T) + sizeof(G)) * s.ept;
-  auto smem = [&](int most) { return static_cast<size_t>(row) * s.threads * ring_rows(row, most); };
+  auto smem = [&](int most) { return (static_cast<size_t>(row) * s.threads + 64) * ring_rows(row, most); };
   if (s.ept == 8)
     return start(where, norm_bwd_kernel<T, G, VEC, 8 / VEC, 1024>, blocks, s.threads, smem(1024), a, stream);
   if (s.ept == 16)
     return start(where, norm_bwd_kernel<T, G, VEC, 16 / VEC, 512>, blocks, s.threads, smem(512), a, stream);
-  if (s.threads <= 256)
-    return start(where, norm_bwd_kernel<T, G, VEC, 32 / VEC, 256>, blocks, s.threads, smem(256), a, stream);
   return start(where, norm_bwd_kernel<T, G, VEC, 32 / VEC, 512>, blocks, s.threads, smem(512), a, stream);
 }
 
