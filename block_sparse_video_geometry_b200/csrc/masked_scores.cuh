@@ -45,8 +45,8 @@ struct ScoreTerms {
 // extrema, relative error below 2^-23; five operations a score.
 // Bias: where the columns lie on one side of every row of the warp it is linear in
 // the column, one operation a score.
-// A call of 2 x 1,111 queries over 5,003 keys, 24 heads, cap and bias: a half tile's
-// softmax 2950 cycles with both general forms in the exponential unit, NEWCYC so.
+// 2 x 1,111 queries over 5,003 keys, 24 heads, cap and bias, forward: 393 us with both
+// general forms in the exponential unit, 350 us so (274-294 us with 128-row blocks).
 template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
                                            Ref ref) {
