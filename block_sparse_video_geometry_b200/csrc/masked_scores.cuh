@@ -34,53 +34,90 @@ struct ScoreTerms {
   }
 };
 
-// Raw scores x (sums of products) -> their log2 values minus a reference (`ref`
-// gives minus the reference for a pair of columns). With a cap t receives
-// tanh(score / cap). Distance of column u: |d0 + dir u|, dir = 1 or -1.
-//
 // tanh: 1 - 2 / (1 + e^(2y)) takes two operations of the exponential unit per
-// score, which then bounds the kernels. Where all of a warp's 32 x 32 scores have
-// |y| <= 0.6 (a cap well above the scores, as caps are), tanh(y) / y is a polynomial
-// in y^2 on the FMA pipe: degree 4, least squares with weights driven to equal
-// extrema, relative error below 2^-23; five operations a score.
+// score, which then bounds the kernels. Where all of a warp's scores have |y| <= 0.6
+// (a cap well above the scores, as caps are), tanh(y) / y is a polynomial in y^2 on
+// the FMA pipe: degree 4, least squares with weights driven to equal extrema, relative
+// error below 2^-23; five operations a score.
 // Bias: where the columns lie on one side of every row of the warp it is linear in
-// the column, one operation a score.
+// the column, one operation a score. Distance of column u: |d0 + dir u|, dir = 1 or -1.
 // 2 x 1,111 queries over 5,003 keys, 24 heads, cap and bias, forward: 393 us with both
-// general forms in the exponential unit, 350 us so (274-294 us with 128-row blocks).
-template <bool kCap, bool kBias, class Ref>
-__device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
-                                           Ref ref) {
-  bool poly = true;
+// general forms in the exponential unit, 350 us so (300 us with 128-row blocks, 249 us with
+// each pair's polynomial next to its exponentials, which keeps both pipes at work).
+
+// Largest |raw score| of 32 columns (a cap's polynomial holds up to ScoreTerms::limit).
+template <bool kCap>
+__device__ __forceinline__ float largest(const float (&x)[32], float top = 0.0f) {
   if constexpr (kCap) {
-    float top = 0.0f;
 #pragma unroll
     for (int u = 0; u < 32; u += 2) top = fmaxf(fmaxf(top, fabsf(x[u])), fabsf(x[u + 1]));
-    poly = __all_sync(0xffffffffu, top <= s.limit);
   }
-  float k = 0.0f;               // bias of column u: k (d0 + dir u)
-  bool linear = true;
-  if constexpr (kBias) {
-    const float d31 = fmaf(dir, 31.0f, d0);
-    const bool right = __all_sync(0xffffffffu, d0 >= 0.0f && d31 >= 0.0f);
-    linear = right || __all_sync(0xffffffffu, d0 <= 0.0f && d31 <= 0.0f);
-    k = right ? -s.slope : s.slope;
+  return top;
+}
+
+// Side of `n` columns from d0: bias of column u = k (d0 + dir u); false where the
+// warp's rows lie on both sides.
+template <bool kBias>
+__device__ __forceinline__ bool one_side(const ScoreTerms& s, float d0, float dir, float n, float& k) {
+  k = 0.0f;
+  if constexpr (!kBias) return true;
+  const float d1 = fmaf(dir, n - 1.0f, d0);
+  const bool right = __all_sync(0xffffffffu, d0 >= 0.0f && d1 >= 0.0f);
+  k = right ? -s.slope : s.slope;
+  return right || __all_sync(0xffffffffu, d0 <= 0.0f && d1 <= 0.0f);
+}
+
+// Log2 scores minus a reference, two columns at a time, by the polynomial and the
+// linear bias.
+template <bool kCap, bool kBias>
+struct PairArgs {
+  uint64_t c2, base, step, p0, p1, p2, p3;
+  // `ref`: minus the reference where it is the same for all columns, else 0
+  __device__ __forceinline__ PairArgs(const ScoreTerms& s, float k, float d0, float dir, float ref) {
+    c2 = pack_f32x2(s.c, s.c);
+    const float at = kBias ? fmaf(k, d0, ref) : ref;
+    base = pack_f32x2(at, at);
+    step = pack_f32x2(k * dir, k * dir);
+    p0 = pack_f32x2(s.poly[0], s.poly[0]), p1 = pack_f32x2(s.poly[1], s.poly[1]);
+    p2 = pack_f32x2(s.poly[2], s.poly[2]), p3 = pack_f32x2(s.poly[3], s.poly[3]);
   }
-  if (poly && linear) {
-    const uint64_t c2 = pack_f32x2(s.c, s.c), base = pack_f32x2(k * d0, k * d0), step = pack_f32x2(k * dir, k * dir);
-    const uint64_t p0 = pack_f32x2(s.poly[0], s.poly[0]), p1 = pack_f32x2(s.poly[1], s.poly[1]);
-    const uint64_t p2 = pack_f32x2(s.poly[2], s.poly[2]), p3 = pack_f32x2(s.poly[3], s.poly[3]);
+  // columns u and u + 1; q receives log2(e) scale tanh(y) / y
+  __device__ __forceinline__ uint64_t operator()(uint64_t v, int u, uint64_t& q) const {
+    q = c2;
+    if constexpr (kCap) {
+      const uint64_t z = mul_f32x2(v, v);
+      q = fma_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(p3, z, p2), z, p1), z, p0), z, c2);
+    }
+    uint64_t add = base;
+    if constexpr (kBias) add = fma_f32x2(step, pack_f32x2(static_cast<float>(u), static_cast<float>(u + 1)), base);
+    return fma_f32x2(v, q, add);
+  }
+};
+
+// Raw scores x (sums of products) -> their log2 values minus a reference (`ref`
+// gives minus the reference for a pair of columns). With a cap t receives
+// tanh(score / cap). kBoth: the polynomial where the columns lie on both sides of the
+// rows too (one more form in the code: faster in the forward pass, whose blocks start
+// with such tiles, slower in the backward's kernels, 544 -> 636 us for 4096 x 24 heads,
+// which have few registers).
+template <bool kCap, bool kBias, bool kBoth, class Ref>
+__device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
+                                           Ref ref) {
+  const bool poly = !kCap || __all_sync(0xffffffffu, largest<kCap>(x) <= s.limit);
+  float k;                      // bias of column u: k (d0 + dir u)
+  const bool linear = one_side<kBias>(s, d0, dir, 32.0f, k);
+  if (poly && (kBoth || linear)) {
+    const PairArgs<kCap, kBias> pair(s, linear ? k : 0.0f, d0, dir, 0.0f);
 #pragma unroll
     for (int u = 0; u < 32; u += 2) {
       const uint64_t v = pack_f32x2(x[u], x[u + 1]);
-      uint64_t q = c2, add = ref(u);
-      if constexpr (kCap) {
-        const uint64_t z = mul_f32x2(v, v);
-        q = fma_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(p3, z, p2), z, p1), z, p0), z, c2);
-      }
-      if constexpr (kBias)
-        add = add_f32x2(add, fma_f32x2(step, pack_f32x2(static_cast<float>(u), static_cast<float>(u + 1)), base));
-      unpack_f32x2(fma_f32x2(v, q, add), x[u], x[u + 1]);
+      uint64_t q;
+      unpack_f32x2(add_f32x2(pair(v, u, q), ref(u)), x[u], x[u + 1]);
       if constexpr (kCap) unpack_f32x2(mul_f32x2(v, q), t[u], t[u + 1]);   // times 1 / cap2 below
+    }
+    if (kBoth && kBias && !linear) {
+#pragma unroll
+      for (int u = 0; u < 32; ++u) x[u] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), x[u]);
     }
     if constexpr (kCap) {
       const float inv = 1.0f / s.cap2;

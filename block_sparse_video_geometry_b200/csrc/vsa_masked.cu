@@ -504,24 +504,6 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ts = lane_addr + kColS + 128 * t, to = lane_addr + kColO + 128 * t;
     const int tile_row0 = one ? qb * kRows : (2 * qb + t) * kRows;
-    // rows of Q into shared memory, 16 lanes per row (rows past the end: zero)
-    if (!one || t == 0) {
-      for (int it = 0; it < 16; ++it) {
-        const int e = it * 128 + r, rr = e >> 4, c = e & 15;
-        const int row = tile_row0 + rr;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (row < a.rows) {
-          const int g = a.packed ? row / p.Sq : 0, i = a.packed ? row - g * p.Sq : row;
-          const int h = a.packed ? hk * p.group + g : unit;
-          w = *reinterpret_cast<const uint4*>(a.q + b * a.sq.b + i * a.sq.s + h * a.sq.h + c * 8);
-        }
-        *reinterpret_cast<uint4*>(sm.q[t] + (c >> 3) * 16384 + rr * 128 + ((c & 7) ^ (rr & 7)) * 16) = w;
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
-
     const int row = tile_row0 + r;
     const bool live = row < a.rows;
     const int g = a.packed ? row / p.Sq : 0;
@@ -533,6 +515,32 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
     const ScoreTerms terms(p.scale, p.cap, kBias ? p.slopes[h] : 0.0f);
+    // rows of Q into shared memory, 16 lanes per row (rows past the end: zero), all
+    // loads in flight at once; one tile: both slots' threads (one by one a block's
+    // first product waited 6-10 us)
+    const int rows0 = one ? tile_row0 + 64 * t : tile_row0;   // this slot's share
+    const int n_it = one ? 8 : 16;
+    uint4 w[16];
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int e = it * 128 + r, c = e & 15, at = rows0 + (e >> 4);
+      w[it] = make_uint4(0, 0, 0, 0);
+      if (it < n_it && at < a.rows) {
+        const int gg = a.packed ? at / p.Sq : 0, i = a.packed ? at - gg * p.Sq : at;
+        const int hh = a.packed ? hk * p.group + gg : unit;
+        w[it] = *reinterpret_cast<const uint4*>(a.q + b * a.sq.b + i * a.sq.s + hh * a.sq.h + c * 8);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int e = it * 128 + r, c = e & 15, rr = (one ? 64 * t : 0) + (e >> 4);
+      if (it < n_it)
+        *reinterpret_cast<uint4*>(sm.q[one ? 0 : t] + (c >> 3) * 16384 + rr * 128 + ((c & 7) ^ (rr & 7)) * 16) = w[it];
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     const int step = one ? 2 : 1;
@@ -556,7 +564,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         auto finish = [&](int q4, float (&x)[32], float minus_ref) {
           const int col = 32 * q4;
           float tanhs[32];
-          score_args<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
+          score_args<kCap, kBias, true>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
                                   [&](int) { return pack_f32x2(minus_ref, minus_ref); });
           if (partial) {
             const int lc = lim_t - k0 - col;
@@ -579,8 +587,15 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
               if (((bits >> u) & 1u) && x[u] != -INFINITY) x[u] = NAN;
           }
         };
-        // P (bf16 pairs) against the reference m, and its 32-bit sum
+        // P (bf16 pairs) against the reference m, and its 32-bit sum. Where no column
+        // needs more than the pairwise form, each pair's arguments stand next to its
+        // exponentials, so that the FMA pipe and the exponential unit run together.
+        // A quarter of the exponentials go to the FMA pipe: 868 -> 834 us for 8192 x
+        // 24 heads (an eighth 848, three eighths 862); none where the cap fills it.
         uint32_t w[2][16];
+        const float d0 = static_cast<float>(i_q + p.off - k0 - 64 * hb);
+        float k_bias;
+        const bool plain = one_side<kBias>(terms, d0, -1.0f, 64.0f, k_bias) && !partial && !flagged;
         auto exponentials = [&]() {
           const float ms = m == -INFINITY ? 0.0f : m;
           uint64_t ls[2] = {0, 0};
@@ -588,19 +603,38 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           tmem_ld32x32f(tb, x[0]);
           tmem_wait_ld32(x[0]);
           tmem_ld32x32f(tb + 32, x[1]);
+          auto take = [&](int q2, int u) {
+            float p0 = x[q2][2 * u], p1 = x[q2][2 * u + 1];
+            ex2_pair(p0, p1, !kCap && u % 4 == 2);
+            ls[u & 1] = add_f32x2(ls[u & 1], pack_f32x2(p0, p1));
+            w[q2][u] = pack_bf16x2(p0, p1);
+          };
+          bool pairwise = plain;
+          if constexpr (kCap) {
+            const float top = largest<kCap>(x[0]);
+            tmem_wait_ld32(x[1]);
+            pairwise = __all_sync(0xffffffffu, largest<kCap>(x[1], top) <= terms.limit) && plain;
+          }
+          if ((kCap || kBias) && pairwise) {
+            const PairArgs<kCap, kBias> pair(terms, k_bias, d0, -1.0f, -ms);
 #pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) {
-            float(&y)[32] = x[q2];
-            if (q2) tmem_wait_ld32(y);
-            finish(2 * hb + q2, y, -ms);
+            for (int q2 = 0; q2 < 2; ++q2) {
+              if (q2 && !kCap) tmem_wait_ld32(x[1]);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              // a quarter of the exponentials on the FMA pipe: 868 -> 834 us for 8192 x 24
-              // heads (an eighth 848, three eighths 862); none where the cap fills it
-              float p0 = y[2 * u], p1 = y[2 * u + 1];
-              ex2_pair(p0, p1, !kCap && u % 4 == 2);
-              ls[u & 1] = add_f32x2(ls[u & 1], pack_f32x2(p0, p1));
-              w[q2][u] = pack_bf16x2(p0, p1);
+              for (int u = 0; u < 16; ++u) {
+                uint64_t q;
+                unpack_f32x2(pair(pack_f32x2(x[q2][2 * u], x[q2][2 * u + 1]), 32 * q2 + 2 * u, q), x[q2][2 * u],
+                             x[q2][2 * u + 1]);
+                take(q2, u);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q2 = 0; q2 < 2; ++q2) {
+              if (q2 && !kCap) tmem_wait_ld32(x[1]);
+              finish(2 * hb + q2, x[q2], -ms);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) take(q2, u);
             }
           }
           float s0, s1;
@@ -613,10 +647,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         // neither a maximum nor a rescale of O is needed. Otherwise (and on the
         // first visible key) the exact maximum is formed, O (complete up to the
         // last half) and l are rescaled and P is formed again.
-        float psum = INFINITY;
-        if (!__all_sync(0xffffffffu, m == -INFINITY)) psum = exponentials();
-        const bool raise = m == -INFINITY || !(psum <= kSumLimit);   // the others of the warp keep theirs
-        if (__any_sync(0xffffffffu, raise)) {
+        auto rise = [&](bool raise) {
           float top = -INFINITY;
 #pragma unroll 1
           for (int q2 = 0; q2 < 2; ++q2) {
@@ -633,7 +664,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           l *= f;
           const int halves = 2 * i + hb;                       // P V products so far
           if (halves > 0) {
-            if (!(ok = warp_wait(sm, sm.pv_done[t], (halves - 1) & 1, a.err))) break;
+            if (!(ok = warp_wait(sm, sm.pv_done[t], (halves - 1) & 1, a.err))) return;
             tc_fence_after();
 #pragma unroll 1
             for (int q4 = 0; q4 < 4; ++q4) {
@@ -646,8 +677,32 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
               tmem_st32x32(to + 32 * q4, ow);
             }
           }
-          psum = exponentials();
+        };
+        float psum = INFINITY;
+        const bool first = __all_sync(0xffffffffu, m == -INFINITY);
+        if constexpr (kCap) {
+          // one copy of the long capped exponentials in a loop (two copies: attn of
+          // 1,555 causal tokens 73 us, so 67; without a cap two copies are faster)
+          bool raised = first, raise = true;
+#pragma unroll 1
+          for (;;) {
+            if (raised) rise(raise);
+            if (!ok) break;
+            psum = exponentials();
+            if (raised) break;
+            raise = m == -INFINITY || !(psum <= kSumLimit);
+            raised = __any_sync(0xffffffffu, raise);
+            if (!raised) break;
+          }
+        } else {
+          if (!first) psum = exponentials();
+          const bool raise = m == -INFINITY || !(psum <= kSumLimit);   // the others of the warp keep theirs
+          if (__any_sync(0xffffffffu, raise)) {
+            rise(raise);
+            if (ok) psum = exponentials();
+          }
         }
+        if (!ok) break;
 #pragma unroll
         for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, w[q2]);
         l += psum;

@@ -275,7 +275,7 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const ScoreTerms& s, float d0, float dir,
                                               Ref ref) {
-  score_args<kCap, kBias>(x, w, s, d0, dir, ref);          // w: tanh
+  score_args<kCap, kBias, false>(x, w, s, d0, dir, ref);          // w: tanh
   const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
