@@ -352,7 +352,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int unit = id % a.units, b = id / a.units;
   const int hk = a.packed ? unit : unit / p.group;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * kWarpLoad) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 1);
       mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one slot, or by both
@@ -375,6 +375,32 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
     tmem_relinquish();
+  }
+  if (warp < 8) {
+    // rows of Q into shared memory, 16 lanes per row (rows past the end: zero), all
+    // loads in flight at once; one tile: both slots' threads (one by one, behind the
+    // block's first barrier, its first product waited 6-10 us)
+    const int t = warp >> 2, r = threadIdx.x & 127;
+    const int rows0 = one ? qb * kRows + 64 * t : (2 * qb + t) * kRows;   // this slot's share
+    const int n_it = one ? 8 : 16;
+    uint4 w[16];
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int e = it * 128 + r, c = e & 15, at = rows0 + (e >> 4);
+      w[it] = make_uint4(0, 0, 0, 0);
+      if (it < n_it && at < a.rows) {
+        const int gg = a.packed ? at / p.Sq : 0, i = a.packed ? at - gg * p.Sq : at;
+        const int hh = a.packed ? hk * p.group + gg : unit;
+        w[it] = *reinterpret_cast<const uint4*>(a.q + b * a.sq.b + i * a.sq.s + hh * a.sq.h + c * 8);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 16; ++it) {
+      const int e = it * 128 + r, c = e & 15, rr = (one ? 64 * t : 0) + (e >> 4);
+      if (it < n_it)
+        *reinterpret_cast<uint4*>(sm.q[one ? 0 : t] + (c >> 3) * 16384 + rr * 128 + ((c & 7) ^ (rr & 7)) * 16) = w[it];
+    }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -515,30 +541,6 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
     const int32_t* dk = p.documents ? p.doc_k + b * p.doc_k_sb : nullptr;
     const ScoreTerms terms(p.scale, p.cap, kBias ? p.slopes[h] : 0.0f);
-    // rows of Q into shared memory, 16 lanes per row (rows past the end: zero), all
-    // loads in flight at once; one tile: both slots' threads (one by one a block's
-    // first product waited 6-10 us)
-    const int rows0 = one ? tile_row0 + 64 * t : tile_row0;   // this slot's share
-    const int n_it = one ? 8 : 16;
-    uint4 w[16];
-#pragma unroll
-    for (int it = 0; it < 16; ++it) {
-      const int e = it * 128 + r, c = e & 15, at = rows0 + (e >> 4);
-      w[it] = make_uint4(0, 0, 0, 0);
-      if (it < n_it && at < a.rows) {
-        const int gg = a.packed ? at / p.Sq : 0, i = a.packed ? at - gg * p.Sq : at;
-        const int hh = a.packed ? hk * p.group + gg : unit;
-        w[it] = *reinterpret_cast<const uint4*>(a.q + b * a.sq.b + i * a.sq.s + hh * a.sq.h + c * 8);
-      }
-    }
-#pragma unroll
-    for (int it = 0; it < 16; ++it) {
-      const int e = it * 128 + r, c = e & 15, rr = (one ? 64 * t : 0) + (e >> 4);
-      if (it < n_it)
-        *reinterpret_cast<uint4*>(sm.q[one ? 0 : t] + (c >> 3) * 16384 + rr * 128 + ((c & 7) ^ (rr & 7)) * 16) = w[it];
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
 
     float m = -INFINITY, l = 0.0f;
@@ -678,33 +680,83 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             }
           }
         };
+        // No row of the warp has a reference yet: the scores are finished once, back into
+        // their columns, and their exact maximum is the reference. (O and l are zero, or
+        // NaN, so nothing is rescaled.) Without cap and bias, whose scores are quickly
+        // finished twice, the form costs more in the main loop than it saves (dense 8192
+        // x 24 heads 833 -> 858 us).
+        auto begin = [&]() {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int q2 = 0; q2 < 2; ++q2) {
+            float x[32];
+            uint32_t y[32];
+            tmem_ld32x32f(tb + 32 * q2, x);
+            tmem_wait_ld32(x);
+            finish(2 * hb + q2, x, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              top = fmaxf(top, x[u]);
+              y[u] = __float_as_uint(x[u]);
+            }
+            tmem_st32x32(tb + 32 * q2, y);
+          }
+          tmem_wait_st();
+          m = fmaxf(m, top);
+          const float ms = m == -INFINITY ? 0.0f : m;
+          uint64_t sum = 0;
+          const uint64_t minus = pack_f32x2(-ms, -ms);
+#pragma unroll 1
+          for (int q2 = 0; q2 < 2; ++q2) {                     // P of 32 columns ends up over scores already read
+            float x[32];
+            uint32_t y[16];
+            tmem_ld32x32f(tb + 32 * q2, x);
+            tmem_wait_ld32(x);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              float p0, p1;
+              unpack_f32x2(add_f32x2(pack_f32x2(x[2 * u], x[2 * u + 1]), minus), p0, p1);
+              ex2_pair(p0, p1, false);
+              sum = add_f32x2(sum, pack_f32x2(p0, p1));
+              y[u] = pack_bf16x2(p0, p1);
+            }
+            tmem_st32x16(tb + 16 * q2, y);
+          }
+          float s0, s1;
+          unpack_f32x2(sum, s0, s1);
+          return s0 + s1;
+        };
         float psum = INFINITY;
-        const bool first = __all_sync(0xffffffffu, m == -INFINITY);
-        if constexpr (kCap) {
-          // one copy of the long capped exponentials in a loop (two copies: attn of
-          // 1,555 causal tokens 73 us, so 67; without a cap two copies are faster)
-          bool raised = first, raise = true;
+        const bool first = __all_sync(0xffffffffu, m == -INFINITY), begun = (kCap || kBias) && first;
+        if (begun) {
+          psum = begin();
+        } else if constexpr (kCap) {
+          // one copy of the long capped exponentials in a loop (1,555 causal tokens 73 us
+          // with two, 67 so; without a cap two copies are faster)
+          bool raised = false, raise = false;
 #pragma unroll 1
           for (;;) {
             if (raised) rise(raise);
             if (!ok) break;
             psum = exponentials();
             if (raised) break;
-            raise = m == -INFINITY || !(psum <= kSumLimit);
+            raise = m == -INFINITY || !(psum <= kSumLimit);    // the others of the warp keep theirs
             raised = __any_sync(0xffffffffu, raise);
             if (!raised) break;
           }
         } else {
-          if (!first) psum = exponentials();
-          const bool raise = m == -INFINITY || !(psum <= kSumLimit);   // the others of the warp keep theirs
+          if (kBias || !first) psum = exponentials();
+          const bool raise = m == -INFINITY || !(psum <= kSumLimit);
           if (__any_sync(0xffffffffu, raise)) {
             rise(raise);
             if (ok) psum = exponentials();
           }
         }
         if (!ok) break;
+        if (!begun) {
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, w[q2]);
+          for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, w[q2]);
+        }
         l += psum;
         tmem_wait_st();
         tc_fence_before();

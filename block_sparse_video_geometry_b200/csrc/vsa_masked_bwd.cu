@@ -6,12 +6,12 @@
 // dK = scale dS^T Q, dQ = scale dS K.
 //
 // Bound: tensor pipe. The formulas need five products per visible pair; the two
-// kernels here run seven (S and dO V^T once per side), so that every sum stays
+// kinds of blocks here run seven (S and dO V^T once per side), so that every sum stays
 // in one block's TMEM in a fixed order: no atomics, equal inputs give equal bits,
 // and dQ needs no 32-bit traffic through memory.
 //
 // Design.
-//  * dkv_kernel: a block owns 128 keys of a key head (TMEM lane = key) and walks
+//  * dkv_block: a block owns 128 keys of a key head (TMEM lane = key) and walks
 //    the query tiles that see them, for every query head of the group:
 //    S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and
 //    dS^T (bf16) as A operands in TMEM over their own 32-bit columns. Two warps
@@ -19,7 +19,7 @@
 //    behind its own accumulation, in issue order. Eight warps (two per lane
 //    quadrant, 64 query columns each) turn S^T into P^T while dP^T and dK run, and
 //    dP^T into dS^T while dV and the next S^T run.
-//  * dq_kernel: a block owns 128 queries of a head (lane = query) and walks the
+//  * dq_block: a block owns 128 queries of a head (lane = query) and walks the
 //    key tiles: S = Q K^T, dP = dO V^T, dQ += dS K, dS in two buffers of its own.
 // Both read their tiles by TMA, three stages of the tensor that is used from the
 // scores to the accumulation, two of the other. D and lse in log2 units come from
@@ -302,22 +302,14 @@ __device__ __forceinline__ void score_gradients(float (&x)[32], const float (&w)
 
 // ----------------------------------------------------------------- dK and dV
 template <bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
-dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
-           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
-           const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_qc,
-           const __grid_constant__ CUtensorMap map_oc) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (smem_u32(smem_raw) & 1023u) {
-    if (threadIdx.x == 0) atomicExch(a.err, VSA_ERR_UNSUPPORTED);
-    return;
-  }
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+__device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, const CUtensorMap& map_k,
+                                          const CUtensorMap& map_v, const CUtensorMap& map_q, const CUtensorMap& map_o,
+                                          const CUtensorMap& map_qc, const CUtensorMap& map_oc) {
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // early key tiles, the longest under a causal mask, first
-  const int per = p.Hk * p.B * a.splits, kt = blockIdx.x / per, split = blockIdx.x % per % a.splits;
-  const int hk = blockIdx.x % per / a.splits % p.Hk, b = blockIdx.x % per / a.splits / p.Hk;
+  const int per = p.Hk * p.B * a.splits, kt = block / per, split = block % per % a.splits;
+  const int hk = block % per / a.splits % p.Hk, b = block % per / a.splits / p.Hk;
   const int k0 = kt * kRows;
   const uint32_t tmem = set_up(sm, kEw / 2, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 2);                // dO is read by dP^T and by dV
@@ -546,20 +538,13 @@ dkv_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap m
 
 // ------------------------------------------------------------------------ dQ
 template <bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
-dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_q,
-          const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_k,
-          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kc) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (smem_u32(smem_raw) & 1023u) {
-    if (threadIdx.x == 0) atomicExch(a.err, VSA_ERR_UNSUPPORTED);
-    return;
-  }
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+__device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, const CUtensorMap& map_q,
+                                         const CUtensorMap& map_o, const CUtensorMap& map_k, const CUtensorMap& map_v,
+                                         const CUtensorMap& map_kc) {
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = p.Hq * p.B, qt = a.nqt - 1 - blockIdx.x / per;   // late query tiles first
-  const int h = blockIdx.x % per % p.Hq, b = blockIdx.x % per / p.Hq, hk = h / p.group;
+  const int per = p.Hq * p.B, qt = a.nqt - 1 - block / per;   // late query tiles first
+  const int h = block % per % p.Hq, b = block % per / p.Hq, hk = h / p.group;
   const int q0 = qt * kRows;
   const uint32_t tmem = set_up(sm, kEw, [&] {
     mbar_init(smem_u32(&sm.b_empty[0]), 1);
@@ -737,6 +722,30 @@ dq_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap ma
   finish(tmem);
 }
 
+// Blocks of dK and dV, then blocks of dQ in the same grid: these do not read those,
+// and fill the SMs as the last of them end (two kernels: 4096 x
+// 24 heads 705 us, so 650; packed documents 886 and 861).
+struct Maps {
+  CUtensorMap q, k, v, o, qc, oc, kc;
+};
+
+template <bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+masked_bwd_kernel(const __grid_constant__ Args kv, const __grid_constant__ Args q, const __grid_constant__ Maps m,
+                  int n_dkv) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {          // swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicExch(kv.err, VSA_ERR_UNSUPPORTED);
+    return;
+  }
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int block = blockIdx.x;
+  if (block < n_dkv)
+    dkv_block<kCap, kBias>(sm, block, kv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+  else
+    dq_block<kCap, kBias>(sm, block - n_dkv, q, m.q, m.o, m.k, m.v, m.kc);
+}
+
 // dk and dv from the blocks' parts, added in order: one piece of 4 channels a thread.
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
   const Problem& p = a.p;
@@ -834,24 +843,18 @@ Workspace workspace_of(const Problem& p, int splits) {
   return w;
 }
 
-struct Maps {
-  CUtensorMap q, k, v, o, qc, oc, kc;
-};
-
 template <bool kCap, bool kBias>
 vsa_status launch(const Args& dkv, const Args& dq, const Maps& m, cudaStream_t stream) {
-  const auto k1 = dkv_kernel<kCap, kBias>;
-  const auto k2 = dq_kernel<kCap, kBias>;
-  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  const auto kernel = masked_bwd_kernel<kCap, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: shared memory", e);
   const Problem& p = dkv.p;
-  k1<<<p.nkt * p.Hk * p.B * dkv.splits, kThreads, sizeof(Smem), stream>>>(dkv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+  const int n_dkv = p.nkt * p.Hk * p.B * dkv.splits;
+  kernel<<<n_dkv + dq.nqt * p.Hq * p.B, kThreads, sizeof(Smem), stream>>>(dkv, dq, m, n_dkv);
   if (dkv.splits > 1) {
     const int64_t pieces = static_cast<int64_t>(p.B) * p.Sk * p.Hk * (kHeadDim / 4);
     join_kernel<<<dim3(static_cast<unsigned>((pieces + 255) / 256), 2), 256, 0, stream>>>(dkv);
   }
-  k2<<<dq.nqt * p.Hq * p.B, kThreads, sizeof(Smem), stream>>>(dq, m.q, m.o, m.k, m.v, m.kc);
   e = cudaGetLastError();
   return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_bwd", e);
 }
