@@ -779,11 +779,16 @@ void zero(const vsa_view* v, int32_t B, int32_t S, cudaStream_t stream) {
                                                                             view_strides(v, B, S), S, v->heads, n);
 }
 
-// Parts of a key tile's query tiles: where one block per key tile leaves SMs idle,
-// or, under a causal mask or with shared heads, where the longest block would
-// outlast the rest. Work in query tiles: the longest block against all work spread
-// over the SMs; the parts' 32-bit sums cost their traffic (3 us a query tile).
+// Parts of a key tile's query tiles: where the longest block would outlast the rest
+// (a causal mask, shared heads, few tiles). Cost in steps of dK and dV (3 us at most): a
+// step of dQ is two thirds of one, a block's start and end two. The grid ends with its
+// longest block or with all work spread over the SMs and a part of a block's length
+// behind it; parts cost their blocks' ends, the traffic of their 32-bit sums and one more
+// launch. Measured, us, chosen first: 2 x 1,555 causal tokens, 8 heads on 4: one part 101,
+// two 115; 3,000 causal, 9 heads on 3: two 141, one 209, three 149; 6,000 causal, 3 heads
+// on 1: three 133, one 285, four 137; 4,000 x 2 heads, no mask: one 90, two 110.
 int splits_of(const Problem& p) {
+  constexpr double kDq = 2.0 / 3.0;
   const double pairs = static_cast<double>(p.B) * p.Hk, sms = sm_count();
   const int nqt = tiles(p.Sq);
   double total = 0.0, longest = 0.0;
@@ -792,11 +797,13 @@ int splits_of(const Problem& p) {
     total += (nqt - first) * p.group;
     longest = std::max(longest, static_cast<double>(nqt - first) * p.group);
   }
+  const double dq = kDq * p.nkt + 2.0;                     // the longest block of dQ
   int best = 1;
   double least = 1e300;
   for (int s = 1; s <= 8 && s <= std::max(1.0, longest / 2); ++s) {
     const double part = std::ceil(longest / s) + 2.0;
-    double t = std::max(part, pairs * (total + 2.0 * p.nkt * s) / sms + (s == 1 && pairs * p.nkt < sms ? 0.0 : part / 3.0));
+    const double spread = pairs * (total * (1.0 + kDq) + 2.0 * p.nkt * s + 2.0 * nqt * p.group) / sms + 0.3 * dq;
+    double t = std::max(std::max(part, dq), spread);
     if (s > 1) t += 2.0 + pairs * p.nkt * kRows * s * 2048.0 / 6.5e12 / 3e-6;
     if (t < least * 0.95) {
       least = t;
