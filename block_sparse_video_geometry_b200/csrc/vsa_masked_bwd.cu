@@ -65,7 +65,7 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   return s;
 }
 
-__global__ void __launch_bounds__(kTileThreads) prepare_kernel(const __grid_constant__ PrepArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 2) prepare_kernel(const __grid_constant__ PrepArgs a) {
   const int tile = blockIdx.y, b = blockIdx.z;
   const bool key = static_cast<int>(blockIdx.x) >= a.Hq;
   const int h = key ? blockIdx.x - a.Hq : blockIdx.x;
@@ -82,32 +82,32 @@ __global__ void __launch_bounds__(kTileThreads) prepare_kernel(const __grid_cons
     write_clean(a.clean_k, w, bad[0], b, h, a.Hk, tile, a.nkt, a.Sk);
     return;
   }
+  // all loads of the tile in flight at once
   const int n = min(kRows, a.Sq - tile * kRows);
+  uint4 o[kPieces], wq[kPieces];
   load_pieces(w, a.dout + b * a.sd.b + r0 * a.sd.s + h * a.sd.h, a.sd.s, n);
+  load_pieces(o, a.out + b * a.so.b + r0 * a.so.s + h * a.so.h, a.so.s, n);
+  if (a.masked) load_pieces(wq, a.q + b * a.sq.b + r0 * a.sq.s + h * a.sq.h, a.sq.s, n);
   const size_t row0 = (static_cast<size_t>(b) * a.Hq + h) * a.nqt * kRows + r0;
-  const float* lse = a.lse + (static_cast<size_t>(b) * a.Hq + h) * a.Sq + r0;
+  if (threadIdx.x < kRows) {
+    const int r = threadIdx.x;
+    const float l = r < n ? a.lse[(static_cast<size_t>(b) * a.Hq + h) * a.Sq + r0 + r] * -kLog2e : -INFINITY;
+    a.lse2[row0 + r] = l == INFINITY ? -INFINITY : l;
+  }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int e = i * kTileThreads + threadIdx.x, r = e >> 4;
-    float d = 0.0f;
-    if (r < n) d = dot8(w[i], *reinterpret_cast<const uint4*>(a.out + b * a.so.b + (r0 + r) * a.so.s + h * a.so.h + (e & 15) * 8));
+    float d = dot8(w[i], o[i]);                            // rows past n: zero
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if ((e & 15) == 0) {
-      float l = -INFINITY;
-      if (r < n) l = lse[r] * -kLog2e;
-      a.delta[row0 + r] = -d;
-      a.lse2[row0 + r] = l == INFINITY ? -INFINITY : l;
-    }
+    for (int s = 8; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+    if ((e & 15) == 0) a.delta[row0 + r] = -d;
   }
   if (!a.masked) return;
   find_bad(w, bad[0]);
+  find_bad(wq, bad[1]);
   __syncthreads();
   write_clean(a.clean_o, w, bad[0], b, h, a.Hq, tile, a.nqt, a.Sq);
-  load_pieces(w, a.q + b * a.sq.b + r0 * a.sq.s + h * a.sq.h, a.sq.s, n);
-  find_bad(w, bad[1]);
-  __syncthreads();
-  write_clean(a.clean_q, w, bad[1], b, h, a.Hq, tile, a.nqt, a.Sq);
+  write_clean(a.clean_q, wq, bad[1], b, h, a.Hq, tile, a.nqt, a.Sq);
 }
 
 // ------------------------------------------------------------------- shared
