@@ -438,17 +438,17 @@ def _view(t) -> bytes:
 def _run(name, tensors, *args) -> None:
     """Calls a library function with the tensors' device current; they must share one CUDA device."""
     import torch
-    device = tensors[0].device
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device, got %s" % device)
+    index = tensors[0].get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device, got %s" % tensors[0].device)
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors must be on one device, got %s and %s" % (device, t.device))
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be on one device, got %s and %s" % (tensors[0].device, t.device))
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         status = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args)
     if status != OK:
         raise VSAError(status, name)
@@ -472,19 +472,21 @@ def rope_positions(layout: Layout, pos, origin=(0, 0, 0), stream=None) -> None:
 
 def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
     import torch
-    if q.dim() != 4 or q.shape[-1] != HEAD_DIM or q_out.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM or q_out.shape != shape:
         raise ValueError("q and its output must be [B, S, H, 128]")
-    B, S = q.shape[0], q.shape[1]
+    B, S = shape[0], shape[1]
     if (k is None) != (k_out is None):
         raise ValueError("k and its output come together")
-    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[-1] != HEAD_DIM
-                          or k_out.shape != k.shape):
-        raise ValueError("k and its output must be [B, S, H, 128] with q's B and S")
-    if pos.dtype != torch.int32 or tuple(pos.shape) not in ((S, 3), (B, S, 3)) \
-            or (S > 1 and pos.stride()[-2:] != (3, 1)):
+    if k is not None:
+        shape = k.shape
+        if len(shape) != 4 or shape[0] != B or shape[1] != S or shape[3] != HEAD_DIM or k_out.shape != shape:
+            raise ValueError("k and its output must be [B, S, H, 128] with q's B and S")
+    shape, strides = pos.shape, pos.stride()
+    if pos.dtype != torch.int32 or shape not in ((S, 3), (B, S, 3)) or (S > 1 and strides[-2:] != (3, 1)):
         raise ValueError("pos must be int32 [S, 3] or [B, S, 3], contiguous in its last two dimensions")
     _run(name, (q, pos, k, q_out, k_out), ctypes.byref(rope), B, S, pos.data_ptr(),
-         pos.stride(0) if pos.dim() == 3 else 0, _view(q), None if k is None else _view(k), _view(q_out),
+         strides[0] if len(strides) == 3 else 0, _view(q), None if k is None else _view(k), _view(q_out),
          None if k is None else _view(k_out), _stream_handle(stream))
 
 
@@ -501,7 +503,7 @@ def rope_bwd(rope: Rope, pos, dq_out, dk_out, dq, dk, stream=None) -> None:
 
 def _norm_shape(x):
     """(B, S, heads, width) of x [S, width], [B, S, width] or [B, S, heads, width]."""
-    s = tuple(x.shape)
+    s = x.shape
     if not 2 <= len(s) <= 4:
         raise ValueError("x must be [S, width], [B, S, width] or [B, S, heads, width]")
     return (1, s[0], 1, s[1]) if len(s) == 2 else (s[0], s[1], 1, s[2]) if len(s) == 3 else s
