@@ -286,7 +286,7 @@ constexpr float kSumLimit = 4294967296.0f;          // 2^32: see the softmax ste
 struct Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[2][kStages], empty[kStages];   // full: see count_of
   uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];   // [slot][score buffer]
   uint64_t first_done, second_out;   // one tile: slot 0 needs Q no longer; slot 1's result is in shared memory
   float m1[kRows], l1[kRows];        // its maximum and sum; its O lies over Q, [channel][row]
@@ -354,7 +354,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 
   if (threadIdx.x == 32 * kWarpLoad) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.full[0][i]), 1);
+      mbar_init(smem_u32(&sm.full[1][i]), 1);
       mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one slot, or by both
     }
     mbar_init(smem_u32(&sm.q_full), 8);
@@ -424,11 +425,19 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int n = s1 - s0;
   const uint4* bad = a.clean_v.bad ? a.clean_v.bad + (static_cast<size_t>(b) * p.Hk + hk) * p.nkt : nullptr;
 
-  // Stage of K or V of key tile j in loading order. With one tile the slots hold
-  // two key tiles' scores at a time, so K runs two tiles ahead of V.
+  // Place of K or V of key tile j in loading order; place % kStages is its stage. With
+  // one tile the slots hold two key tiles' scores at a time, so K runs two tiles ahead
+  // of V.
   const int ahead = one ? 2 : 1;
   auto place_k = [&](int j) { return j + max(0, j - ahead + 1); };
   auto place_v = [&](int j) { return j + min(n, j + ahead); };
+  // Count of the barrier that its landing completes, full[one ? j & 1 : 0][count %
+  // kStages]. A barrier's parity tells its phases apart only for one who saw the
+  // last. Both slots see every stage of two tiles; with one tile each sees its own key
+  // tiles only, so that the slots have barriers of their own, counted over their own
+  // stages (K and V in turn). A count comes round, kStages of them later, behind at
+  // least kStages stages of the ring: the stage before has been read, and seen, by then.
+  auto count_of = [&](int j, bool v) { return one ? (j & ~1) + v : v ? place_v(j) : place_k(j); };
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
@@ -448,14 +457,20 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           const uint4 m = bad[kt];
           if (m.x | m.y | m.z | m.w) map = &map_vc, h = hk, bb = b;
         }
-        const uint32_t bar = smem_u32(&sm.full[st]), dst = smem_u32(sm.kv[st]);
+        const uint32_t bar = smem_u32(&sm.full[one ? j & 1 : 0][count_of(j, is_v) % kStages]), dst = smem_u32(sm.kv[st]);
         mbar_arrive_expect_tx(bar, kTileBytes);
         tma_load_4d(dst, map, 0, kt * kRows, h, bb, bar);
         tma_load_4d(dst + kTileBytes / 2, map, 64, kt * kRows, h, bb, bar);
       }
-      if (!ok)                                             // every issued copy lands before the block exits
-        for (int i = max(0, e - kStages); i < e; ++i)
-          mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
+      if (!ok) {                                           // every issued copy lands before the block exits
+        kj = vj = 0;
+        for (int i = 0; i < e; ++i) {
+          const bool is_v = kj == min(n, vj + ahead);
+          const int j = is_v ? vj++ : kj++, c = count_of(j, is_v);
+          if (i >= e - kStages)
+            mbar_wait(smem_u32(&sm.full[one ? j & 1 : 0][c % kStages]), (c / kStages) & 1, nullptr, kDrainNs);
+        }
+      }
     }
     __syncwarp();
   } else if (warp == kWarpMma || warp == kWarpMma + 1) {
@@ -469,19 +484,15 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const uint32_t ts = tmem + kColS + 128 * t, to = tmem + kColO + 128 * t;
     const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[one ? 0 : t]), 16, 1024);
     bool ok = warp_wait(sm, sm.q_full, 0, a.err);
-    // Waits for every stage up to the e-th in loading order, the other slot's among
-    // them: a barrier's parity tells its phases apart only for one who saw the last.
-    int seen = 0;
-    auto landed = [&](int e) {
-      for (; seen <= e; ++seen)
-        if (!warp_wait(sm, sm.full[seen % kStages], (seen / kStages) & 1, a.err)) return false;
-      return true;
+    auto landed = [&](int j, bool v) {
+      const int c = count_of(j, v);
+      return warp_wait(sm, sm.full[one ? t : 0][c % kStages], (c / kStages) & 1, a.err);
     };
     // S(j, hb) = Q K^T over half hb of key tile j: 16 channels per K step, 32 B
     // inside a swizzled row of the d half kk / 4; 64 key rows = 8 KB.
     auto scores = [&](int j, int hb) {
-      const int e = place_k(j), st = e % kStages;
-      if (hb == 0 && !landed(e)) return false;
+      const int st = place_k(j) % kStages;
+      if (hb == 0 && !landed(j, false)) return false;
       tc_fence_after();
       const uint64_t kd = smem_desc_sw128(smem_u32(sm.kv[st]) + 8192 * hb, 16, 1024);
       if (elect_one()) {
@@ -498,8 +509,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int step = one ? 2 : 1, j0 = one ? t : 0;
     if (ok && j0 < n) ok = scores(j0, 0) && scores(j0, 1);
     for (int j = j0, i = 0; ok && j < n; j += step, ++i) {
-      const int e = place_v(j), st = e % kStages;
-      if (!(ok = landed(e))) break;
+      const int st = place_v(j) % kStages;
+      if (!(ok = landed(j, true))) break;
 #pragma unroll 1
       for (int hb = 0; hb < 2; ++hb) {
         if (!(ok = warp_wait(sm, sm.p_full[t][hb], i & 1, a.err))) break;

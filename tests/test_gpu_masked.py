@@ -491,3 +491,28 @@ def test_many_blocks_agree_with_themselves(cuda_ok, shape):
         assert torch.equal(first, again)
     ref = Reference(q[:1, :, :1], k[:1, :, :1], v[:1, :, :1], visible(1, Sq, Sk))
     within(first[:1, :, :1], ref.out, ref.t_out, "out")
+
+
+@pytest.mark.parametrize("parity", [0, 1])
+@pytest.mark.parametrize("shape", [(1, 300, 20000, 8, 8), (2, 120, 6000, 6, 6)], ids=lambda s: "x".join(map(str, s)))
+def test_slots_far_apart(cuda_ok, shape, parity):
+    """Every second key tile lies so far above the one before that its slot raises the reference each time and falls
+    behind the other slot of the block: the shared ring must not move on by more than a stage that a slot has seen
+    (its parity would come round again, and the slot would wait for good)."""
+    import torch
+    B, Sq, Sk, Hq, Hk = shape
+    q, k, v, _ = tensors(*shape, seed=23)
+    tile = torch.arange(Sk, device="cuda") // 128
+    up = 23.0 * ((int(tile[-1]) - tile) // 2 % 13) * (tile % 2 == parity)
+    q[..., 0] = 1.0
+    k[..., 0] = (up * math.sqrt(128)).to(k.dtype)[None, :, None]
+    attn = vsa.MaskedAttention(vsa.make_mask(causal=True), *shape)
+    first, lse = attn.forward(q, k, v)
+    assert vsa.masked_attn_status(attn.ws_fwd[0]) == vsa.OK
+    for _ in range(10):
+        again, _ = attn.forward(q, k, v)
+        assert torch.equal(first, again)
+    assert vsa.masked_attn_status(attn.ws_fwd[0]) == vsa.OK
+    ref = Reference(q[:, :, :2], k[:, :, :2], v[:, :, :2], visible(B, Sq, Sk, causal=True))
+    within(first[:, :, :2], ref.out, ref.t_out, "out")
+    within(lse[:, :2], ref.lse, ref.t_lse, "lse")
