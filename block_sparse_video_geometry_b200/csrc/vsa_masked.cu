@@ -288,8 +288,8 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes];
   uint64_t full[2][kStages], empty[kStages];   // full: see count_of
   uint64_t q_full, s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];   // [slot][score buffer]
-  uint64_t first_done, second_out;   // one tile: slot 0 needs Q no longer; slot 1's result is in shared memory
-  float m1[kRows], l1[kRows];        // its maximum and sum; its O lies over Q, [channel][row]
+  uint64_t joined;                   // one tile: both slots' halves of O, maxima and sums are in shared memory
+  float m[2][kRows], l[2][kRows];
   uint32_t tmem_base;
   int abort;
 };
@@ -352,6 +352,16 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int unit = id % a.units, b = id / a.units;
   const int hk = a.packed ? unit : unit / p.group;
 
+  // key tiles of this block: entries [s0, s1) of its list (or the numbers themselves)
+  const size_t plan_row = static_cast<size_t>(b) * a.n_blocks + qb;
+  int n_all;
+  if (a.count) {
+    n_all = a.count[plan_row];
+  } else {
+    const int last = a.packed ? p.Sq - 1 : min((qb + 1) * (one ? kRows : 2 * kRows), p.Sq) - 1;
+    n_all = max(0, p.limit(b, last) + kRows) / kRows;     // tiles up to the last row's limit (none: below 0)
+  }
+
   if (threadIdx.x == 32 * kWarpLoad) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sm.full[0][i]), 1);
@@ -359,8 +369,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       mbar_init(smem_u32(&sm.empty[i]), one ? 1 : 2);     // a stage is read by one slot, or by both
     }
     mbar_init(smem_u32(&sm.q_full), 8);
-    mbar_init(smem_u32(&sm.first_done), 4);
-    mbar_init(smem_u32(&sm.second_out), 4);
+    mbar_init(smem_u32(&sm.joined), 8);
     for (int t = 0; t < 2; ++t) {
       for (int hb = 0; hb < 2; ++hb) {
         mbar_init(smem_u32(&sm.s_full[t][hb]), 1);
@@ -408,15 +417,6 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // key tiles of this block: entries [s0, s1) of its list (or the numbers themselves)
-  const size_t plan_row = static_cast<size_t>(b) * a.n_blocks + qb;
-  int n_all;
-  if (a.count) {
-    n_all = a.count[plan_row];
-  } else {
-    const int last = a.packed ? p.Sq - 1 : min((qb + 1) * (one ? kRows : 2 * kRows), p.Sq) - 1;
-    n_all = max(0, p.limit(b, last) + kRows) / kRows;     // tiles up to the last row's limit (none: below 0)
-  }
   const int32_t* list = a.count ? a.list + plan_row * p.nkt : nullptr;
   const int s0 = static_cast<int>(static_cast<int64_t>(n_all) * split / a.splits);
   const int s1 = static_cast<int>(static_cast<int64_t>(n_all) * (split + 1) / a.splits);
@@ -781,72 +781,68 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       ok = warp_wait(sm, sm.o_full[t], 0, a.err);
       tc_fence_after();
     }
-    float* o1 = reinterpret_cast<float*>(sm.q[0]);          // 64 KB over both Q tiles
+    // One tile: each slot joins its own 64 channels with the other's, which lie over Q,
+    // [channel][row] (slot 0 joining all: 1 us a block more).
+    float* held = reinterpret_cast<float*>(sm.q[0]);        // 64 KB over both Q tiles
+    const int c0 = one ? 64 * t : 0, c1 = one ? c0 + 64 : kHeadDim;
+    const bool other = one && n > 1;                        // both slots had a key tile
     float f0 = 1.0f, f1 = 0.0f;
-    if (one && ok) {
-      if (t == 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.first_done));
-        ok = warp_wait(sm, sm.second_out, 0, a.err);
-        if (ok) {
-          const float m1 = sm.m1[r], l1 = sm.l1[r], top = fmaxf(m, m1), ref = top == -INFINITY ? 0.0f : top;
-          f0 = ex2_approx(m - ref);
-          f1 = ex2_approx(m1 - ref);
-          l = fmaf(l, f0, l1 * f1);
-          m = top;
-        }
-      } else {
-        ok = warp_wait(sm, sm.first_done, 0, a.err);
-        if (ok) {
-          sm.m1[r] = m;
-          sm.l1[r] = l;
+    if (other && ok) {
+      ok = warp_wait(sm, sm.o_full[t ^ 1], 0, a.err);       // its products read Q no longer
+      if (ok) {
+        sm.m[t][r] = m;
+        sm.l[t][r] = l;
 #pragma unroll 1
-          for (int q4 = 0; i > 0 && q4 < 4; ++q4) {
-            float o[32];
-            tmem_ld32x32f(to + 32 * q4, o);
-            tmem_wait_ld32(o);
+        for (int c = 64 - c0; c < 128 - c0; c += 32) {
+          float o[32];
+          tmem_ld32x32f(to + c, o);
+          tmem_wait_ld32(o);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o1[(32 * q4 + u) * kRows + r] = o[u];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.second_out));
+          for (int u = 0; u < 32; ++u) held[(c + u) * kRows + r] = o[u];
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.joined));
+        ok = warp_wait(sm, sm.joined, 0, a.err);
+        const float mo = sm.m[t ^ 1][r], top = fmaxf(m, mo), ref = top == -INFINITY ? 0.0f : top;
+        f0 = ex2_approx(m - ref);
+        f1 = ex2_approx(mo - ref);
+        l = l * f0 + sm.l[t ^ 1][r] * f1;
+        m = top;
       }
     }
-    if (ok && !(one && t == 1)) {
-      const bool second = one && n > 1;                      // slot 1 had a key tile
+    if (ok && !(one && t == 1 && !other)) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
       const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.Sq + i_q;
       const size_t all = static_cast<size_t>(p.B) * p.Hq * p.Sq;
-      if (live) {
+      if (live && !(one && t == 1)) {
         if (a.part_o) a.part_lse[split * all + at] = lse2;
         else a.lse[at] = lse2 * 0.6931471805599453f;
       }
 #pragma unroll 1
-      for (int q4 = 0; q4 < 4; ++q4) {
+      for (int c = c0; c < (other ? c1 : kHeadDim); c += 32) {
         float o[32];
         __syncwarp();
         if (i > 0) {
-          tmem_ld32x32f(to + 32 * q4, o);
+          tmem_ld32x32f(to + c, o);
           tmem_wait_ld32(o);
         } else {
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0.0f;
         }
         if (live) {
-          if (second) {
+          if (other) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = fmaf(o1[(32 * q4 + u) * kRows + r], f1, o[u] * f0);
+            for (int u = 0; u < 32; ++u) o[u] = fmaf(held[(c + u) * kRows + r], f1, o[u] * f0);
           }
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
           if (a.part_o) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (split * all + at) * kHeadDim + 32 * q4);
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (split * all + at) * kHeadDim + c);
 #pragma unroll
             for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + 32 * q4);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + c);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
