@@ -940,11 +940,13 @@ Layout layout_of(const Problem& p) {
     const double tile = !one ? 4.0 : n_blocks > 1 ? 2.2 : 3.3, fixed = one && n_blocks == 1 ? 16.0 : 6.0;
     // key tiles of the blocks together, and of the longest
     double total = static_cast<double>(n_blocks) * p.nkt;
-    const bool unequal = p.causal && !best.packed && n_blocks > 1;
+    bool unequal = p.causal && !best.packed && n_blocks > 1;
     if (unequal) {
       total = 0.0;
       for (int qb = 0; qb < n_blocks; ++qb)
         total += std::max(0, std::min(p.nkt, (std::min((qb + 1) * per, p.Sq) + p.off + kRows - 1) / kRows));
+      // queries behind a long cache: as good as equal (300 over 20,000 keys, 8 heads: 144 blocks 79 us, 192 98 us)
+      if (total > 0.95 * n_blocks * p.nkt) unequal = false;
     }
     for (int s = 1; s <= 64 && s <= std::max(1, p.nkt / 2); ++s) {
       const double longest = tile * ((p.nkt + s - 1) / s) + fixed, blocks = n_blocks * pairs * s;
