@@ -20,7 +20,7 @@ struct ScoreTerms {
   __device__ __forceinline__ ScoreTerms(float scale, float cap, float slope_) {
     c = scale * kLog2e;
     cap2 = cap * kLog2e;
-    in = cap > 0.0f ? scale / cap : 0.0f;
+    in = cap > 0.0f ? fminf(scale / cap, 1e37f) : 0.0f;    // finite: 0 stays 0 under the smallest caps
     slope = slope_ * kLog2e;
     // c tanh(y) / y = c (1 + a1 z + a2 z^2 + a3 z^3 + a4 z^4), z = y^2 = (in x)^2, with
     // in^2 and c multiplied into the coefficients
@@ -97,9 +97,11 @@ struct PairArgs {
 // Raw scores x (sums of products) -> their log2 values minus a reference (`ref`
 // gives minus the reference for a pair of columns). With a cap t receives
 // tanh(score / cap). kBoth: the polynomial where the columns lie on both sides of the
-// rows too (one more form in the code: faster in the forward pass, whose blocks start
-// with such tiles, slower in the backward's kernels, 544 -> 636 us for 4096 x 24 heads,
-// which have few registers).
+// rows too. That is one more form in the code: faster in the forward pass, whose blocks
+// start with such tiles; slower in the backward pass, which has few registers (4096 x 24
+// heads 544 -> 636 us) and takes it for caps above kFarCap only: the general form of tanh
+// is off by a part of 1, not of the score, and would lose the scores under a cap of 10^6.
+constexpr float kFarCap = 128.0f;
 template <bool kCap, bool kBias, bool kBoth, class Ref>
 __device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
                                            Ref ref) {

@@ -34,7 +34,7 @@ struct Problem {
   // Last key position that query i sees by order.
   __device__ __forceinline__ int limit(int b, int i) const {
     if (!causal) return Sk - 1;
-    const int p = prefix ? prefix[b] : 0;
+    const int p = prefix ? max(prefix[b], 0) : 0;          // any 32-bit value
     return min(max(i + off, p - 1), Sk - 1);
   }
 };

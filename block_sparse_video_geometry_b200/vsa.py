@@ -640,7 +640,8 @@ def masked_attn_status(workspace, stream=None) -> int:
 
 class MaskedAttention:
     """Dense attention of one shape and mask with its workspaces (allocated by the first call that needs them, so
-    run one call before a capture)."""
+    run one call before a capture). Calls of one object share them: for calls on two streams, or graphs that may run
+    at once, make one object each."""
 
     def __init__(self, mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int, device="cuda"):
         self.shape, self.device = (B, Sq, Sk, Hq, Hk), device

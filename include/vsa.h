@@ -635,7 +635,7 @@ vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32
  *                 vsa_masked_attn_status), the visible tiles, partial results;
  *                 written before it is read. Two calls that may overlap need
  *                 two workspaces.
- * Masked keys do not reach a row whatever they hold: infinities and NaN in
+ * No output may overlap an input or another output. Masked keys do not reach a row whatever they hold: infinities and NaN in
  * their k and v change nothing. A row that sees a key with an infinity or NaN
  * in its v is NaN throughout when the call masks anything.
  * Scores, softmax statistics and sums are 32-bit; the probabilities enter the
@@ -658,7 +658,7 @@ vsa_status vsa_masked_attn_bwd_workspace_size(const vsa_mask* mask, int32_t B, i
  *               nothing, or that nothing sees, gets 0. The slopes get no
  *               gradient.
  *  workspace  : vsa_masked_attn_bwd_workspace_size bytes, 256-byte aligned.
- * With P = exp(s - lse) and D = sum(dout * out): dS = P (dout v - D), times
+ * No output may overlap an input or another output. With P = exp(s - lse) and D = sum(dout * out): dS = P (dout v - D), times
  * 1 - tanh^2 under a cap; dq = scale dS k, dk = scale dS^T q, dv = P^T dout. P and
  * dS enter the products as bf16, every sum is 32-bit and in a fixed order: equal
  * inputs give equal bits. Masked rows that hold infinities or NaN change

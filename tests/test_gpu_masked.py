@@ -516,3 +516,42 @@ def test_slots_far_apart(cuda_ok, shape, parity):
     ref = Reference(q[:, :, :2], k[:, :, :2], v[:, :, :2], visible(B, Sq, Sk, causal=True))
     within(first[:, :, :2], ref.out, ref.t_out, "out")
     within(lse[:, :2], ref.lse, ref.t_lse, "lse")
+
+
+def test_prefixes_of_every_size(cuda_ok):
+    """The smallest and largest 32-bit prefixes: none, and all keys."""
+    import torch
+    case = (3, 200, 333, 2, 1, True, (-2 ** 31, 2 ** 31 - 1, -1), 0.0, False, None)
+    q, k, v, dout = tensors(*case[:5], seed=29)
+    terms = terms_of(case)
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, dout=dout, **terms)
+    ref = reference(case, q, k, v, {"prefix": terms["prefix"].double()}, dout)
+    for name, got in (("lse", lse), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+@pytest.mark.parametrize("cap", [1e6, 1e30, 3e38])
+@pytest.mark.parametrize("bias", [False, True])
+def test_caps_far_above_the_scores(cuda_ok, cap, bias):
+    """A cap c far above the scores is none: s - c tanh(s / c) <= s^3 / (3 c^2) < 2^-24 |s| for |s| < 400. The bounds
+    are those without a cap, and 2^-23 |s| for the polynomial, below their 64 u."""
+    case = (1, 300, 300, 2, 1, True, None, 0.0, bias, None)
+    q, k, v, dout = tensors(*case[:5], seed=31)
+    terms = terms_of(case)
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, cap=cap, dout=dout, **terms)
+    ref = reference(case, q, k, v, terms, dout)
+    for name, got in (("lse", lse), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1e-30, 1e-40])
+def test_caps_far_below_the_scores(cuda_ok, cap):
+    """Every score at the cap (or 0 for a query of zeros): nearly equal weights, no gradient of q and k."""
+    case = (1, 150, 270, 2, 2, True, None, cap, False, None)
+    q, k, v, dout = tensors(*case[:5], seed=37)
+    q[:, 5] = 0
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, cap=cap, dout=dout)
+    ref = reference(case, q, k, v, {}, dout)
+    for name, got in (("lse", lse), ("out", out), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+    assert dq.isfinite().all() and dk.isfinite().all()
