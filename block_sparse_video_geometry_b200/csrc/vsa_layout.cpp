@@ -327,7 +327,7 @@ const char* vsa_status_string(vsa_status s) {
   return "unknown status";
 }
 
-int32_t vsa_version(void) { return (1 << 16) | 4; }
+int32_t vsa_version(void) { return (1 << 16) | 5; }
 
 const char* vsa_last_error_detail(void) { return g_detail; }
 
