@@ -572,6 +572,22 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         const uint32_t tb = ts + 64 * hb;                    // this half's scores
         if (!(ok = warp_wait(sm, sm.s_full[t][hb], i & 1, a.err))) break;
         tc_fence_after();
+        // A row that sees none of the half by order or by the tile's document waits for
+        // its reference; a warp of such rows has P = 0. (Blocks across two documents had
+        // their second rows' references sought at every tile of the first: 150 us
+        // for 40 tiles.)
+        const bool none = lim_t < k0 + 64 * hb;
+        if (__all_sync(0xffffffffu, none)) {
+          uint32_t zero[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) zero[u] = 0;
+          for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, zero);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t][hb]));
+          continue;
+        }
         // scores of key columns [32 q4, 32 q4 + 32) in place -> log2 units minus a
         // reference: cap, bias, mask
         auto finish = [&](int q4, float (&x)[32], float minus_ref) {
@@ -751,13 +767,13 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             if (!ok) break;
             psum = exponentials();
             if (raised) break;
-            raise = m == -INFINITY || !(psum <= kSumLimit);    // the others of the warp keep theirs
+            raise = (m == -INFINITY && !none) || !(psum <= kSumLimit);   // the others of the warp keep theirs
             raised = __any_sync(0xffffffffu, raise);
             if (!raised) break;
           }
         } else {
           if (kBias || !first) psum = exponentials();
-          const bool raise = m == -INFINITY || !(psum <= kSumLimit);
+          const bool raise = (m == -INFINITY && !none) || !(psum <= kSumLimit);
           if (__any_sync(0xffffffffu, raise)) {
             rise(raise);
             if (ok) psum = exponentials();

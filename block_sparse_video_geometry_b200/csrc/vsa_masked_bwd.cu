@@ -475,6 +475,23 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
       tc_fence_after();
       float x[32], w[32];
       uint32_t pw[16];
+      if (partial && __all_sync(0xffffffffu, see == 0)) {   // none of the warp's pairs is visible
+#pragma unroll
+        for (int u = 0; u < 16; ++u) pw[u] = 0;
+        tmem_st32x16(ts, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[half]));
+        if (!(ok = warp_wait(sm, sm.dp_full[half], j & 1, a.err))) break;
+        tc_fence_after();
+        tmem_st32x16(tp, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[half]));
+        continue;
+      }
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       const float* lse = sm.lse2[st] + 32 * part;
@@ -682,6 +699,19 @@ __device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, con
       tc_fence_after();
       float x[32], w[32];
       uint32_t pw[16];
+      if (partial && __all_sync(0xffffffffu, see == 0)) {   // none of the warp's pairs is visible
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
+        if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) pw[u] = 0;
+        tmem_st32x16(lane_addr + kColDs + 64 * (j & 1) + 16 * part, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[0]));
+        continue;
+      }
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       tc_fence_before();                                   // S(j) is in registers: S(j + 1) may replace it
