@@ -835,6 +835,11 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         if (a.part_o) a.part_lse[split * all + at] = lse2;
         else a.lse[at] = lse2 * 0.6931471805599453f;
       }
+      // bf16 rows of the output go through shared memory that no product reads any more
+      // (Q, or where both slots' products have ended a stage of the ring), each warp's own
+      // rows, so that whole rows are stored and not 16 bytes of 32 rows at a time.
+      const int chunks = other ? 8 : 16;                    // 16-byte pieces of a row
+      uint8_t* rows = (other ? sm.kv[t] : sm.q[t]) + (warp & 3) * 32 * chunks * 16;
 #pragma unroll 1
       for (int c = c0; c < (other ? c1 : kHeadDim); c += 32) {
         float o[32];
@@ -846,24 +851,33 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0.0f;
         }
-        if (live) {
-          if (other) {
+        if (other) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = fmaf(held[(c + u) * kRows + r], f1, o[u] * f0);
-          }
+          for (int u = 0; u < 32; ++u) o[u] = fmaf(held[(c + u) * kRows + r], f1, o[u] * f0);
+        }
 #pragma unroll
-          for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
-          if (a.part_o) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (split * all + at) * kHeadDim + c);
+        for (int u = 0; u < 32; ++u) o[u] = l == 0.0f ? 0.0f : o[u] * inv;
+        if (!a.part_o) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + b * a.so.b + i_q * a.so.s + h * a.so.h + c);
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(rows + (lane * chunks + (((c - c0) / 8 + u) ^ (lane & (chunks - 1)))) * 16) =
+                make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                           pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+        } else if (live) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (split * all + at) * kHeadDim + c);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                                  pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-          }
+          for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
+      }
+      if (!a.part_o) {
+        const int64_t mine = live ? b * a.so.b + i_q * a.so.s + h * a.so.h : -1;   // the row's place in out
+        __syncwarp();
+        for (int it = 0; it < chunks; ++it) {
+          const int e = it * 32 + lane, rr = e / chunks, k = e & (chunks - 1);
+          const int64_t place = __shfl_sync(0xffffffffu, mine, rr);
+          if (place >= 0)
+            *reinterpret_cast<uint4*>(a.out + place + c0 + 8 * k) =
+                *reinterpret_cast<const uint4*>(rows + (rr * chunks + (k ^ (rr & (chunks - 1)))) * 16);
         }
       }
     }

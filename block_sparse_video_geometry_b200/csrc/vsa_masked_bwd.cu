@@ -191,8 +191,11 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 
 __device__ __forceinline__ bool any(uint4 m) { return m.x | m.y | m.z | m.w; }
 
-// 32 columns of 32-bit sums times `f` as bf16 into a row (or zeros).
-__device__ __forceinline__ void write_columns(uint32_t taddr, bool have, float f, bool live, uint16_t* row) {
+// 32 columns of 32-bit sums times `f` (or zeros) as bf16 into `row` (a row per lane;
+// null: none). They go through the warp's 2 KB at `stage`, so that 64 bytes of a
+// row are stored together and not 16 of 32 rows at a time.
+__device__ __forceinline__ void write_columns(uint32_t taddr, bool have, float f, uint16_t* row, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
   float o[32];
   __syncwarp();
   if (have) {
@@ -202,12 +205,19 @@ __device__ __forceinline__ void write_columns(uint32_t taddr, bool have, float f
 #pragma unroll
     for (int u = 0; u < 32; ++u) o[u] = 0.0f;
   }
-  if (!live) return;
-  uint4* dst = reinterpret_cast<uint4*>(row);
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    dst[u] = make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
-                        pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f), pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
+    *reinterpret_cast<uint4*>(stage + lane * 64 + (u ^ (lane >> 1 & 3)) * 16) =
+        make_uint4(pack_bf16x2(o[8 * u] * f, o[8 * u + 1] * f), pack_bf16x2(o[8 * u + 2] * f, o[8 * u + 3] * f),
+                   pack_bf16x2(o[8 * u + 4] * f, o[8 * u + 5] * f), pack_bf16x2(o[8 * u + 6] * f, o[8 * u + 7] * f));
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 8 + (lane >> 2), k = lane & 3;
+    uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+    if (to)
+      *reinterpret_cast<uint4*>(to + 8 * k) = *reinterpret_cast<const uint4*>(stage + r * 64 + (k ^ (r >> 1 & 3)) * 16);
+  }
 }
 
 // 32 columns of 32-bit sums times `f` (or zeros).
@@ -475,23 +485,6 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
       tc_fence_after();
       float x[32], w[32];
       uint32_t pw[16];
-      if (partial && __all_sync(0xffffffffu, see == 0)) {   // none of the warp's pairs is visible
-#pragma unroll
-        for (int u = 0; u < 16; ++u) pw[u] = 0;
-        tmem_st32x16(ts, pw);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[half]));
-        if (!(ok = warp_wait(sm, sm.dp_full[half], j & 1, a.err))) break;
-        tc_fence_after();
-        tmem_st32x16(tp, pw);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[half]));
-        continue;
-      }
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       const float* lse = sm.lse2[st] + 32 * part;
@@ -531,8 +524,9 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[half]));
     }
-    if (ok && n > 0) {
-      ok = warp_wait(sm, sm.acc[0], 0, a.err) && warp_wait(sm, sm.acc[1], 0, a.err);
+    if (ok) {                                              // K and V are read no more; nor are they on their way
+      ok = n > 0 ? warp_wait(sm, sm.acc[0], 0, a.err) && warp_wait(sm, sm.acc[1], 0, a.err)
+                 : warp_wait(sm, sm.own_full, 0, a.err);
       tc_fence_after();
     }
     if (ok && a.part) {
@@ -544,10 +538,12 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
     } else if (ok) {
       const bool live = key < p.Sk;
       const int64_t kk = live ? key : 0;
-      write_columns(lane_addr + kColDk + 32 * part, n > 0, p.scale, live,
-                    a.out1 + b * a.so1.b + kk * a.so1.s + hk * a.so1.h + 32 * part);
-      write_columns(lane_addr + kColDv + 32 * part, n > 0, 1.0f, live,
-                    a.out2 + b * a.so2.b + kk * a.so2.s + hk * a.so2.h + 32 * part);
+      write_columns(lane_addr + kColDk + 32 * part, n > 0, p.scale,
+                    live ? a.out1 + b * a.so1.b + kk * a.so1.s + hk * a.so1.h + 32 * part : nullptr,
+                    sm.own[0] + warp * 2048);
+      write_columns(lane_addr + kColDv + 32 * part, n > 0, 1.0f,
+                    live ? a.out2 + b * a.so2.b + kk * a.so2.s + hk * a.so2.h + 32 * part : nullptr,
+                    sm.own[1] + warp * 2048);
     }
   }
   finish(tmem);
@@ -699,19 +695,6 @@ __device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, con
       tc_fence_after();
       float x[32], w[32];
       uint32_t pw[16];
-      if (partial && __all_sync(0xffffffffu, see == 0)) {   // none of the warp's pairs is visible
-        if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
-        if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int u = 0; u < 16; ++u) pw[u] = 0;
-        tmem_st32x16(lane_addr + kColDs + 64 * (j & 1) + 16 * part, pw);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[0]));
-        continue;
-      }
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       tc_fence_before();                                   // S(j) is in registers: S(j + 1) may replace it
@@ -741,13 +724,14 @@ __device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, con
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.ds_done[0]));
     }
-    if (ok && n > 0) {
-      ok = warp_wait(sm, sm.acc[0], 0, a.err);
+    if (ok) {                                              // Q and dO are read no more; nor are they on their way
+      ok = warp_wait(sm, n > 0 ? sm.acc[0] : sm.own_full, 0, a.err);
       tc_fence_after();
     }
     if (ok)
-      write_columns(lane_addr + kColDq + 32 * part, n > 0, p.scale, live,
-                    a.out1 + b * a.so1.b + i_q * a.so1.s + h * a.so1.h + 32 * part);
+      write_columns(lane_addr + kColDq + 32 * part, n > 0, p.scale,
+                    live ? a.out1 + b * a.so1.b + i_q * a.so1.s + h * a.so1.h + 32 * part : nullptr,
+                    sm.own[0] + warp * 2048);
   }
   finish(tmem);
 }
