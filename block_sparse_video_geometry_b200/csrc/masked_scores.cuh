@@ -43,7 +43,8 @@ struct ScoreTerms {
 // the column, one operation a score. Distance of column u: |d0 + dir u|, dir = 1 or -1.
 // 2 x 1,111 queries over 5,003 keys, 24 heads, cap and bias, forward: 393 us with both
 // general forms in the exponential unit, 350 us so (300 us with 128-row blocks, 249 us with
-// each pair's polynomial next to its exponentials, which keeps both pipes at work).
+// each pair's polynomial next to its exponentials, which keeps both pipes at work; 205 us
+// with blocks that start and end faster).
 
 // Largest |raw score| of 32 columns (a cap's polynomial holds up to ScoreTerms::limit).
 template <bool kCap>

@@ -5,17 +5,20 @@
 // l = sum 2^(x_j - m), O = sum 2^(x_j - m) v_j; out = O / l, lse = ln2 (m + log2 l).
 // Partial results over parts of the key axis join by their lse.
 //
-// Bound: tensor pipe (4 * 128 FLOP per visible pair) next to the exponentials
-// (one per pair; two more operations of that unit with a cap); one query over a
-// long cache: HBM (k and v read once).
+// Bound: tensor pipe (4 * 128 FLOP per visible pair) next to the exponentials (one
+// per pair; a cap and a bias cost seven more FMA operations); one query over a long
+// cache: HBM (k and v read once). Measured: 8192 x 8192, 24 heads 820 us (1010
+// TFLOP/s; 938 us back to back under the power cap), one query over 4 x 33,001 keys
+// 102 us (81% of the copy rate), 2 x 1,111 queries over 5,003 keys with cap and bias
+// 205 us.
 //
 // Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks the
 // key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
 // 32 KB stages; one warp issues the products, the two tiles in turn; two groups of
 // four warps run the softmax, a thread per row. Scores come in two buffers of 64
 // keys per query tile; P (bf16, the A operand of O += P V) overwrites its scores
-// in TMEM, and the next scores follow behind that product. The softmax's reference is raised, and O rescaled in TMEM,
-// only when a row's sum of P in a tile passes 2^32.
+// in TMEM, and the next scores follow behind that product. The softmax's reference
+// is raised, and O rescaled in TMEM, only when a row's sum of P in a tile passes 2^32.
 // Few rows: blocks of 128 rows, whose two slots take the key tiles in turn with the
 // same queries and join their results in shared memory. Few queries (a new token
 // over a cache): the heads that share a key head are packed into one tile, and the
@@ -574,8 +577,8 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         tc_fence_after();
         // A row that sees none of the half by order or by the tile's document waits for
         // its reference; a warp of such rows has P = 0. (Blocks across two documents had
-        // their second rows' references sought at every tile of the first: 150 us
-        // for 40 tiles.)
+        // their second rows' references sought at every tile of the first: 146 us
+        // for 40 tiles, so 96.)
         const bool none = lim_t < k0 + 64 * hb;
         if (__all_sync(0xffffffffu, none)) {
           uint32_t zero[16];
