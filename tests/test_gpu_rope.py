@@ -221,3 +221,25 @@ def test_layout_positions(cuda_ok, cond, grid, after):
     pos = torch.empty((at, 3), dtype=torch.int32, device="cuda")
     vsa.rope_positions(vsa.Layout(segs, at), pos, origin=(100, -3, 7))
     assert pos.tolist() == [list(p) for p in want]
+
+
+@pytest.mark.parametrize("dims", [(34, 30, 30), (16, 24, 8), (44, 42, 42), (16, 56, 56)], ids=lambda d: "%d-%d-%d" % d)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_halves_in_place_at_every_alignment(cuda_ok, dims, dtype):
+    """Halves whose partners lie at multiples of four channels or not, in place, with infinities and NaN behind the
+    rotated channels and rows of views with space between them."""
+    import torch
+    end = sum(dims)
+    wide = draw((2, 83, 5, 160), dtype, 21)
+    x = wide[:, :, 1:4, :128]
+    x[..., end:] = float("inf")
+    x[..., end + 1::3] = float("nan")
+    pos = torch.arange(83, device="cuda", dtype=torch.int32)[:, None].repeat(1, 3) * 77
+    want = reference(x, pos, dims, vsa.ROPE_HALVES)
+    before = wide.clone()
+    vsa.rope_fwd(vsa.make_rope(dims, pairing=vsa.ROPE_HALVES), pos, x, None, x, None)
+    check(x[..., :end], *(t[..., :end] for t in want))
+    tail, old = x[..., end:].float(), before[:, :, 1:4, end:128].float()
+    assert torch.equal(tail.isnan(), old.isnan()) and torch.equal(tail.isinf(), old.isinf())
+    assert torch.equal(wide[..., 128:], before[..., 128:]) and torch.equal(wide[:, :, 0], before[:, :, 0])
+    assert torch.equal(wide[:, :, 4], before[:, :, 4])
