@@ -483,7 +483,7 @@ def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
         if len(shape) != 4 or shape[0] != B or shape[1] != S or shape[3] != HEAD_DIM or k_out.shape != shape:
             raise ValueError("k and its output must be [B, S, H, 128] with q's B and S")
     shape, strides = pos.shape, pos.stride()
-    if pos.dtype != torch.int32 or shape not in ((S, 3), (B, S, 3)) or (S > 1 and strides[-2:] != (3, 1)):
+    if pos.dtype != torch.int32 or shape not in ((S, 3), (B, S, 3)) or strides[-1] != 1 or (S > 1 and strides[-2] != 3):
         raise ValueError("pos must be int32 [S, 3] or [B, S, 3], contiguous in its last two dimensions")
     _run(name, (q, pos, k, q_out, k_out), ctypes.byref(rope), B, S, pos.data_ptr(),
          strides[0] if len(strides) == 3 else 0, _view(q), None if k is None else _view(k), _view(q_out),

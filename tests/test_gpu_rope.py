@@ -243,3 +243,17 @@ def test_halves_in_place_at_every_alignment(cuda_ok, dims, dtype):
     assert torch.equal(tail.isnan(), old.isnan()) and torch.equal(tail.isinf(), old.isinf())
     assert torch.equal(wide[..., 128:], before[..., 128:]) and torch.equal(wide[:, :, 0], before[:, :, 0])
     assert torch.equal(wide[:, :, 4], before[:, :, 4])
+
+
+@pytest.mark.parametrize("pairing", [vsa.ROPE_ADJACENT, vsa.ROPE_HALVES])
+def test_one_token_of_a_table_of_positions(cuda_ok, pairing):
+    """A streaming step takes its token's row out of a longer table, shared or of each batch entry."""
+    import torch
+    dims = (44, 42, 42)
+    rope = vsa.make_rope(dims, pairing=pairing)
+    table = torch.randint(0, 5000, (3, 30, 3), device="cuda").to(torch.int32)
+    q = draw((3, 1, 5, 128), "bf16", 41)
+    for pos in (table[0, 17:18], table[:, 17:18], table[0, 17].expand(3, 1, 3)):
+        out = torch.full_like(q, float("nan"))
+        vsa.rope_fwd(rope, pos, q, None, out, None)
+        check(out, *reference(q, pos, dims, pairing))

@@ -189,3 +189,28 @@ def test_masked_attention_binding_refusals():
     attn = vsa.MaskedAttention(mask, 1, 8, 8, 4, 2)
     with pytest.raises(ValueError, match="made for"):
         attn.forward(q, k, k)
+
+
+@pytest.mark.parametrize("name", ["rope_fwd", "rope_bwd"])
+def test_positions_at_foreign_strides_are_refused(name):
+    """One token's positions read at strides that the tensor does not have would be other tokens' (or lie behind it):
+    refused like those of several tokens. Views whose last two dimensions are contiguous reach the device check."""
+    import torch
+    call = getattr(vsa, name)
+    table = torch.arange(3 * 10, dtype=torch.int32).view(3, 10)          # axis-major
+    tables = table.expand(2, 3, 10).contiguous()
+    wide = torch.zeros((5, 6), dtype=torch.int32)
+    x = lambda B, S: torch.zeros((B, S, 2, 128))                          # noqa: E731
+    for pos, B in ((table[:, 4:5].t(), 1), (table[0, 4:5].expand(1, 3), 1), (wide[:1, ::2], 1),
+                   (tables[:, :, 4:5].transpose(1, 2), 2), (tables[:1, :, 4:5].transpose(1, 2), 1),
+                   (table[0, 4:5].expand(2, 1, 3), 2)):
+        with pytest.raises(ValueError, match="pos must"):
+            call(vsa.make_rope(), pos, x(B, 1), None, x(B, 1), None)
+    for pos, B, S in ((table.t(), 1, 10), (wide[:4, :3], 1, 4), (tables.transpose(1, 2), 2, 10)):
+        with pytest.raises(ValueError, match="pos must"):
+            call(vsa.make_rope(), pos, x(B, S), None, x(B, S), None)
+    rows = torch.zeros((2, 10, 3), dtype=torch.int32)
+    for pos, B, S in ((rows[0, 4:5], 1, 1), (rows[:, 4:5], 2, 1), (rows[:1, 4:5], 1, 1), (rows[0, 4].expand(2, 1, 3), 2, 1),
+                      (wide[2:3, :3], 1, 1), (wide[2:3, 1:4].t().t(), 1, 1), (rows[:, 2:9], 2, 7), (rows[:, :0], 2, 0)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(vsa.make_rope(), pos, x(B, S), None, x(B, S), None)
