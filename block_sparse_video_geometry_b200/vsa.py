@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library. torch tensors are used as device buffers and torch streams as CUDA
-streams. The library is loaded on first use; if it is missing the call raises,
-there is no fallback path.
+streams: `stream` is a torch stream or a CUDA handle (0: the legacy default
+stream), None torch's current stream, so that a call stands in order with the
+torch operations around it. The library is loaded on first use; if it is missing
+the call raises, there is no fallback path.
 """
 
 from __future__ import annotations
@@ -168,9 +170,16 @@ def make_params(mode: int = SELECT_TOPK, keep: float = 0.1, tau: float = 1.0,
     return Params(mode, keep, tau, sink, scale, coarse, extra_tokens)
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, index=None) -> int:
+    """CUDA stream of a call; None: torch's current stream of device `index` (of the current device)."""
     if stream is None:
-        return 0
+        import torch
+        if index is None:
+            if not torch.cuda.is_initialized():
+                return 0             # nothing but the default stream yet
+            index = torch.cuda.current_device()
+        # the handle alone: torch.cuda.current_stream makes an object of it, 2 us of a call of 10
+        return torch._C._cuda_getCurrentRawStream(index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream        # torch.cuda.Stream
@@ -435,8 +444,9 @@ def _view(t) -> bytes:
     raise ValueError("tensors must have 2, 3 or 4 dimensions")
 
 
-def _run(name, tensors, *args) -> None:
-    """Calls a library function with the tensors' device current; they must share one CUDA device."""
+def _run(name, tensors, stream, *args) -> None:
+    """Calls a library function with the tensors' device current and the stream as last argument; they must share
+    one CUDA device."""
     import torch
     index = tensors[0].get_device()
     if index < 0:
@@ -444,12 +454,12 @@ def _run(name, tensors, *args) -> None:
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("tensors must be on one device, got %s and %s" % (tensors[0].device, t.device))
-    fn = getattr(lib(), name)
+    fn, handle = getattr(lib(), name), _stream_handle(stream, index)
     if index == torch.cuda.current_device():
-        status = fn(*args)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = fn(*args)
+            status = fn(*args, handle)
     if status != OK:
         raise VSAError(status, name)
 
@@ -467,7 +477,7 @@ def rope_positions(layout: Layout, pos, origin=(0, 0, 0), stream=None) -> None:
     import torch
     if pos.dtype != torch.int32 or tuple(pos.shape) != (layout.info.seq_len, 3) or not pos.is_contiguous():
         raise ValueError("pos must be a contiguous int32 [seq_len, 3] tensor")
-    _run("vsa_rope_positions", (pos,), layout.handle, *origin, pos.data_ptr(), _stream_handle(stream))
+    _run("vsa_rope_positions", (pos,), stream, layout.handle, *origin, pos.data_ptr())
 
 
 def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
@@ -485,9 +495,9 @@ def _rope_call(name, rope, pos, q, k, q_out, k_out, stream):
     shape, strides = pos.shape, pos.stride()
     if pos.dtype != torch.int32 or shape not in ((S, 3), (B, S, 3)) or strides[-1] != 1 or (S > 1 and strides[-2] != 3):
         raise ValueError("pos must be int32 [S, 3] or [B, S, 3], contiguous in its last two dimensions")
-    _run(name, (q, pos, k, q_out, k_out), ctypes.byref(rope), B, S, pos.data_ptr(),
+    _run(name, (q, pos, k, q_out, k_out), stream, ctypes.byref(rope), B, S, pos.data_ptr(),
          strides[0] if len(strides) == 3 else 0, _view(q), None if k is None else _view(k), _view(q_out),
-         None if k is None else _view(k_out), _stream_handle(stream))
+         None if k is None else _view(k_out))
 
 
 def rope_fwd(rope: Rope, pos, q, k, q_out, k_out, stream=None) -> None:
@@ -530,9 +540,9 @@ def layer_norm_fwd(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have one type")
     f32 = (torch.float32,)
-    _run("vsa_layer_norm_fwd", (x, weight, bias, y, mean, rstd), B, S, N, _view(x), _vector(weight, N, "weight", types),
-         _vector(bias, N, "bias", types), 0 if wt is None else _dtype(wt), eps, _view(y),
-         _vector(mean, B * S * H, "mean", f32), _vector(rstd, B * S * H, "rstd", f32), _stream_handle(stream))
+    _run("vsa_layer_norm_fwd", (x, weight, bias, y, mean, rstd), stream, B, S, N, _view(x),
+         _vector(weight, N, "weight", types), _vector(bias, N, "bias", types), 0 if wt is None else _dtype(wt), eps,
+         _view(y), _vector(mean, B * S * H, "mean", f32), _vector(rstd, B * S * H, "rstd", f32))
 
 
 def layer_norm_bwd_workspace_size(x) -> int:
@@ -551,11 +561,11 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, str
     if dy.shape != x.shape or dx.shape != x.shape:
         raise ValueError("dy and dx must have x's shape")
     f32 = (torch.float32,)
-    _run("vsa_layer_norm_bwd", (x, dy, weight, mean, rstd, dx, dweight, dbias, workspace), B, S, N, _view(dy), _view(x),
-         _vector(weight, N, "weight", (x.dtype, torch.float32)), 0 if weight is None else _dtype(weight),
+    _run("vsa_layer_norm_bwd", (x, dy, weight, mean, rstd, dx, dweight, dbias, workspace), stream, B, S, N, _view(dy),
+         _view(x), _vector(weight, N, "weight", (x.dtype, torch.float32)), 0 if weight is None else _dtype(weight),
          _vector(mean, B * S * H, "mean", f32), _vector(rstd, B * S * H, "rstd", f32), _view(dx),
          _vector(dweight, N, "dweight", f32), _vector(dbias, N, "dbias", f32), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), _stream_handle(stream))
+         workspace.numel() * workspace.element_size())
 
 
 def make_mask(causal: bool = False, softcap: float = 0.0, scale: float = 0.0, documents: bool = False) -> Mask:
@@ -603,10 +613,10 @@ def masked_attn_fwd(mask: Mask, q, k, v, out, lse, workspace, doc_q=None, doc_k=
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
-    _run("vsa_masked_attn_fwd", (q, k, v, out, lse, workspace, doc_q, doc_k, prefix, slopes), ctypes.byref(mask),
-         ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
+    _run("vsa_masked_attn_fwd", (q, k, v, out, lse, workspace, doc_q, doc_k, prefix, slopes), stream,
+         ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
          _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), _stream_handle(stream))
+         workspace.numel() * workspace.element_size())
 
 
 def masked_attn_bwd_workspace_size(mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int) -> int:
@@ -628,14 +638,16 @@ def masked_attn_bwd(mask: Mask, q, k, v, out, lse, dout, dq, dk, dv, workspace, 
         raise ValueError("dk and dv must have k's shape")
     terms = _mask_terms(mask, B, Sq, Sk, Hq, doc_q, doc_k, prefix, slopes)
     _run("vsa_masked_attn_bwd", (q, k, v, out, lse, dout, dq, dk, dv, workspace, doc_q, doc_k, prefix, slopes),
-         ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
+         stream, ctypes.byref(mask), ctypes.byref(terms), B, Sq, Sk, _view(q), _view(k), _view(v), _view(out),
          _vector(lse, B * Hq * Sq, "lse", (torch.float32,)), _view(dout), _view(dq), _view(dk), _view(dv),
-         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def masked_attn_status(workspace, stream=None) -> int:
     """Synchronises the stream; the status of the latest masked attention call on `workspace` (OK or ERR_TIMEOUT)."""
-    return lib().vsa_masked_attn_status(workspace.data_ptr(), _stream_handle(stream))
+    import torch
+    with torch.cuda.device(workspace.device):
+        return lib().vsa_masked_attn_status(workspace.data_ptr(), _stream_handle(stream, workspace.get_device()))
 
 
 class MaskedAttention:

@@ -2,6 +2,7 @@
 arguments return a status before any GPU work (the pointers here are never
 followed)."""
 
+import contextlib
 import ctypes
 
 import pytest
@@ -214,3 +215,110 @@ def test_positions_at_foreign_strides_are_refused(name):
                       (wide[2:3, :3], 1, 1), (wide[2:3, 1:4].t().t(), 1, 1), (rows[:, 2:9], 2, 7), (rows[:, :0], 2, 0)):
         with pytest.raises(ValueError, match="CUDA device"):
             call(vsa.make_rope(), pos, x(B, S), None, x(B, S), None)
+
+
+@pytest.fixture
+def fake_cuda(monkeypatch):
+    """Tensors that say they are on cuda:1 while cuda:0 is current, torch streams that are numbers, and a library that
+    notes the stream (its last argument) of each call."""
+    import torch
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    class Fake(torch.Tensor):
+        device = torch.device("cuda", 1)
+        kept = ()
+
+        def get_device(self):
+            return 1
+
+        def record_stream(self, s):
+            self.kept = (*self.kept, s.cuda_stream)
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return lambda *a: setattr(a[-1]._obj, "value", 1024) or vsa.OK
+            return lambda *a: calls.append((name, a[-1], here[-1])) or vsa.OK
+
+    calls, here, memory = [], ["cuda:0"], []
+    current = {None: Stream(70), 0: Stream(70), 1: Stream(71)}
+    state = {"stream": None}
+
+    @contextlib.contextmanager
+    def on_device(index):
+        here.append("cuda:%d" % getattr(index, "index", index))
+        yield
+        here.pop()
+
+    @contextlib.contextmanager
+    def on_stream(s):
+        before, state["stream"] = state["stream"], s
+        yield
+        state["stream"] = before
+
+    def current_stream(device=None):
+        return state["stream"] or current[getattr(device, "index", device)]
+
+    make = torch.empty
+
+    def empty(shape, dtype=None, device=None):
+        memory.append(current_stream(device).cuda_stream)
+        return make(shape, dtype=dtype).as_subclass(Fake)
+
+    for name, x in (("current_device", lambda: 0), ("current_stream", current_stream), ("is_initialized", lambda: True),
+                    ("device", on_device), ("stream", on_stream), ("ExternalStream", Stream),
+                    ("default_stream", lambda device=None: Stream(0))):
+        monkeypatch.setattr(torch.cuda, name, x)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: current_stream(i).cuda_stream)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(vsa, "lib", Library)
+    tensor = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype).as_subclass(Fake)   # noqa: E731
+    return tensor, calls, memory, on_stream, Stream
+
+
+def test_none_is_the_current_stream_of_the_tensors_device(fake_cuda):
+    """Every call stands in order with the torch operations around it: on the current stream of its tensors' device,
+    with that device current; on a given stream otherwise."""
+    import torch
+    tensor, calls, _, on_stream, Stream = fake_cuda
+    q, x, f = tensor(1, 4, 2, 128), tensor(4, 64), tensor(4, dtype=torch.float32)
+    pos, ws = tensor(4, 3, dtype=torch.int32), tensor(1024, dtype=torch.uint8)
+    w = tensor(64, dtype=torch.float32)
+    lse, mask = tensor(1, 2, 4, dtype=torch.float32), vsa.make_mask()
+    attn = vsa.MaskedAttention(mask, 1, 4, 4, 2, 2)
+    layout = type("L", (), {"info": type("I", (), {"seq_len": 4}), "handle": 0})
+    every = [lambda **kw: vsa.rope_positions(layout, pos, **kw),
+             lambda **kw: vsa.rope_fwd(vsa.make_rope(), pos, q, q, q, q, **kw),
+             lambda **kw: vsa.rope_bwd(vsa.make_rope(), pos, q, None, q, None, **kw),
+             lambda **kw: vsa.layer_norm_fwd(x, w, None, 1e-6, x, f, f, **kw),
+             lambda **kw: vsa.layer_norm_bwd(x, x, w, f, f, x, w, w, ws, **kw),
+             lambda **kw: vsa.masked_attn_fwd(mask, q, q, q, q, lse, ws, **kw),
+             lambda **kw: vsa.masked_attn_bwd(mask, q, q, q, q, lse, q, q, q, q, ws, **kw),
+             lambda **kw: vsa.masked_attn_status(ws, **kw),
+             lambda **kw: attn.forward(q, q, q, q, lse, **kw),
+             lambda **kw: attn.backward(q, q, q, q, lse, q, q, q, q, **kw)]
+    for call in every:
+        for kw, side, want in (({}, None, 71), ({}, Stream(5), 5), (dict(stream=Stream(9)), None, 9),
+                               (dict(stream=9), Stream(5), 9), (dict(stream=0), None, 0)):
+            calls.clear()
+            with on_stream(side) if side else contextlib.nullcontext():
+                call(**kw)
+            assert [c[1:] for c in calls] == [(want, "cuda:1")], (calls, kw)
+
+
+def test_older_calls_take_the_current_stream_too(fake_cuda):
+    """The sparse calls beside them, on the same stream without being given one."""
+    import torch
+    tensor, calls, _, on_stream, Stream = fake_cuda
+    q, g, i = tensor(1, 64, 2, 128), tensor(1, 64, 2), tensor(1, 2, 1, 1, dtype=torch.int32)
+    layout = type("L", (), {"handle": 0})
+    for side, want in ((None, 70), (Stream(5), 5)):
+        calls.clear()
+        with on_stream(side) if side else contextlib.nullcontext():
+            vsa.coarse_select(layout, vsa.make_params(), q, q, q, i, i, g, g)
+            vsa.coarse_select_status(g)
+        assert [c[1] for c in calls] == [want, want]
+    assert vsa._stream_handle(0) == 0
