@@ -650,53 +650,84 @@ def masked_attn_status(workspace, stream=None) -> int:
         return lib().vsa_masked_attn_status(workspace.data_ptr(), _stream_handle(stream, workspace.get_device()))
 
 
+def _torch_stream(handle, device):
+    """The torch stream of a CUDA handle."""
+    import torch
+    here = torch.cuda.current_stream(device)
+    if handle == here.cuda_stream:
+        return here
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype, device, handle):
+    """A tensor that a call on the stream `handle` writes: out of that stream's memory, which nothing queued elsewhere
+    still uses, and kept while the current stream, where the caller goes on with it, still reads it."""
+    import torch
+    if handle == _stream_handle(None, device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(handle, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 class MaskedAttention:
     """Dense attention of one shape and mask with its workspaces (allocated by the first call that needs them, so
     run one call before a capture). Calls of one object share them: for calls on two streams, or graphs that may run
-    at once, make one object each."""
+    at once, make one object each. Outputs that a call allocates are written on its `stream`: a caller that reads them
+    on another one waits for it, as for any torch operation on a side stream."""
 
     def __init__(self, mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int, device="cuda"):
-        self.shape, self.device = (B, Sq, Sk, Hq, Hk), device
+        import torch
+        self.shape, self.device, self._made = (B, Sq, Sk, Hq, Hk), device, torch.device(device)
         self.masks = [Mask(mask.mode, d, mask.scale, mask.softcap) for d in (0, 1)]
         for m in self.masks:
             masked_attn_workspace_size(m, *self.shape)       # refuses a shape or mask at once
         self.ws_fwd, self.ws_bwd = {}, {}      # by whether documents are given
+        self._kept_for = {}                    # id of a workspace -> handles of the streams that it is kept for
 
-    def _workspace(self, held, size, documents):
-        import torch
-        if documents not in held:
-            held[documents] = torch.empty(size(self.masks[documents], *self.shape), dtype=torch.uint8, device=self.device)
-        return held[documents]
-
-    def _own_shape(self, q, k, v):
+    def _begin(self, q, k, v, stream) -> int:
+        """Checks a call's tensors; the handle of its stream."""
         if _attn_shapes(q, k, v) != self.shape:
             raise ValueError("made for B, Sq, Sk, Hq, Hk = %s, called with %s" % (self.shape, _attn_shapes(q, k, v)))
+        if self._made.type != q.device.type or self._made.index not in (None, q.device.index):
+            raise ValueError("made for device %s, called with tensors on %s" % (self.device, q.device))
+        return _stream_handle(stream, q.device.index)
+
+    def _workspace(self, held, size, documents, device, handle):
+        import torch
+        ws = held.get(documents)
+        if ws is None:
+            ws = held[documents] = _empty(size(self.masks[documents], *self.shape), torch.uint8, device, handle)
+            self._kept_for[id(ws)] = {handle}
+        elif handle not in self._kept_for[id(ws)]:        # its memory outlives the object while that stream needs it
+            ws.record_stream(_torch_stream(handle, device))
+            self._kept_for[id(ws)].add(handle)
+        return ws
 
     def forward(self, q, k, v, out=None, lse=None, doc_q=None, doc_k=None, prefix=None, slopes=None, stream=None):
         """masked_attn_fwd; returns (out, lse)."""
         import torch
-        self._own_shape(q, k, v)
+        handle = self._begin(q, k, v, stream)
         B, Sq, _, Hq, _ = self.shape
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
         d = int(doc_q is not None)
-        masked_attn_fwd(self.masks[d], q, k, v, out, lse, self._workspace(self.ws_fwd, masked_attn_workspace_size, d),
-                        doc_q, doc_k, prefix, slopes, stream)
+        ws = self._workspace(self.ws_fwd, masked_attn_workspace_size, d, q.device, handle)
+        if out is None:
+            out = _empty(q.shape, q.dtype, q.device, handle)
+        if lse is None:
+            lse = _empty((B, Hq, Sq), torch.float32, q.device, handle)
+        masked_attn_fwd(self.masks[d], q, k, v, out, lse, ws, doc_q, doc_k, prefix, slopes, handle)
         return out, lse
 
     def backward(self, q, k, v, out, lse, dout, dq=None, dk=None, dv=None, doc_q=None, doc_k=None, prefix=None,
                  slopes=None, stream=None):
         """masked_attn_bwd; returns (dq, dk, dv)."""
-        import torch
-        self._own_shape(q, k, v)
-        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if g is None else g
-                      for g, x in ((dq, q), (dk, k), (dv, v)))
+        handle = self._begin(q, k, v, stream)
         d = int(doc_q is not None)
-        masked_attn_bwd(self.masks[d], q, k, v, out, lse, dout, dq, dk, dv,
-                        self._workspace(self.ws_bwd, masked_attn_bwd_workspace_size, d), doc_q, doc_k, prefix, slopes,
-                        stream)
+        ws = self._workspace(self.ws_bwd, masked_attn_bwd_workspace_size, d, q.device, handle)
+        dq, dk, dv = (_empty(x.shape, x.dtype, x.device, handle) if g is None else g
+                      for g, x in ((dq, q), (dk, k), (dv, v)))
+        masked_attn_bwd(self.masks[d], q, k, v, out, lse, dout, dq, dk, dv, ws, doc_q, doc_k, prefix, slopes, handle)
         return dq, dk, dv
 
 

@@ -1,5 +1,5 @@
 """The operators on streams: in order with the torch operations of the current
-stream."""
+stream, and memory that their calls allocate on another one."""
 
 import pytest
 
@@ -86,3 +86,57 @@ def test_calls_are_captured_on_the_current_stream(cuda_ok):
     want = M.run(q, k, v, causal=True, dout=dout)
     assert all(torch.equal(a, b) for a, b in zip((out, lse, *grads), want))
     del graph
+
+
+def test_allocating_calls_on_another_stream(cuda_ok):
+    """Memory that was freed on the current stream, whose queued work still reads it, is not what a call on another
+    stream writes; nor does that stream's next call get the outputs that the current stream still reads."""
+    import torch
+    shape = (1, 300, 300, 4, 2)
+    q, k, v, dout = M.tensors(*shape, seed=53)
+    want = M.run(q, k, v, causal=True, dout=dout)
+    side = torch.cuda.Stream()
+    attn = vsa.MaskedAttention(vsa.make_mask(causal=True), *shape)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        pending = [torch.full_like(t, 7) for t in want for _ in range(4)]
+        torch.cuda._sleep(DELAY)
+        seen = [t.clone() for t in pending]
+        del pending                                                  # free on the current stream, read late
+        out, lse = attn.forward(q, k, v, stream=side)
+        grads = attn.backward(q, k, v, out, lse, dout, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(DELAY)
+        mine = [t.clone() for t in (out, lse, *grads)]
+        del out, lse, grads                                          # read late by the current stream
+        attn.forward(k.repeat(1, 1, 2, 1), k, k, stream=side)        # other outputs of the same sizes
+        torch.cuda.synchronize()
+        assert all(bool((t == 7).all()) for t in seen)
+        assert all(torch.equal(a, b) for a, b in zip(mine, want))
+
+
+def test_one_workspace_on_several_streams(cuda_ok):
+    """An object used on one stream after another, each waiting for the one before, and dropped while the last still
+    runs."""
+    import torch
+    shape = (1, 300, 300, 4, 2)
+    q, k, v, dout = M.tensors(*shape, seed=54)
+    want = M.run(q, k, v, causal=True, dout=dout)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        attn = vsa.MaskedAttention(vsa.make_mask(causal=True), *shape)
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i:
+                    s.wait_stream(streams[i - 1])
+                torch.cuda._sleep(DELAY // 4)
+                out, lse = attn.forward(q, k, v)
+                grads = attn.backward(q, k, v, out, lse, dout)
+        sizes = [ws.numel() for ws in (*attn.ws_fwd.values(), *attn.ws_bwd.values())]
+        del attn
+        with torch.cuda.stream(streams[0]):                          # whose memory the workspaces were
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((out, lse, *grads), want))
+        del junk

@@ -322,3 +322,25 @@ def test_older_calls_take_the_current_stream_too(fake_cuda):
             vsa.coarse_select_status(g)
         assert [c[1] for c in calls] == [want, want]
     assert vsa._stream_handle(0) == 0
+
+
+def test_tensors_that_a_call_allocates_belong_to_its_stream(fake_cuda):
+    """Outputs and workspaces of a call on a side stream come out of that stream's memory and stay while the caller's
+    stream uses them; a workspace stays for every stream that has used it."""
+    import torch
+    tensor, calls, memory, on_stream, Stream = fake_cuda
+    q, lse = tensor(1, 4, 2, 128), tensor(1, 2, 4, dtype=torch.float32)
+    attn = vsa.MaskedAttention(vsa.make_mask(), 1, 4, 4, 2, 2)
+    outs = attn.forward(q, q, q, stream=Stream(9)) + attn.backward(q, q, q, q, lse, q, stream=Stream(9))
+    assert memory == [9] * 7 and all(t.kept == (71,) for t in outs)          # five outputs, two workspaces
+    memory.clear()
+    ws = attn.ws_fwd[0]
+    attn.forward(q, q, q, q, lse, stream=9)
+    attn.forward(q, q, q, q, lse)
+    attn.forward(q, q, q, q, lse)
+    assert not memory and ws.kept == (71, 71)              # as allocated for another stream, and once as used on this
+    with on_stream(Stream(5)):
+        out, _ = attn.forward(q, q, q)
+    assert memory == [5, 5] and out.kept == () and ws.kept == (71, 71, 5)
+    with pytest.raises(ValueError, match="made for device"):
+        vsa.MaskedAttention(vsa.make_mask(), 1, 4, 4, 2, 2, device="cuda:0").forward(q, q, q)
