@@ -558,7 +558,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
 
     float m = -INFINITY, l = 0.0f;
-    bool ok = true;
+    bool ok = true, fresh = true;              // fresh: no half tile so far had a row that sees some of it
     const int step = one ? 2 : 1;
     int i = 0;
     for (int j = one ? t : 0; j < n; j += step, ++i) {
@@ -710,7 +710,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             }
           }
         };
-        // No row of the warp has a reference yet: the scores are finished once, back into
+        // The first half tile that a row of the warp sees: the scores are finished once, back into
         // their columns, and their exact maximum is the reference. (O and l are zero, or
         // NaN, so nothing is rescaled.) Without cap and bias, whose scores are quickly
         // finished twice, the form costs more in the main loop than it saves (dense 8192
@@ -757,7 +757,12 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           return s0 + s1;
         };
         float psum = INFINITY;
-        const bool first = __all_sync(0xffffffffu, m == -INFINITY), begun = (kCap || kBias) && first;
+        // With cap or bias a row's bits depend on which of the forms it takes: that goes by
+        // order and documents alone (`fresh`), not by whether another row of the warp has met
+        // nothing but NaN, in a key that this row may not see.
+        const bool first = kCap || kBias ? fresh : __all_sync(0xffffffffu, m == -INFINITY);
+        const bool begun = (kCap || kBias) && first;
+        fresh = false;
         if (begun) {
           psum = begin();
         } else if constexpr (kCap) {

@@ -555,3 +555,28 @@ def test_caps_far_below_the_scores(cuda_ok, cap):
     for name, got in (("lse", lse), ("out", out), ("dv", dv)):
         within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
     assert dq.isfinite().all() and dk.isfinite().all()
+
+
+def later_keys(Sq, Sk, H, cap, bias, at):
+    """A key that only later queries see reaches no earlier one, whatever it holds: the same bits."""
+    import torch
+    q, k, v, dout = tensors(1, Sq, Sk, H, H, seed=41)
+    terms = {"slopes": slopes_of(H)} if bias else {}
+    want = run(q, k, v, causal=True, cap=cap, dout=dout, **terms)
+    for j in at:
+        for loud in (float("nan"), float("inf"), 1e6):
+            k2, v2 = k.clone(), v.clone()
+            k2[:, j] = loud
+            v2[:, j, :, 9] = float("inf")
+            got = run(q, k2, v2, causal=True, cap=cap, dout=dout, **terms)
+            before = max(0, j - (Sk - Sq))                   # queries that do not see it
+            assert torch.equal(got[0][:, :before], want[0][:, :before]), ("out", j, loud)
+            assert torch.equal(got[1][..., :before], want[1][..., :before]), ("lse", j, loud)
+            assert torch.equal(got[2][:, :before], want[2][:, :before]), ("dq", j, loud)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_first_visible_key_of_a_warps_last_row(cuda_ok, bias):
+    """Keys at multiples of 64 that only the last row of 32 sees in their half of a tile: the others of the warp meet
+    their own first keys in the half before, where that row has found a maximum or not."""
+    later_keys(700, 765, 8, 0.0, bias, range(128, 765, 64))
