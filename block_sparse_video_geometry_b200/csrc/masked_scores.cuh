@@ -35,9 +35,9 @@ struct ScoreTerms {
 };
 
 // tanh: 1 - 2 / (1 + e^(2y)) takes two operations of the exponential unit per
-// score, which then bounds the kernels. Where all of a warp's scores have |y| <= 0.6
-// (a cap well above the scores, as caps are), tanh(y) / y is a polynomial in y^2 on
-// the FMA pipe: degree 4, least squares with weights driven to equal extrema, relative
+// score, which then bounds the kernels, and is off by a part of 1, not of the score. For
+// |y| <= 0.6 (a cap well above the scores, as caps are) tanh(y) / y is a polynomial in y^2
+// on the FMA pipe: degree 4, least squares with weights driven to equal extrema, relative
 // error below 2^-23; five operations a score.
 // Bias: where the columns lie on one side of every row of the warp it is linear in
 // the column, one operation a score. Distance of column u: |d0 + dir u|, dir = 1 or -1.
@@ -95,22 +95,26 @@ struct PairArgs {
   }
 };
 
+// tanh(y) from e = 2 log2(e) y.
+__device__ __forceinline__ float tanh_of(float e) { return fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(e)), 1.0f); }
+
 // Raw scores x (sums of products) -> their log2 values minus a reference (`ref`
 // gives minus the reference for a pair of columns). With a cap t receives
-// tanh(score / cap). kBoth: the polynomial where the columns lie on both sides of the
-// rows too. That is one more form in the code: faster in the forward pass, whose blocks
-// start with such tiles; slower in the backward pass, which has few registers (4096 x 24
-// heads 544 -> 636 us) and takes it for caps above kFarCap only: the general form of tanh
-// is off by a part of 1, not of the score, and would lose the scores under a cap of 10^6.
-constexpr float kFarCap = 128.0f;
-template <bool kCap, bool kBias, bool kBoth, class Ref>
+// tanh(score / cap). What a score becomes does not depend on the scores beside it, which
+// other rows see or none: where some score of the warp lies beyond the polynomial, its
+// tanh comes from the general form and every other one's by the polynomial's own steps.
+// (One form for the whole warp: under a cap of 10^6 a hidden score of 10^6 left the visible
+// ones beside it off by 0.1. 4096 causal tokens x 24 heads with a bias, forward and backward,
+// under a cap of 3: 854 us then, 1005 us now; of 50, which no score reaches, 656 and 678 us.)
+template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const ScoreTerms& s, float d0, float dir,
                                            Ref ref) {
-  const bool poly = !kCap || __all_sync(0xffffffffu, largest<kCap>(x) <= s.limit);
   float k;                      // bias of column u: k (d0 + dir u)
   const bool linear = one_side<kBias>(s, d0, dir, 32.0f, k);
-  if (poly && (kBoth || linear)) {
-    const PairArgs<kCap, kBias> pair(s, linear ? k : 0.0f, d0, dir, 0.0f);
+  const float in_e = 2.0f * kLog2e * s.in, inv = kCap ? 1.0f / s.cap2 : 0.0f;
+  const float kk = linear ? k : 0.0f;        // columns on both sides of the rows: added below
+  if (!kCap || __all_sync(0xffffffffu, largest<kCap>(x) <= s.limit)) {
+    const PairArgs<kCap, kBias> pair(s, kk, d0, dir, 0.0f);
 #pragma unroll
     for (int u = 0; u < 32; u += 2) {
       const uint64_t v = pack_f32x2(x[u], x[u + 1]);
@@ -118,31 +122,29 @@ __device__ __forceinline__ void score_args(float (&x)[32], float (&t)[32], const
       unpack_f32x2(add_f32x2(pair(v, u, q), ref(u)), x[u], x[u + 1]);
       if constexpr (kCap) unpack_f32x2(mul_f32x2(v, q), t[u], t[u + 1]);   // times 1 / cap2 below
     }
-    if (kBoth && kBias && !linear) {
-#pragma unroll
-      for (int u = 0; u < 32; ++u) x[u] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), x[u]);
-    }
     if constexpr (kCap) {
-      const float inv = 1.0f / s.cap2;
 #pragma unroll
       for (int u = 0; u < 32; ++u) t[u] *= inv;
     }
-    return;
-  }
-  const float in_e = 2.0f * kLog2e * s.in;
+  } else if constexpr (kCap) {
 #pragma unroll
-  for (int u = 0; u < 32; u += 2) {
-#pragma unroll
-    for (int i = u; i < u + 2; ++i) {
-      if constexpr (kCap) {
-        t[i] = fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(x[i] * in_e)), 1.0f);
-        x[i] = t[i] * s.cap2;
-      } else {
-        x[i] *= s.c;
-      }
-      if constexpr (kBias) x[i] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(i), d0)), x[i]);
+    for (int u = 0; u < 32; ++u) {
+      float r[2];
+      unpack_f32x2(ref(u & ~1), r[0], r[1]);
+      const float v = x[u], z = __fmul_rn(v, v);
+      const float q = fmaf(fmaf(fmaf(fmaf(s.poly[3], z, s.poly[2]), z, s.poly[1]), z, s.poly[0]), z, s.c);
+      float add = kBias ? fmaf(kk, d0, 0.0f) : 0.0f;
+      if constexpr (kBias) add = fmaf(__fmul_rn(kk, dir), static_cast<float>(u), add);
+      const float tanh = tanh_of(v * in_e);
+      const float by_poly = __fmul_rn(__fmul_rn(v, q), inv);
+      const bool near = fabsf(v) <= s.limit;
+      x[u] = __fadd_rn(near ? fmaf(v, q, add) : fmaf(tanh, s.cap2, add), r[u & 1]);
+      t[u] = near ? by_poly : tanh;
     }
-    unpack_f32x2(add_f32x2(pack_f32x2(x[u], x[u + 1]), ref(u)), x[u], x[u + 1]);
+  }
+  if (kBias && !linear) {
+#pragma unroll
+    for (int u = 0; u < 32; ++u) x[u] = fmaf(-s.slope, fabsf(fmaf(dir, static_cast<float>(u), d0)), x[u]);
   }
 }
 

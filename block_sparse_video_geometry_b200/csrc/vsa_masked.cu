@@ -596,7 +596,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         auto finish = [&](int q4, float (&x)[32], float minus_ref) {
           const int col = 32 * q4;
           float tanhs[32];
-          score_args<kCap, kBias, true>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
+          score_args<kCap, kBias>(x, tanhs, terms, static_cast<float>(i_q + p.off - k0 - col), -1.0f,
                                   [&](int) { return pack_f32x2(minus_ref, minus_ref); });
           if (partial) {
             const int lc = lim_t - k0 - col;

@@ -283,10 +283,10 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 // Scores of 32 columns in place -> P against `ref` (minus lse in log2 units, a pair
 // of columns at a time), and into `w` P times the cap's derivative. Without a
 // cap a quarter of the exponentials go to the FMA pipe.
-template <bool kCap, bool kBias, bool kBoth, class Ref>
+template <bool kCap, bool kBias, class Ref>
 __device__ __forceinline__ void probabilities(float (&x)[32], float (&w)[32], const ScoreTerms& s, float d0, float dir,
                                               Ref ref) {
-  score_args<kCap, kBias, kBoth>(x, w, s, d0, dir, ref);          // w: tanh
+  score_args<kCap, kBias>(x, w, s, d0, dir, ref);          // w: tanh
   const uint64_t one = pack_f32x2(1.0f, 1.0f), neg = pack_f32x2(-1.0f, -1.0f);
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
@@ -312,7 +312,7 @@ __device__ __forceinline__ void score_gradients(float (&x)[32], const float (&w)
 }
 
 // ----------------------------------------------------------------- dK and dV
-template <bool kCap, bool kBias, bool kBoth>
+template <bool kCap, bool kBias>
 __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, const CUtensorMap& map_k,
                                           const CUtensorMap& map_v, const CUtensorMap& map_q, const CUtensorMap& map_o,
                                           const CUtensorMap& map_qc, const CUtensorMap& map_oc) {
@@ -489,7 +489,7 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
       tmem_ld32x32f(ts, x);
       tmem_wait_ld32(x);
       const float* lse = sm.lse2[st] + 32 * part;
-      probabilities<kCap, kBias, kBoth>(x, w, terms, static_cast<float>(i0 + p.off - key), 1.0f,
+      probabilities<kCap, kBias>(x, w, terms, static_cast<float>(i0 + p.off - key), 1.0f,
                                  [&](int u) { return *reinterpret_cast<const uint64_t*>(lse + u); });
       if (partial) {
 #pragma unroll
@@ -551,7 +551,7 @@ __device__ __forceinline__ void dkv_block(Smem& sm, int block, const Args& a, co
 }
 
 // ------------------------------------------------------------------------ dQ
-template <bool kCap, bool kBias, bool kBoth>
+template <bool kCap, bool kBias>
 __device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, const CUtensorMap& map_q,
                                          const CUtensorMap& map_o, const CUtensorMap& map_k, const CUtensorMap& map_v,
                                          const CUtensorMap& map_kc) {
@@ -701,7 +701,7 @@ __device__ __forceinline__ void dq_block(Smem& sm, int block, const Args& a, con
       tc_fence_before();                                   // S(j) is in registers: S(j + 1) may replace it
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.s_done[0]));
-      probabilities<kCap, kBias, kBoth>(x, w, terms, static_cast<float>(i_q + p.off - col), -1.0f,
+      probabilities<kCap, kBias>(x, w, terms, static_cast<float>(i_q + p.off - col), -1.0f,
                                  [&](int) { return lse2; });
       if (!(ok = warp_wait(sm, sm.dp_full[0], j & 1, a.err))) break;
       tc_fence_after();
@@ -744,7 +744,7 @@ struct Maps {
   CUtensorMap q, k, v, o, qc, oc, kc;
 };
 
-template <bool kCap, bool kBias, bool kBoth>
+template <bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_bwd_kernel(const __grid_constant__ Args kv, const __grid_constant__ Args q, const __grid_constant__ Maps m,
                   int n_dkv) {
@@ -756,9 +756,9 @@ masked_bwd_kernel(const __grid_constant__ Args kv, const __grid_constant__ Args 
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int block = blockIdx.x;
   if (block < n_dkv)
-    dkv_block<kCap, kBias, kBoth>(sm, block, kv, m.k, m.v, m.q, m.o, m.qc, m.oc);
+    dkv_block<kCap, kBias>(sm, block, kv, m.k, m.v, m.q, m.o, m.qc, m.oc);
   else
-    dq_block<kCap, kBias, kBoth>(sm, block - n_dkv, q, m.q, m.o, m.k, m.v, m.kc);
+    dq_block<kCap, kBias>(sm, block - n_dkv, q, m.q, m.o, m.k, m.v, m.kc);
 }
 
 // dk and dv from the blocks' parts, added in order: one piece of 4 channels a thread.
@@ -865,9 +865,9 @@ Workspace workspace_of(const Problem& p, int splits) {
   return w;
 }
 
-template <bool kCap, bool kBias, bool kBoth>
+template <bool kCap, bool kBias>
 vsa_status launch(const Args& dkv, const Args& dq, const Maps& m, cudaStream_t stream) {
-  const auto kernel = masked_bwd_kernel<kCap, kBias, kBoth>;
+  const auto kernel = masked_bwd_kernel<kCap, kBias>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: shared memory", e);
   const Problem& p = dkv.p;
@@ -1015,9 +1015,8 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
   kv.clean_b = pa.clean_o;
   qq.clean_a = pa.clean_k;
   const bool cap = p.cap > 0.0f, bias = p.slopes != nullptr;
-  if (cap && bias && p.cap > kFarCap) return launch<true, true, true>(kv, qq, m, stream);
-  if (cap) return bias ? launch<true, true, false>(kv, qq, m, stream) : launch<true, false, false>(kv, qq, m, stream);
-  return bias ? launch<false, true, false>(kv, qq, m, stream) : launch<false, false, false>(kv, qq, m, stream);
+  if (cap) return bias ? launch<true, true>(kv, qq, m, stream) : launch<true, false>(kv, qq, m, stream);
+  return bias ? launch<false, true>(kv, qq, m, stream) : launch<false, false>(kv, qq, m, stream);
 }
 
 }  // extern "C"

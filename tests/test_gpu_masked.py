@@ -557,6 +557,27 @@ def test_caps_far_below_the_scores(cuda_ok, cap):
     assert dq.isfinite().all() and dk.isfinite().all()
 
 
+@pytest.mark.parametrize("cap", [3.0, 30.0, 1e6])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("loud", [float("inf"), float("nan"), 3e38, 4e4])
+def test_masked_places_change_nothing_under_a_cap(cuda_ok, cap, bias, loud):
+    """Padding rows that hold infinities, NaN or numbers far beyond the cap: the same bits as with zeros there, in the
+    other rows of their tiles too."""
+    import torch
+    case, clean, terms, pad = with_padding()
+    if bias:
+        terms["slopes"] = slopes_of(case[3])
+    for t in clean:
+        t[pad] = 0
+    want = run(*clean[:3], causal=True, cap=cap, dout=clean[3], **terms)
+    dirty = [t.clone() for t in clean]
+    for t in dirty:
+        t[pad] = torch.where(torch.rand(t[pad].shape, device="cuda") < 0.5, loud, -loud).to(t.dtype)
+    got = run(*dirty[:3], causal=True, cap=cap, dout=dirty[3], **terms)
+    for name, a, b in zip(("out", "lse", "dq", "dk", "dv"), got, want):
+        assert torch.equal(a, b), name
+
+
 def later_keys(Sq, Sk, H, cap, bias, at):
     """A key that only later queries see reaches no earlier one, whatever it holds: the same bits."""
     import torch
@@ -580,3 +601,28 @@ def test_first_visible_key_of_a_warps_last_row(cuda_ok, bias):
     """Keys at multiples of 64 that only the last row of 32 sees in their half of a tile: the others of the warp meet
     their own first keys in the half before, where that row has found a maximum or not."""
     later_keys(700, 765, 8, 0.0, bias, range(128, 765, 64))
+
+
+@pytest.mark.parametrize("cap", [3.0, 30.0, 1e6])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("Sq,Sk", [(1, 500), (40, 500), (333, 500), (200, 265), (700, 765)])
+def test_later_keys_may_hold_anything_under_a_cap(cuda_ok, cap, bias, Sq, Sk):
+    later_keys(Sq, Sk, 4, cap, bias, {Sk - Sq // 2 - 1, 128 if Sk - Sq < 128 else Sk - 1, (Sk - 1) // 64 * 64})
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_scores_beside_others_far_beyond_the_cap(cuda_ok, bias):
+    """Under a cap of 10^6, rows of ordinary scores beside one in sixteen whose scores reach the cap: s - c tanh(s / c)
+    is below 2^-24 |s| for the ordinary ones, so that they keep the bounds of a call without a cap."""
+    import torch
+    case = (1, 300, 300, 2, 1, True, None, 0.0, bias, None)
+    q, k, v, dout = tensors(*case[:5], seed=43)
+    terms = terms_of(case)
+    loud = torch.arange(300, device="cuda") % 16 == 5
+    ref = reference(case, q, k, v, terms, dout)
+    q = torch.where(loud[None, :, None, None], q * 1e6, q)
+    out, lse, dq, dk, dv = run(q, k, v, causal=True, cap=1e6, dout=dout, **terms)
+    assert torch.isfinite(lse).all()
+    within(lse[..., ~loud], ref.lse[..., ~loud], ref.t_lse[..., ~loud], "lse")
+    for name, got in (("out", out), ("dq", dq)):
+        within(got[:, ~loud], getattr(ref, name)[:, ~loud], getattr(ref, "t_" + name)[:, ~loud], name)
