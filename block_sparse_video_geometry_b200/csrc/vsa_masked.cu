@@ -152,10 +152,11 @@ vsa_status check_tensor(const vsa_view* v, int32_t B, int32_t S, int32_t heads, 
 namespace {
 
 // Rows of v with an infinity or NaN, and the tiles' copies without them. One block
-// per (head, tile, batch entry), heads first: neighbours read neighbouring memory.
+// per (head, tile) in x and batch entry, heads first: neighbours read neighbouring memory.
 // HBM bound: v read once.
-__global__ void __launch_bounds__(kTileThreads) scan_kernel(const uint16_t* __restrict__ x, Strides st, int S, Clean c) {
-  const int h = blockIdx.x, tile = blockIdx.y, b = blockIdx.z;
+__global__ void __launch_bounds__(kTileThreads)
+scan_kernel(const uint16_t* __restrict__ x, Strides st, int S, int heads, int n_tiles, Clean c) {
+  const int h = blockIdx.x % heads, tile = blockIdx.x / heads, b = blockIdx.y;
   __shared__ uint32_t bad[4];
   if (threadIdx.x < 4) bad[threadIdx.x] = 0;
   uint4 w[kPieces];
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kTileThreads) scan_kernel(const uint16_t* __re
   __syncthreads();
   find_bad(w, bad);
   __syncthreads();
-  write_clean(c, w, bad, b, h, gridDim.x, tile, gridDim.y, S);
+  write_clean(c, w, bad, b, h, heads, tile, n_tiles, S);
 }
 
 // Smallest and largest document of positions [i0, i0 + n) of a row of ids
@@ -1038,10 +1039,11 @@ template <bool kCap, bool kBias>
 vsa_status launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mvc,
                   cudaStream_t stream) {
   const auto kernel = masked_fwd_kernel<kCap, kBias>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: shared memory", e);
   kernel<<<a.n_blocks * a.units * a.p.B * a.splits, kThreads, sizeof(Smem), stream>>>(a, mk, mv, mvc);
-  return VSA_OK;
+  e = cudaGetLastError();
+  return e == cudaSuccess ? VSA_OK : cuda_fail("vsa_masked_attn_fwd", e);
 }
 
 }  // namespace
@@ -1146,9 +1148,11 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
     a.clean_v = Clean{reinterpret_cast<uint4*>(ws + w.bad), reinterpret_cast<uint16_t*>(ws + w.copy)};
     st = make_map(&mvc, a.clean_v.copy, B, Sk, k->heads);
     if (st != VSA_OK) return st;
-    scan_kernel<<<dim3(k->heads, a.p.nkt, B), kTileThreads, 0, stream>>>(static_cast<const uint16_t*>(v->data), sv, Sk,
-                                                                         a.clean_v);
+    scan_kernel<<<dim3(k->heads * a.p.nkt, B), kTileThreads, 0, stream>>>(static_cast<const uint16_t*>(v->data), sv, Sk,
+                                                                          k->heads, a.p.nkt, a.clean_v);
   }
+  e = cudaGetLastError();                                 // nothing reads marks or lists that nobody wrote
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: lists and scan", e);
   const bool cap = a.p.cap > 0.0f, bias = a.p.slopes != nullptr;
   st = cap ? (bias ? launch<true, true>(a, mk, mv, mvc, stream) : launch<true, false>(a, mk, mv, mvc, stream))
            : (bias ? launch<false, true>(a, mk, mv, mvc, stream) : launch<false, false>(a, mk, mv, mvc, stream));

@@ -44,7 +44,7 @@ namespace {
 // Minus D and minus lse2 of every row, [B][Hq][nqt * 128]; rows past Sq, and rows
 // without visible keys: 0 and -inf, so that P = 0. Where the call masks anything,
 // also the rows of dout, q and k with an infinity or NaN (see Clean). One block per
-// (head of q, then of k; tile; batch entry), heads first: neighbours read
+// (head of q, then of k; tile) in x and batch entry, heads first: neighbours read
 // neighbouring memory. HBM bound: out and dout (and q, k) read once.
 struct PrepArgs {
   const uint16_t *out, *dout, *q, *k;
@@ -67,9 +67,10 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
 }
 
 __global__ void __launch_bounds__(kTileThreads, 2) prepare_kernel(const __grid_constant__ PrepArgs a) {
-  const int tile = blockIdx.y, b = blockIdx.z;
-  const bool key = static_cast<int>(blockIdx.x) >= a.Hq;
-  const int h = key ? blockIdx.x - a.Hq : blockIdx.x;
+  const int heads = a.Hq + (a.masked ? a.Hk : 0), tile = blockIdx.x / heads, b = blockIdx.y;
+  const int head = blockIdx.x % heads;
+  const bool key = head >= a.Hq;
+  const int h = key ? head - a.Hq : head;
   if (tile >= (key ? a.nkt : a.nqt)) return;               // the whole block
   __shared__ uint32_t bad[2][4];
   if (threadIdx.x < 8) (&bad[0][0])[threadIdx.x] = 0;
@@ -873,6 +874,7 @@ vsa_status launch(const Args& dkv, const Args& dq, const Maps& m, cudaStream_t s
   const Problem& p = dkv.p;
   const int n_dkv = p.nkt * p.Hk * p.B * dkv.splits;
   kernel<<<n_dkv + dq.nqt * p.Hq * p.B, kThreads, sizeof(Smem), stream>>>(dkv, dq, m, n_dkv);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd", e);
   if (dkv.splits > 1) {
     const int64_t pieces = static_cast<int64_t>(p.B) * p.Sk * p.Hk * (kHeadDim / 4);
     join_kernel<<<dim3(static_cast<unsigned>((pieces + 255) / 256), 2), 256, 0, stream>>>(dkv);
@@ -972,7 +974,7 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
         (st = make_map(&m.kc, pa.clean_k.copy, B, Sk, p.Hk)) != VSA_OK)
       return st;
   }
-  prepare_kernel<<<dim3(p.Hq + (p.masked ? p.Hk : 0), p.masked ? std::max(nqt, p.nkt) : nqt, B), kTileThreads, 0,
+  prepare_kernel<<<dim3((p.Hq + (p.masked ? p.Hk : 0)) * (p.masked ? std::max(nqt, p.nkt) : nqt), B), kTileThreads, 0,
                    stream>>>(pa);
 
   Args g{};
@@ -1009,6 +1011,8 @@ vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms
     kv.count = ck;
     kv.list = lk;
   }
+  e = cudaGetLastError();                                 // nothing reads sums or lists that nobody wrote
+  if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_bwd: lists and sums", e);
   kv.splits = splits;
   kv.part = splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
   kv.clean_a = pa.clean_q;

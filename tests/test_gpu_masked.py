@@ -626,3 +626,48 @@ def test_scores_beside_others_far_beyond_the_cap(cuda_ok, bias):
     within(lse[..., ~loud], ref.lse[..., ~loud], ref.t_lse[..., ~loud], "lse")
     for name, got in (("out", out), ("dq", dq)):
         within(got[:, ~loud], getattr(ref, name)[:, ~loud], getattr(ref, "t_" + name)[:, ~loud], name)
+
+
+def test_cache_of_more_than_65535_tiles(cuda_ok):
+    """Two queries at the end of a cache of 8,388,900 positions. The bias leaves weight to the last keys only (e^-8000
+    is 0), so that the formula over the last 8,000 is the formula over all; an infinity at the last key, which the
+    first query does not see, is found where its tile lies."""
+    import torch
+    Sk, near = 8388900, 8000
+    g = torch.Generator(device="cuda").manual_seed(61)
+    q, dout = (torch.randn((1, 2, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn((1, Sk, 1, 128), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    slopes = torch.ones(1, device="cuda")
+    attn = vsa.MaskedAttention(vsa.make_mask(causal=True), 1, 2, Sk, 1, 1)
+    out, lse = attn.forward(q, k, v, slopes=slopes)
+    dq, dk, dv = attn.backward(q, k, v, out, lse, dout, slopes=slopes)
+    assert all(vsa.masked_attn_status(ws) == vsa.OK for ws in (*attn.ws_fwd.values(), *attn.ws_bwd.values()))
+    kn, vn = k[:, -near:], v[:, -near:]
+    ref = Reference(q, kn, vn, visible(1, 2, near, True), slopes=slopes, dout=dout)
+    for name, got in (("lse", lse), ("out", out), ("dq", dq), ("dk", dk[:, -near:]), ("dv", dv[:, -near:])):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+    assert not dk[:, :-near].any() and not dv[:, :-near].any()
+    v[:, -1, :, 3] = float("inf")
+    again, lse2 = attn.forward(q, k, v, slopes=slopes)
+    assert torch.equal(again[:, 0], out[:, 0]) and again[:, 1].isnan().all() and torch.equal(lse2[..., 0], lse[..., 0])
+
+
+def test_queries_of_more_than_65535_tiles(cuda_ok):
+    """8,388,900 queries over five keys, without a mask; only the first and last queries have a gradient."""
+    import torch
+    Sq, Sk, ends = 8388900, 5, 300
+    g = torch.Generator(device="cuda").manual_seed(62)
+    q = torch.randn((1, Sq, 1, 128), generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn((1, Sk, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    dout = torch.zeros_like(q)
+    at = torch.cat([torch.arange(ends), torch.arange(Sq - ends, Sq)]).cuda()
+    dout[:, at] = torch.randn((1, 2 * ends, 1, 128), generator=g, device="cuda").bfloat16()
+    attn = vsa.MaskedAttention(vsa.make_mask(), 1, Sq, Sk, 1, 1)
+    out, lse = attn.forward(q, k, v)
+    dq, dk, dv = attn.backward(q, k, v, out, lse, dout)
+    assert all(vsa.masked_attn_status(ws) == vsa.OK for ws in (*attn.ws_fwd.values(), *attn.ws_bwd.values()))
+    ref = Reference(q[:, at], k, v, torch.ones((1, 2 * ends, Sk), dtype=torch.bool, device="cuda"), dout=dout[:, at])
+    for name, got in (("lse", lse[..., at]), ("out", out[:, at]), ("dq", dq[:, at]), ("dk", dk), ("dv", dv)):
+        within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+    dq[:, at] = 0
+    assert not dq.any()
