@@ -671,3 +671,32 @@ def test_queries_of_more_than_65535_tiles(cuda_ok):
         within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
     dq[:, at] = 0
     assert not dq.any()
+
+
+@pytest.mark.parametrize("case", [(2, 2300, 2300, 12, 4, True, (700,), 0.0, False, None),
+                                  (1, 3000, 3000, 24, 24, False, None, 0.0, False, (700, 1500, 90, 600)),
+                                  (2, 2300, 2300, 12, 4, True, None, 20.0, True, None)], ids=ident)
+def test_gradients_over_many_waves_of_blocks(cuda_ok, case):
+    """Several blocks after one another on each SM: equal bits every time, and within the formula's bounds in the
+    first and last heads."""
+    import torch
+    B, Sq, Sk, Hq, Hk, causal, prefix, cap, bias, docs = case
+    q, k, v, dout = tensors(B, Sq, Sk, Hq, Hk, seed=63)
+    terms = terms_of(case)
+    first = run(q, k, v, causal=causal, cap=cap, dout=dout, **terms)
+    attn = vsa.MaskedAttention(vsa.make_mask(causal=causal, softcap=cap), B, Sq, Sk, Hq, Hk)
+    for _ in range(10):
+        out, lse = attn.forward(q, k, v, **terms)
+        grads = attn.backward(q, k, v, out, lse, dout, **terms)
+        assert all(torch.equal(a, b) for a, b in zip((out, lse, *grads), first))
+    n = Hq // Hk
+    for h in (0, Hk - 1):
+        rows = slice(h * n, (h + 1) * n)
+        part = dict(terms, slopes=terms["slopes"][rows]) if bias else terms
+        ref = Reference(q[:, :, rows], k[:, :, h:h + 1], v[:, :, h:h + 1],
+                        visible(B, Sq, Sk, causal, terms.get("prefix"), terms.get("doc_q"), terms.get("doc_k")), cap,
+                        part.get("slopes"), dout=dout[:, :, rows])
+        for name, got in zip(("out", "lse", "dq", "dk", "dv"),
+                             (first[0][:, :, rows], first[1][:, rows], first[2][:, :, rows],
+                              first[3][:, :, h:h + 1], first[4][:, :, h:h + 1])):
+            within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
