@@ -12,7 +12,7 @@ namespace vsa {
 namespace masked {
 
 constexpr int kRows = 128;                  // rows of a query or key tile
-constexpr size_t kHeader = 256;             // status word, count of failed calls
+constexpr size_t kHeader = 256;             // status word
 constexpr uint32_t kTileBytes = 32768;      // 128 rows x 128 bf16: [d half][row][128 B], swizzled
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;

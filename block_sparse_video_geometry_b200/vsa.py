@@ -730,6 +730,15 @@ class MaskedAttention:
         masked_attn_bwd(self.masks[d], q, k, v, out, lse, dout, dq, dk, dv, ws, doc_q, doc_k, prefix, slopes, handle)
         return dq, dk, dv
 
+    def status(self, stream=None) -> int:
+        """Synchronises the stream; OK, or ERR_TIMEOUT where a bounded wait ran out and left the outputs of the latest
+        forward or backward call (with documents or without, each for itself) incomplete."""
+        for ws in (*self.ws_fwd.values(), *self.ws_bwd.values()):
+            status = masked_attn_status(ws, stream)
+            if status != OK:
+                return status
+        return OK
+
 
 def debug_inject_wait_timeout(timeout_ns):
     """Test hook: while timeout_ns > 0, each sparse_attn_fwd runs into a bounded

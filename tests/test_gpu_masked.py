@@ -700,3 +700,21 @@ def test_gradients_over_many_waves_of_blocks(cuda_ok, case):
                              (first[0][:, :, rows], first[1][:, rows], first[2][:, :, rows],
                               first[3][:, :, h:h + 1], first[4][:, :, h:h + 1])):
             within(got, getattr(ref, name), getattr(ref, "t_" + name), name)
+
+
+def test_status_of_the_latest_calls(cuda_ok):
+    """A status word that a call left behind is read through the object (written here by the host), and cleared by the
+    next call on that workspace."""
+    import torch
+    q, k, v, dout = tensors(1, 200, 200, 2, 2, seed=67)
+    attn = vsa.MaskedAttention(vsa.make_mask(), 1, 200, 200, 2, 2)
+    assert attn.status() == vsa.OK
+    out, lse = attn.forward(q, k, v)
+    attn.backward(q, k, v, out, lse, dout)
+    assert attn.status() == vsa.OK
+    for held, again in ((attn.ws_fwd, lambda: attn.forward(q, k, v)),
+                        (attn.ws_bwd, lambda: attn.backward(q, k, v, out, lse, dout))):
+        held[0][:4].view(torch.int32).fill_(vsa.ERR_TIMEOUT)
+        assert attn.status() == vsa.ERR_TIMEOUT
+        again()
+        assert attn.status() == vsa.OK

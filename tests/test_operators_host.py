@@ -344,3 +344,19 @@ def test_tensors_that_a_call_allocates_belong_to_its_stream(fake_cuda):
     assert memory == [5, 5] and out.kept == () and ws.kept == (71, 71, 5)
     with pytest.raises(ValueError, match="made for device"):
         vsa.MaskedAttention(vsa.make_mask(), 1, 4, 4, 2, 2, device="cuda:0").forward(q, q, q)
+
+
+def test_status_of_an_attention_object(fake_cuda, monkeypatch):
+    """The first error among the workspaces of its calls."""
+    tensor, calls, _, _, _ = fake_cuda
+    import torch
+    q, lse = tensor(1, 4, 2, 128), tensor(1, 2, 4, dtype=torch.float32)
+    attn = vsa.MaskedAttention(vsa.make_mask(), 1, 4, 4, 2, 2)
+    assert attn.status() == vsa.OK                         # nothing ran
+    attn.forward(q, q, q, q, lse)
+    attn.backward(q, q, q, q, lse, q, q, q, q)
+    calls.clear()
+    assert attn.status(stream=9) == vsa.OK and calls == [("vsa_masked_attn_status", 9, "cuda:1")] * 2
+    monkeypatch.setattr(vsa, "masked_attn_status",
+                        lambda ws, stream=None: vsa.ERR_TIMEOUT if ws is attn.ws_bwd[0] else vsa.OK)
+    assert attn.status() == vsa.ERR_TIMEOUT
