@@ -722,9 +722,9 @@ int sm_count() {
 
 constexpr int kMaxSms = 160;                        // the workspace is sized for this many
 // Persistent blocks: as many per SM as make about `threads` threads, at most 8.
-int persistent(int64_t rows, const Shape& s, int threads) {
+int persistent(int64_t rows, const Shape& s, int threads, int sms) {
   const int per_sm = std::max(1, std::min(8, threads / s.threads));
-  const int64_t most = static_cast<int64_t>(std::min(sm_count(), kMaxSms)) * per_sm;
+  const int64_t most = static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm;
   return static_cast<int>(std::min<int64_t>((rows + s.rows_per_block - 1) / s.rows_per_block, most));
 }
 
@@ -744,7 +744,7 @@ template <class T, int VEC>
 vsa_status fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
   const char* where = "vsa_layer_norm_fwd";
   const bool wide = s.ept == VEC;                          // of the warp kernels: one vector per lane
-  const int n = persistent(a.R.n, s, s.lanes > 32 ? 960 : (wide ? kFwdBlocks : 2) * kWarpBlock);
+  const int n = persistent(a.R.n, s, s.lanes > 32 ? 960 : (wide ? kFwdBlocks : 2) * kWarpBlock, sm_count());
   if (s.lanes == 16) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 16, kFwdU>, n, s.threads, 0, a, stream);
   if (s.lanes == 32 && wide) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 32, kFwdU>, n, s.threads, 0, a, stream);
   if constexpr (VEC == 1) {
@@ -759,8 +759,8 @@ vsa_status fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
 }
 
 // Blocks of the backward kernel: a partial row each.
-int bwd_blocks(int64_t rows, const Shape& s) {
-  return persistent(rows, s, s.lanes > 32 ? 640 : (s.ept > 8 ? 2 : 4) * kWarpBlock);
+int bwd_blocks(int64_t rows, const Shape& s, int sms) {
+  return persistent(rows, s, s.lanes > 32 ? 640 : (s.ept > 8 ? 2 : 4) * kWarpBlock, sms);
 }
 
 template <class T, class G, int VEC>
@@ -872,8 +872,11 @@ vsa_status vsa_layer_norm_bwd_workspace_size(int32_t B, int64_t S, int32_t heads
   if (!bytes) return VSA_ERR_INVALID_ARG;
   const vsa_status st = check_rows(B, S, heads, width, &R);
   if (st != VSA_OK) return st;
-  // a partial row of dw and db per block: at most 8 blocks per SM
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(R.n, kMaxSms * 8));
+  // a partial row of dw and db per block, of the access (single elements, 4 or 8) with the
+  // most blocks: types and alignment are not at hand
+  int blocks = 1;
+  for (int vec : {1, 4, 8})
+    if (width % vec == 0) blocks = std::max(blocks, bwd_blocks(R.n, shape_of(width, vec, R.n, 1), kMaxSms));
   *bytes = align_up(static_cast<size_t>(blocks) * 2 * width * sizeof(float), 256);
   return VSA_OK;
 }
@@ -927,7 +930,7 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(dy, a.sdy, vec, width) && vec_ok(dx, a.sdx, vec, width);
   const Shape s = shape_of(width, wide ? vec : 1, a.R.n, 1);
-  const int n = bwd_blocks(a.R.n, s);
+  const int n = bwd_blocks(a.R.n, s, sm_count());           // at most those that the workspace was sized for
   const bool g32 = dy->dtype == VSA_F32;
   if (x->dtype == VSA_F32)
     st = wide ? bwd_launch<float, float, 4>(s, a, n, stream) : bwd_launch<float, float, 1>(s, a, n, stream);

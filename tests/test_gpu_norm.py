@@ -312,3 +312,30 @@ def test_same_bits_and_captured_replay(cuda_ok):
     graph.replay()
     torch.cuda.synchronize()
     check_step(x, w, None, dy, (y, mean, rstd, dx, dw, db))
+
+
+@pytest.mark.parametrize("shape", [(17408, 5120), (40, 16384), (3000, 9009), (1, 4096), (2, 300, 24, 128), (5000, 257),
+                                   (700, 1153), (1500, 2048)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shift", [0, 1])
+def test_nothing_is_written_behind_the_workspace(cuda_ok, shape, shift):
+    """Exactly the bytes that were asked for, marked ones behind them, rows aligned or not."""
+    import torch
+    n = 1
+    for s in shape:
+        n *= s
+    flat = torch.randn(n + shift, device="cuda").bfloat16()
+    x = flat[shift:].view(shape)
+    dy = torch.randn(shape, device="cuda")
+    y = torch.empty_like(x)
+    mean, rstd = (torch.empty(shape[:-1], device="cuda") for _ in range(2))
+    vsa.layer_norm_fwd(x, None, None, 1e-6, y, mean, rstd)
+    size = vsa.layer_norm_bwd_workspace_size(x)
+    ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    dx = torch.empty(shape, device="cuda")
+    dw, db = (torch.empty(shape[-1], device="cuda") for _ in range(2))
+    vsa.layer_norm_bwd(dy, x, None, mean, rstd, dx, dw, db, ws[:size])
+    assert bool((ws[size:] == 0x5A).all())
+    ref = Reference(x, None, None, 1e-6)
+    _, _, wdw, tw, wdb, tb = ref.backward(dy)
+    within(dw, wdw, tw, "dweight")
+    within(db, wdb, tb, "dbias")

@@ -360,3 +360,14 @@ def test_status_of_an_attention_object(fake_cuda, monkeypatch):
     monkeypatch.setattr(vsa, "masked_attn_status",
                         lambda ws, stream=None: vsa.ERR_TIMEOUT if ws is attn.ws_bwd[0] else vsa.OK)
     assert attn.status() == vsa.ERR_TIMEOUT
+
+
+@pytest.mark.parametrize("rows,width,blocks", [(17408, 5120, 320), (148, 16384, 148), (100000, 16384, 160), (40, 16384, 40),
+                                               (3693, 1153, 640), (1 << 20, 128, 640), (300, 128, 38), (1, 1, 1),
+                                               (1 << 20, 2048, 800), (100, 2048, 100)])
+def test_layer_norm_workspace_holds_the_blocks_that_run(rows, width, blocks):
+    """A partial row of two sums for each block that can run: on 160 SMs, as many blocks per SM as make 640 threads
+    (long rows) or 1024 (short ones, 8 rows or more a block), and no more blocks than rows."""
+    n = ctypes.c_size_t()
+    assert vsa.lib().vsa_layer_norm_bwd_workspace_size(1, rows, 1, width, ctypes.byref(n)) == vsa.OK
+    assert n.value == (blocks * 2 * width * 4 + 255) // 256 * 256
