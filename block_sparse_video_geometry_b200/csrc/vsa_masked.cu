@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "masked_scores.cuh"
 #include "sm100.cuh"
@@ -331,7 +332,20 @@ __device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t& bar, uint32_t pari
   return __all_sync(0xffffffffu, bounded_wait(sm, bar, parity, err));
 }
 
-template <bool kCap, bool kBias>
+// What the bf16 pair `first` left of p0 and p1, as bf16 again.
+__device__ __forceinline__ uint32_t second_term(uint32_t first, float p0, float p1) {
+  const uint64_t f = pack_f32x2(__uint_as_float(first << 16), __uint_as_float(first & 0xFFFF0000u));
+  unpack_f32x2(fma_f32x2(f, pack_f32x2(-1.0f, -1.0f), pack_f32x2(p0, p1)), p0, p1);
+  return pack_bf16x2(p0, p1);
+}
+
+// kFine: P enters the second product as two bf16 terms, its rounding and what that left
+// (2^-16 of it together), so that the output is off by its own rounding only. One term
+// makes a long sum's relative error 0.0023-0.0026 instead of 0.0017. Taken for up to 128
+// queries, whose blocks wait for HBM: one query over 4 x 33,001 keys 95.7 us with one
+// term, 98.6 with two; 128 queries over 8,000 keys, 4 x 48 heads 181 and 189. Longer calls
+// would pay 2 to 22% (8192 x 24 heads 830 -> 1014 us).
+template <bool kCap, bool kBias, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_vc) {
@@ -343,7 +357,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const Problem& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool one = a.one_tile;
+  const bool one = kFine || a.one_tile;
 
   // block -> (query block, split, unit, batch entry); late query blocks, the
   // longest under a causal mask, first
@@ -524,8 +538,12 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         const uint64_t vd = smem_desc_sw128(smem_u32(sm.kv[st]) + 8192 * hb, 16384, 1024);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(to, ts + 64 * hb + kk * 8, vd + kk * (2048 >> 4), kIdescPV, i > 0 || hb > 0 || kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) {
+            // two terms: the first of 32 keys over 16 of their columns, the second over the others
+            const uint32_t p = ts + 64 * hb + (kFine ? (kk >> 1) * 32 + (kk & 1) * 8 : kk * 8);
+            umma_ts(to, p, vd + kk * (2048 >> 4), kIdescPV, i > 0 || hb > 0 || kk > 0 ? 1u : 0u);
+            if constexpr (kFine) umma_ts(to, p + 16, vd + kk * (2048 >> 4), kIdescPV, 1u);
+          }
           umma_commit(smem_u32(&sm.pv_done[t]));
           if (hb == 1) umma_commit(smem_u32(&sm.empty[st]));
           if (hb == 1 && j + step >= n) umma_commit(smem_u32(&sm.o_full[t]));
@@ -550,7 +568,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     const int g = a.packed ? row / p.Sq : 0;
     const int i_q = min(a.packed ? row - g * p.Sq : row, p.Sq - 1);
     const int h = a.packed ? min(hk * p.group + g, p.Hq - 1) : unit;
-    const int lim = p.limit(b, i_q);
+    const int lim = kFine && !live ? -1 : p.limit(b, i_q);   // few queries: warps without any row skip the softmax
     // smallest limit of the tile's rows: tiles up to there are seen by all of them
     const int lim0 = p.limit(b, a.packed ? 0 : min(tile_row0, p.Sq - 1));
     const int doc = p.documents && live ? p.doc_q[b * p.doc_q_sb + i_q] : -1;
@@ -585,7 +603,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           uint32_t zero[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) zero[u] = 0;
-          for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, zero);
+          for (int q2 = 0; q2 < (kFine ? 4 : 2); ++q2) tmem_st32x16(tb + 16 * q2, zero);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -625,7 +643,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         // exponentials, so that the FMA pipe and the exponential unit run together.
         // A quarter of the exponentials go to the FMA pipe: 868 -> 834 us for 8192 x
         // 24 heads (an eighth 848, three eighths 862); none where the cap fills it.
-        uint32_t w[2][16];
+        uint32_t w[2][16], w2[kFine ? 2 : 1][16];
         const float d0 = static_cast<float>(i_q + p.off - k0 - 64 * hb);
         float k_bias;
         const bool plain = one_side<kBias>(terms, d0, -1.0f, 64.0f, k_bias) && !partial && !flagged;
@@ -641,6 +659,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
             ex2_pair(p0, p1, !kCap && u % 4 == 2);
             ls[u & 1] = add_f32x2(ls[u & 1], pack_f32x2(p0, p1));
             w[q2][u] = pack_bf16x2(p0, p1);
+            if constexpr (kFine) w2[q2][u] = second_term(w[q2][u], p0, p1);
           };
           bool pairwise = plain;
           if constexpr (kCap) {
@@ -740,7 +759,7 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 #pragma unroll 1
           for (int q2 = 0; q2 < 2; ++q2) {                     // P of 32 columns ends up over scores already read
             float x[32];
-            uint32_t y[16];
+            uint32_t y[16], y2[16];
             tmem_ld32x32f(tb + 32 * q2, x);
             tmem_wait_ld32(x);
 #pragma unroll
@@ -750,8 +769,10 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
               ex2_pair(p0, p1, false);
               sum = add_f32x2(sum, pack_f32x2(p0, p1));
               y[u] = pack_bf16x2(p0, p1);
+              if constexpr (kFine) y2[u] = second_term(y[u], p0, p1);
             }
-            tmem_st32x16(tb + 16 * q2, y);
+            tmem_st32x16(tb + (kFine ? 32 : 16) * q2, y);
+            if constexpr (kFine) tmem_st32x16(tb + 32 * q2 + 16, y2);
           }
           float s0, s1;
           unpack_f32x2(sum, s0, s1);
@@ -791,7 +812,10 @@ masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         if (!ok) break;
         if (!begun) {
 #pragma unroll
-          for (int q2 = 0; q2 < 2; ++q2) tmem_st32x16(tb + 16 * q2, w[q2]);
+          for (int q2 = 0; q2 < 2; ++q2) {
+            tmem_st32x16(tb + (kFine ? 32 : 16) * q2, w[q2]);
+            if constexpr (kFine) tmem_st32x16(tb + 32 * q2 + 16, w2[q2]);
+          }
         }
         l += psum;
         tmem_wait_st();
@@ -1035,10 +1059,10 @@ Workspace workspace_of(const Problem& p, const Layout& L) {
   return w;
 }
 
-template <bool kCap, bool kBias>
+template <bool kCap, bool kBias, bool kFine>
 vsa_status launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mvc,
                   cudaStream_t stream) {
-  const auto kernel = masked_fwd_kernel<kCap, kBias>;
+  const auto kernel = masked_fwd_kernel<kCap, kBias, kFine>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: shared memory", e);
   kernel<<<a.n_blocks * a.units * a.p.B * a.splits, kThreads, sizeof(Smem), stream>>>(a, mk, mv, mvc);
@@ -1154,8 +1178,12 @@ vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms
   e = cudaGetLastError();                                 // nothing reads marks or lists that nobody wrote
   if (e != cudaSuccess) return cuda_fail("vsa_masked_attn_fwd: lists and scan", e);
   const bool cap = a.p.cap > 0.0f, bias = a.p.slopes != nullptr;
-  st = cap ? (bias ? launch<true, true>(a, mk, mv, mvc, stream) : launch<true, false>(a, mk, mv, mvc, stream))
-           : (bias ? launch<false, true>(a, mk, mv, mvc, stream) : launch<false, false>(a, mk, mv, mvc, stream));
+  const auto run = [&](auto fine) {
+    constexpr bool kFine = decltype(fine)::value;
+    return cap ? (bias ? launch<true, true, kFine>(a, mk, mv, mvc, stream) : launch<true, false, kFine>(a, mk, mv, mvc, stream))
+               : (bias ? launch<false, true, kFine>(a, mk, mv, mvc, stream) : launch<false, false, kFine>(a, mk, mv, mvc, stream));
+  };
+  st = L.rows <= kRows ? run(std::true_type{}) : run(std::false_type{});
   if (st != VSA_OK) return st;
   if (L.splits > 1) join_kernel<<<row_blocks, 256, 0, stream>>>(a);
   e = cudaGetLastError();

@@ -5,6 +5,13 @@
 // dS = P (dO V^T - D) (times 1 - tanh^2 under a cap), dV = P^T dO,
 // dK = scale dS^T Q, dQ = scale dS K.
 //
+// Roundings to bf16: P and dS as operands of the accumulating products (the tensor cores
+// take nothing wider at this rate; a sum of many terms is off by a relative 0.0016 from
+// it, like one rounding of the result), and `out`, which the caller kept and D is formed
+// from (dq and dk 0.0024 without, 0.0027 with it, more for rows of few keys; exact D would
+// take two more products per pair). The results are rounded once more. Sums, P, dS, D and
+// the statistics are 32-bit.
+//
 // Bound: tensor pipe. The formulas need five products per visible pair; the two
 // kinds of blocks here run seven (S and dO V^T once per side), so that every sum stays
 // in one block's TMEM in a fixed order: no atomics, equal inputs give equal bits,

@@ -718,3 +718,33 @@ def test_status_of_the_latest_calls(cuda_ok):
         assert attn.status() == vsa.ERR_TIMEOUT
         again()
         assert attn.status() == vsa.OK
+
+
+@pytest.mark.parametrize("case", [
+    (2, 1, 3001, 6, 2, True, None, 0.0, False, None),
+    (1, 1, 33, 2, 2, False, None, 0.0, False, None),
+    (1, 7, 900, 8, 2, True, None, 25.0, True, None),
+    (1, 64, 1500, 4, 2, True, (1200,), 0.0, True, None),
+    (2, 128, 700, 2, 2, False, None, 30.0, False, None),
+    (1, 100, 520, 4, 4, True, None, 0.0, False, (100, 1, 130, 200)),
+    (1, 3, 5000, 24, 1, False, None, 0.0, False, (3, 2000, 2997)),
+    (1, 128, 128, 1, 1, True, None, 0.0, True, None),
+], ids=ident)
+@pytest.mark.parametrize("size", [1.3, 8.0])
+def test_rows_of_one_tile_keep_two_terms_of_each_probability(cuda_ok, case, size):
+    """Queries that fit one tile of 128 rows: a probability enters the second product as two bf16 terms, whose sum is
+    within 2^-16 of it (each rounds by 2^-8, the second what the first left), so that in the bound of the output
+    2^-16 stands for 2^-8."""
+    import torch
+    B, Sq, Sk, Hq, Hk, causal, prefix, cap, bias, docs = case
+    q, k, v, _ = tensors(*case[:5], seed=71, size=size)
+    terms = terms_of(case)
+    out, lse = run(q, k, v, causal=causal, cap=cap, **terms)
+    ref = reference(case, q, k, v, terms)
+    within(lse, ref.lse, ref.t_lse, "lse")
+    see = visible(B, Sq, Sk, causal, terms.get("prefix"), terms.get("doc_q"), terms.get("doc_k"))
+    size_of = reference(case, q, k, v.abs(), terms).out                  # sum p |v|
+    was = (ref.t_out - E * ref.out.abs()) / (1 + E)                      # the bound before the output's rounding
+    now = was - (E - 2.0 ** -16) * size_of
+    assert see.any() and (now >= 0).all()
+    within(out, ref.out, now + E * (ref.out.abs() + now), "out")
