@@ -100,9 +100,12 @@ float effective_scale(const vsa_params* p);
 vsa_status check_qkv(const void* q, const void* k, const void* v, int64_t sb, int64_t ss,
                      int64_t sh, int32_t B, int32_t H);
 
+// SMs of the current device (148 where it cannot be asked).
+int device_sms();
+
 // A view of `heads` heads and rows of `width` elements: data, type and strides
 // (of dimensions of size above 1) valid, `align` bytes aligned rows. With
-// `output` no dimension of size above 1 may have stride 0.
+// `output` the strides of dimensions of size above 1 are at least `width`.
 vsa_status check_view(const vsa_view* v, int32_t B, int64_t S, int64_t width, int align, bool output);
 inline size_t dtype_bytes(int32_t dtype) { return dtype == VSA_F32 ? 4 : 2; }
 // Strides of dimensions of size 1 replaced by 0.

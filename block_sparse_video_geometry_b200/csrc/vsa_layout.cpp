@@ -77,6 +77,13 @@ vsa_status check_qkv(const void* q, const void* k, const void* v, int64_t sb, in
   return VSA_OK;
 }
 
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  return n;
+}
+
 vsa_status check_view(const vsa_view* v, int32_t B, int64_t S, int64_t width, int align, bool output) {
   if (!v || v->heads <= 0 || v->dtype < VSA_F32 || v->dtype > VSA_F16) return VSA_ERR_INVALID_ARG;
   if (B == 0 || S == 0) return VSA_OK;

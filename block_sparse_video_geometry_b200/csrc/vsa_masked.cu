@@ -14,15 +14,16 @@
 //
 // Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks the
 // key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
-// 32 KB stages; one warp issues the products, the two tiles in turn; two groups of
-// four warps run the softmax, a thread per row. Scores come in two buffers of 64
+// 32 KB stages; two warps issue the products, one for each slot; two groups of
+// four warps, one for each slot too, run the softmax, a thread per row. Scores come in two buffers of 64
 // keys per query tile; P (bf16, the A operand of O += P V) overwrites its scores
 // in TMEM, and the next scores follow behind that product. The softmax's reference
 // is raised, and O rescaled in TMEM, only when a row's sum of P in a tile passes 2^32.
 // Few rows: blocks of 128 rows, whose two slots take the key tiles in turn with the
 // same queries and join their results in shared memory. Few queries (a new token
 // over a cache): the heads that share a key head are packed into one tile, and the
-// key axis is split over blocks; a second kernel joins the parts.
+// key axis is split over blocks; a second kernel joins the parts. Up to 128 queries keep
+// two bf16 terms of each P (see masked_fwd_kernel).
 // Tiles that no row of the block sees are skipped: by arithmetic for causal
 // masks, by a list that plan_kernel makes from the tiles' document ranges.
 // Every wait is bounded (see vsa_masked_attn_status).
@@ -42,13 +43,6 @@ namespace masked {
 using namespace sm100;
 
 // ------------------------------------------------------------------- host
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
-  return n;
-}
-
 namespace {
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -995,7 +989,7 @@ Layout layout_of(const Problem& p) {
   best.packed = p.group > 1 && static_cast<int64_t>(p.group) * p.Sq <= kRows;
   best.units = best.packed ? p.Hk : p.Hq;
   best.rows = best.packed ? p.group * p.Sq : p.Sq;
-  const double sms = sm_count(), pairs = static_cast<double>(best.units) * p.B;
+  const double sms = device_sms(), pairs = static_cast<double>(best.units) * p.B;
   double least = 1e300;
   for (int one = best.rows <= kRows ? 1 : 0; one < 2; ++one) {
     const int per = one ? kRows : 2 * kRows, n_blocks = (best.rows + per - 1) / per;

@@ -115,7 +115,5 @@ void plan(const Problem& p, PlanRows rows, int n_blocks, int4* range, int32_t* c
 // plan(); count [B][nkt], list [B][nkt][nqt] out.
 void plan_keys(const Problem& p, const int4* range, int4* range_q, int32_t* count, int32_t* list, cudaStream_t stream);
 
-int sm_count();
-
 }  // namespace masked
 }  // namespace vsa

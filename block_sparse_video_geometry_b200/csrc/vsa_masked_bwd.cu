@@ -24,9 +24,11 @@
 //    S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and
 //    dS^T (bf16) as A operands in TMEM over their own 32-bit columns. Two warps
 //    issue products, one S^T and dV, one dP^T and dK; each rewrites its columns
-//    behind its own accumulation, in issue order. Eight warps (two per lane
-//    quadrant, 64 query columns each) turn S^T into P^T while dP^T and dK run, and
-//    dP^T into dS^T while dV and the next S^T run.
+//    behind its own accumulation, in issue order. The two halves of a tile's query
+//    columns are pipelines of their own, with barriers of their own. Sixteen warps
+//    (four per lane quadrant, 32 query columns each, so two per quadrant and half)
+//    turn S^T into P^T while dP^T and dK run, and dP^T into dS^T while dV and the
+//    next S^T run.
 //  * dq_block: a block owns 128 queries of a head (lane = query) and walks the
 //    key tiles: S = Q K^T, dP = dO V^T, dQ += dS K, dS in two buffers of its own.
 // Both read their tiles by TMA, three stages of the tensor that is used from the
@@ -812,7 +814,7 @@ void zero(const vsa_view* v, int32_t B, int32_t S, cudaStream_t stream) {
 // on 1: three 133, one 285, four 137; 4,000 x 2 heads, no mask: one 90, two 110.
 int splits_of(const Problem& p) {
   constexpr double kDq = 2.0 / 3.0;
-  const double pairs = static_cast<double>(p.B) * p.Hk, sms = sm_count();
+  const double pairs = static_cast<double>(p.B) * p.Hk, sms = device_sms();
   const int nqt = tiles(p.Sq);
   double total = 0.0, longest = 0.0;
   for (int kt = 0; kt < p.nkt; ++kt) {

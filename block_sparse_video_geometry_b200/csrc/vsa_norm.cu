@@ -7,12 +7,14 @@
 // from values held in registers (a one-pass E[x^2] - m^2 loses the rows whose
 // mean is far from zero).
 //
-// Bound: HBM (forward: x read, y written; backward: x, dy read, dx written). A
-// row is read once into registers, by a group of lanes of one warp when it is
-// short and by one block when it is long. Backward: every thread owns fixed
-// columns and sums dw and db of the rows its block passes in registers; blocks
-// leave one partial row each, which a second kernel adds in a fixed order (no
-// atomics: equal inputs give equal bits). Measured: 17,408 x 24 rows of 128 45 us (73%
+// Bound: HBM (forward: x read, y written; backward: x, dy read, dx written). Every row
+// is read from memory once: a short one into registers, by a group of lanes of one
+// warp, the next rows' loads ahead of the current ones' arithmetic; a long one by one
+// persistent block through a ring of rows in shared memory, from where the forward pass
+// takes it into registers and the backward pass reads it twice (the sums, then dx).
+// Backward: every thread owns fixed columns and sums dw and db of the rows its block
+// passes in registers; blocks leave one partial row each, which a second kernel adds in
+// a fixed order (no atomics: equal inputs give equal bits). Measured: 17,408 x 24 rows of 128 45 us (73%
 // of the copy rate); 17,408 rows of 5,120 forward 77 us (71%), backward 119 us (69%) and
 // 8 us for the sums.
 
@@ -713,13 +715,6 @@ Shape shape_of(int width, int vec, int64_t rows, int u) {
   return Shape{vec, 64, ept, ((nv + e - 1) / e + 31) / 32 * 32, 1};
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
-  return n;
-}
-
 constexpr int kMaxSms = 160;                        // the workspace is sized for this many
 // Persistent blocks: as many per SM as make about `threads` threads, at most 8.
 int persistent(int64_t rows, const Shape& s, int threads, int sms) {
@@ -744,7 +739,7 @@ template <class T, int VEC>
 vsa_status fwd_launch(const Shape& s, const FwdArgs& a, cudaStream_t stream) {
   const char* where = "vsa_layer_norm_fwd";
   const bool wide = s.ept == VEC;                          // of the warp kernels: one vector per lane
-  const int n = persistent(a.R.n, s, s.lanes > 32 ? 960 : (wide ? kFwdBlocks : 2) * kWarpBlock, sm_count());
+  const int n = persistent(a.R.n, s, s.lanes > 32 ? 960 : (wide ? kFwdBlocks : 2) * kWarpBlock, device_sms());
   if (s.lanes == 16) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 16, kFwdU>, n, s.threads, 0, a, stream);
   if (s.lanes == 32 && wide) return start(where, norm_fwd_warp_kernel<T, VEC, 1, 32, kFwdU>, n, s.threads, 0, a, stream);
   if constexpr (VEC == 1) {
@@ -930,7 +925,7 @@ vsa_status vsa_layer_norm_bwd(int32_t B, int64_t S, int32_t width, const vsa_vie
   const int vec = 16 / static_cast<int>(dtype_bytes(x->dtype));
   const bool wide = vec_ok(x, a.sx, vec, width) && vec_ok(dy, a.sdy, vec, width) && vec_ok(dx, a.sdx, vec, width);
   const Shape s = shape_of(width, wide ? vec : 1, a.R.n, 1);
-  const int n = bwd_blocks(a.R.n, s, sm_count());           // at most those that the workspace was sized for
+  const int n = bwd_blocks(a.R.n, s, device_sms());           // at most those that the workspace was sized for
   const bool g32 = dy->dtype == VSA_F32;
   if (x->dtype == VSA_F32)
     st = wide ? bwd_launch<float, float, 4>(s, a, n, stream) : bwd_launch<float, float, 1>(s, a, n, stream);

@@ -487,8 +487,8 @@ typedef enum { VSA_F32 = 0, VSA_BF16 = 1, VSA_F16 = 2 } vsa_dtype;
 
 /* A [B, S, heads, width] tensor at element strides, the last dimension
  * contiguous. The stride of a dimension of size 1 is not read. Inputs may be
- * broadcast (stride 0); an output's strides must be non-zero where its size is
- * above 1. */
+ * broadcast (stride 0); an output's strides are at least `width` where its size
+ * is above 1, and no two of its rows overlap. */
 typedef struct {
   void* data;
   int64_t stride_b, stride_s, stride_h;
@@ -622,9 +622,11 @@ vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32
 
 /* vsa_masked_attn_fwd: exact attention of q [B, Sq, Hq, 128] over k, v
  * [B, Sk, Hk, 128], query head h reading key head h / (Hq / Hk): the dense call
- * for the cases that the sparse call refuses, for packed clips (documents), for
- * padding and for causal video behind a bidirectional prefix; one query over a
- * long cache splits the key axis over the GPU.
+ * for the sequences that the sparse call refuses (without a video segment, or with
+ * several), for packed clips (documents), for padding and for causal video behind
+ * a bidirectional prefix; one query over a long cache splits the key axis over the
+ * GPU. Like the sparse call it takes a head dim of 128 alone; its output and
+ * gradients are bf16.
  *  q, k, v, out : bf16; data and strides 16-byte multiples; Hq a multiple of
  *                 Hk. Batch and head dimensions of inputs may be broadcast.
  *  lse          : float [B, Hq, Sq] out, contiguous: natural log of the sum of
@@ -635,9 +637,11 @@ vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32
  *                 vsa_masked_attn_status), the visible tiles, partial results;
  *                 written before it is read. Two calls that may overlap need
  *                 two workspaces.
- * No output may overlap an input or another output. Masked keys do not reach a row whatever they hold: infinities and NaN in
- * their k and v change nothing. A row that sees a key with an infinity or NaN
- * in its v is NaN throughout when the call masks anything.
+ * No output may overlap an input or another output. Masked keys do not reach a
+ * row whatever they hold: large numbers, infinities and NaN in their k and v
+ * change nothing. A row that sees a key with an infinity or NaN in its v is NaN
+ * throughout when the call masks anything, and else, for up to 128 queries, NaN
+ * in that channel.
  * Scores, softmax statistics and sums are 32-bit; the probabilities enter the
  * second tensor-core product as bf16 (the output's own rounding), for up to 128
  * queries as two bf16 terms (2^-16). B, Sq, Sk >= 0; at most 65535 batch entries
@@ -659,11 +663,12 @@ vsa_status vsa_masked_attn_bwd_workspace_size(const vsa_mask* mask, int32_t B, i
  *               nothing, or that nothing sees, gets 0. The slopes get no
  *               gradient.
  *  workspace  : vsa_masked_attn_bwd_workspace_size bytes, 256-byte aligned.
- * No output may overlap an input or another output. With P = exp(s - lse) and D = sum(dout * out): dS = P (dout v - D), times
- * 1 - tanh^2 under a cap; dq = scale dS k, dk = scale dS^T q, dv = P^T dout. P and
- * dS enter the products as bf16, every sum is 32-bit and in a fixed order: equal
- * inputs give equal bits. Masked rows that hold infinities or NaN change
- * nothing, as in the forward pass. */
+ * No output may overlap an input or another output. With P = exp(s - lse) and
+ * D = sum(dout * out) (of the bf16 out): dS = P (dout v - D), times 1 - tanh^2
+ * under a cap; dq = scale dS k, dk = scale dS^T q, dv = P^T dout. P and dS enter
+ * the products as bf16, every sum is 32-bit and in a fixed order: equal inputs
+ * give equal bits. Masked rows change nothing whatever they hold, as in the
+ * forward pass. */
 vsa_status vsa_masked_attn_bwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
                                const vsa_view* q, const vsa_view* k, const vsa_view* v, const vsa_view* out,
                                const float* lse, const vsa_view* dout, const vsa_view* dq, const vsa_view* dk,

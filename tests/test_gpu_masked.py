@@ -748,3 +748,19 @@ def test_rows_of_one_tile_keep_two_terms_of_each_probability(cuda_ok, case, size
     now = was - (E - 2.0 ** -16) * size_of
     assert see.any() and (now >= 0).all()
     within(out, ref.out, now + E * (ref.out.abs() + now), "out")
+
+
+@pytest.mark.parametrize("Sq", [1, 128, 129])
+def test_visible_infinities_without_a_mask(cuda_ok, Sq):
+    """An infinity in a visible v reaches its own channel only, of every query that sees it: the infinity, or for up to
+    128 queries (whose two terms of a probability take it with both signs) NaN."""
+    import torch
+    q, k, v, _ = tensors(1, Sq, 300, 2, 1, seed=73)
+    want, lse = run(q, k, v)
+    v[0, 250, 0, 3] = float("inf")
+    got, lse2 = run(q, k, v)
+    rest = torch.arange(128, device="cuda") != 3
+    assert torch.equal(got[..., rest], want[..., rest]) and torch.equal(lse, lse2)
+    assert not torch.isfinite(got[..., 3]).any()
+    if Sq > 128:
+        assert (got[..., 3] == float("inf")).all()
