@@ -316,7 +316,7 @@ struct Args {
 __device__ __forceinline__ bool bounded_wait(Smem& sm, uint64_t& bar, uint32_t parity, int* err) {
   bool ok = mbar_wait(smem_u32(&bar), parity, &sm.abort, kTimeoutNs);
   if (!ok) {
-    atomicExch(err, VSA_ERR_TIMEOUT);
+    *reinterpret_cast<volatile int*>(err) = VSA_ERR_TIMEOUT;
     *reinterpret_cast<volatile int*>(&sm.abort) = 1;
   }
   return ok;

@@ -673,8 +673,8 @@ def _empty(shape, dtype, device, handle):
 
 class MaskedAttention:
     """Dense attention of one shape and mask with its workspaces (allocated by the first call that needs them, so
-    run one call before a capture). Calls of one object share them: for calls on two streams, or graphs that may run
-    at once, make one object each. Outputs that a call allocates are written on its `stream`: a caller that reads them
+    run one call before a capture, and keep the object while its graph is replayed). Calls of one object share them:
+    for calls on two streams, or graphs that may run at once, make one object each. Outputs that a call allocates are written on its `stream`: a caller that reads them
     on another one waits for it, as for any torch operation on a side stream."""
 
     def __init__(self, mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int, device="cuda"):
@@ -731,8 +731,9 @@ class MaskedAttention:
         return dq, dk, dv
 
     def status(self, stream=None) -> int:
-        """Synchronises the stream; OK, or ERR_TIMEOUT where a bounded wait ran out and left the outputs of the latest
-        forward or backward call (with documents or without, each for itself) incomplete."""
+        """Synchronises the stream (the one that the calls ran on); OK, or ERR_TIMEOUT where a bounded wait ran out and
+        left the outputs of the latest forward or backward call (with documents or without, each for itself)
+        incomplete."""
         for ws in (*self.ws_fwd.values(), *self.ws_bwd.values()):
             status = masked_attn_status(ws, stream)
             if status != OK:
