@@ -9,7 +9,7 @@
 // per pair; a cap and a bias cost seven more FMA operations); one query over a long
 // cache: HBM (k and v read once). Measured: 8192 x 8192, 24 heads 820 us (1010
 // TFLOP/s; 938 us back to back under the power cap), one query over 4 x 33,001 keys
-// 102 us (81% of the copy rate), 2 x 1,111 queries over 5,003 keys with cap and bias
+// 99-101 us (82% of the copy rate), 2 x 1,111 queries over 5,003 keys with cap and bias
 // 205 us.
 //
 // Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks the
