@@ -337,8 +337,8 @@ __device__ __forceinline__ uint32_t second_term(uint32_t first, float p0, float 
 // (2^-16 of it together), so that the output is off by its own rounding only. One term
 // makes a long sum's relative error 0.0023-0.0026 instead of 0.0017. Taken for up to 128
 // queries, whose blocks wait for HBM: one query over 4 x 33,001 keys 95.7 us with one
-// term, 98.6 with two; 128 queries over 8,000 keys, 4 x 48 heads 181 and 189. Longer calls
-// would pay 2 to 22% (8192 x 24 heads 830 -> 1014 us).
+// term, 98.6 with two (with cap and bias 120 and 132); 128 queries over 8,000 keys, 4 x 48
+// heads 181 and 189. Longer calls would pay 2 to 22% (8192 x 24 heads 830 -> 1014 us).
 template <bool kCap, bool kBias, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
