@@ -12,18 +12,18 @@
 // 99-101 us (82% of the copy rate), 2 x 1,111 queries over 5,003 keys with cap and bias
 // 205 us.
 //
-// Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks the
-// key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five
-// 32 KB stages; two warps issue the products, one for each slot; two groups of
-// four warps, one for each slot too, run the softmax, a thread per row. Scores come in two buffers of 64
-// keys per query tile; P (bf16, the A operand of O += P V) overwrites its scores
-// in TMEM, and the next scores follow behind that product. The softmax's reference
-// is raised, and O rescaled in TMEM, only when a row's sum of P in a tile passes 2^32.
-// Few rows: blocks of 128 rows, whose two slots take the key tiles in turn with the
-// same queries and join their results in shared memory. Few queries (a new token
-// over a cache): the heads that share a key head are packed into one tile, and the
-// key axis is split over blocks; a second kernel joins the parts. Up to 128 queries keep
-// two bf16 terms of each P (see masked_fwd_kernel).
+// Design. A block owns 256 rows of one head as two M = 128 tiles (slots) and walks
+// the key tiles of 128. One warp copies K and V tiles (TMA) into a ring of five 32 KB
+// stages; two warps issue the products, one for each slot; two groups of four warps,
+// one for each slot too, run the softmax, a thread per row. Scores come in two
+// buffers of 64 keys per query tile; P (bf16, the A operand of O += P V) overwrites
+// its scores in TMEM, and the next scores follow behind that product. The softmax's
+// reference is raised, and O rescaled in TMEM, only when a row's sum of P in a tile
+// passes 2^32. Few rows: blocks of 128 rows, whose two slots take the key tiles in
+// turn with the same queries and join their results in shared memory. Few queries (a
+// new token over a cache): the heads that share a key head are packed into one tile,
+// and the key axis is split over blocks; a second kernel joins the parts. Up to 128
+// queries keep two bf16 terms of each P (see masked_fwd_kernel).
 // Tiles that no row of the block sees are skipped: by arithmetic for causal
 // masks, by a list that plan_kernel makes from the tiles' document ranges.
 // Every wait is bounded (see vsa_masked_attn_status).

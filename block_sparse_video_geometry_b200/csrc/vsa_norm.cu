@@ -7,16 +7,17 @@
 // from values held in registers (a one-pass E[x^2] - m^2 loses the rows whose
 // mean is far from zero).
 //
-// Bound: HBM (forward: x read, y written; backward: x, dy read, dx written). Every row
-// is read from memory once: a short one into registers, by a group of lanes of one
-// warp, the next rows' loads ahead of the current ones' arithmetic; a long one by one
-// persistent block through a ring of rows in shared memory, from where the forward pass
-// takes it into registers and the backward pass reads it twice (the sums, then dx).
-// Backward: every thread owns fixed columns and sums dw and db of the rows its block
-// passes in registers; blocks leave one partial row each, which a second kernel adds in
-// a fixed order (no atomics: equal inputs give equal bits). Measured: 17,408 x 24 rows of 128 45 us (73%
-// of the copy rate), backward 88 us and 11 us for the sums (49% together); 17,408 rows of
-// 5,120 forward 77 us (71%), backward 119 us (69%) and 8 us for the sums.
+// Bound: HBM (forward: x read, y written; backward: x, dy read, dx written). Every
+// row is read from memory once: a short one into registers, by a group of lanes of
+// one warp, the next rows' loads ahead of the current ones' arithmetic; a long one by
+// one persistent block through a ring of rows in shared memory, from where the
+// forward pass takes it into registers and the backward pass reads it twice (the
+// sums, then dx). Backward: every thread owns fixed columns and sums dw and db of the
+// rows its block passes in registers; blocks leave one partial row each, which a
+// second kernel adds in a fixed order (no atomics: equal inputs give equal bits).
+// Measured: 17,408 x 24 rows of 128 45 us (73% of the copy rate), backward 88 us and
+// 11 us for the sums (49% together); 17,408 rows of 5,120 forward 77 us (71%),
+// backward 119 us (69%) and 8 us for the sums.
 
 #include <algorithm>
 #include <cmath>

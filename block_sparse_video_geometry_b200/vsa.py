@@ -674,8 +674,9 @@ def _empty(shape, dtype, device, handle):
 class MaskedAttention:
     """Dense attention of one shape and mask with its workspaces (allocated by the first call that needs them, so
     run one call before a capture, and keep the object while its graph is replayed). Calls of one object share them:
-    for calls on two streams, or graphs that may run at once, make one object each. Outputs that a call allocates are written on its `stream`: a caller that reads them
-    on another one waits for it, as for any torch operation on a side stream."""
+    for calls on two streams, or graphs that may run at once, make one object each. Outputs that a call allocates are
+    written on its `stream`: a caller that reads them on another one waits for it, as for any torch operation on a side
+    stream. A stream that is given as a handle outlives the object and the outputs."""
 
     def __init__(self, mask: Mask, B: int, Sq: int, Sk: int, Hq: int, Hk: int, device="cuda"):
         import torch

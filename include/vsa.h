@@ -644,7 +644,8 @@ vsa_status vsa_masked_attn_workspace_size(const vsa_mask* mask, int32_t B, int32
  * in that channel.
  * Scores, softmax statistics and sums are 32-bit; the probabilities enter the
  * second tensor-core product as bf16 (the output's own rounding), for up to 128
- * queries as two bf16 terms (2^-16). B, Sq, Sk >= 0; at most 65535 batch entries
+ * queries as two bf16 terms (2^-16). The sums stand undivided until the end: a
+ * |v| above 2^64 may overflow them. B, Sq, Sk >= 0; at most 65535 batch entries
  * and heads, and 2^24 positions (UNSUPPORTED beyond, and for an input whose
  * sequence stride is 0). */
 vsa_status vsa_masked_attn_fwd(const vsa_mask* mask, const vsa_mask_terms* terms, int32_t B, int32_t Sq, int32_t Sk,
